@@ -4,6 +4,8 @@
 
 #include <cmath>
 #include <cstdint>
+#include <initializer_list>
+#include <limits>
 #include <mutex>
 
 #include "../../include/kda.h"
@@ -11,7 +13,7 @@
 
 namespace {
 
-constexpr int kVersion = 220;  // 0.2.2
+constexpr int kVersion = 300;  // 0.3.0
 
 bool valid_dtype(int dt) { return dt == KDA_F32 || dt == KDA_BF16; }
 int64_t esize(int dt) { return dt == KDA_F32 ? 4 : 2; }
@@ -332,6 +334,204 @@ int kda_decode_commit(const void* q, const void* k, const void* v, const void* b
     }
     return from_hip(kda::launch_decode_commit(q, k, v, beta, in_dtype, g, g_dtype, state, accepted,
                                               N, K, H, dk, dv, static_cast<hipStream_t>(stream)));
+}
+
+// ---- linear attention with one decay per head ------------------------------------------------
+
+size_t kda_linear_chunk_workspace_size(int32_t n_seqs, int64_t total_tokens, int32_t H, int32_t dk,
+                                       int32_t dv, int in_dtype, int backward) {
+    if (n_seqs < 1 || total_tokens < 0 || H < 1 || !supported_d(dk) || !supported_d(dv) ||
+        !valid_dtype(in_dtype))
+        return 0;
+    return kda::linear_workspace_bytes(n_seqs, total_tokens, H, dk, dv, in_dtype, backward != 0);
+}
+
+}  // extern "C"
+
+namespace {
+
+bool aligned16(std::initializer_list<const void*> ps) {
+    for (const void* p : ps)
+        if (reinterpret_cast<uintptr_t>(p) % 16 != 0) return false;
+    return true;
+}
+bool aligned4(std::initializer_list<const void*> ps) {
+    for (const void* p : ps)
+        if (reinterpret_cast<uintptr_t>(p) % 4 != 0) return false;
+    return true;
+}
+
+// No output overlaps an input or another output.
+bool disjoint(std::initializer_list<Range> outs, std::initializer_list<Range> ins) {
+    for (const Range* a = outs.begin(); a != outs.end(); ++a) {
+        for (const Range* b = a + 1; b != outs.end(); ++b)
+            if (overlap(*a, *b)) return false;
+        for (const Range& b : ins)
+            if (overlap(*a, b)) return false;
+    }
+    return true;
+}
+
+// Checks the forward and the backward share; KDA_OK, or the status to return.
+int linear_sizes(int in_dtype, const int32_t* cu, int32_t B, int64_t T, int32_t n_seqs, int32_t H,
+                 int32_t dk, int32_t dv, float scale) {
+    if (!valid_dtype(in_dtype)) return KDA_ERR_INVALID_ARGUMENT;
+    if (B < 1 || T < 0 || n_seqs < 1 || H < 1 || dk < 1 || dv < 1 || !std::isfinite(scale))
+        return KDA_ERR_INVALID_ARGUMENT;
+    if (cu ? (B != 1) : (n_seqs != B)) return KDA_ERR_INVALID_ARGUMENT;
+    if (!supported_d(dk) || !supported_d(dv)) return KDA_ERR_UNSUPPORTED;
+    // a grid of 256-lane workgroups (up to six per (sequence, head)) must stay within 2^32 lanes
+    if (int64_t(n_seqs) * H > (int64_t(1) << 21)) return KDA_ERR_UNSUPPORTED;
+    return KDA_OK;
+}
+
+// The debug check of g and cu_seqlens; KDA_OK with the check off.
+int linear_debug(const float* g, const int32_t* cu, int32_t n_seqs, int64_t ntok, int32_t H, void* stream) {
+    if (!kda::debug_validation_enabled() || ntok == 0) return KDA_OK;
+    bool ok = true;
+    if (kda::debug_validate(g, KDA_F32, H, cu, n_seqs, ntok, static_cast<hipStream_t>(stream), &ok,
+                            -std::numeric_limits<float>::infinity()) != hipSuccess)
+        return KDA_ERR_HIP;
+    return ok ? KDA_OK : KDA_ERR_INVALID_ARGUMENT;
+}
+
+int state_cache_check(const float* states, const int32_t* slots, const void* codes, int code,
+                      const float* scales, int32_t N, int32_t n_slots, int32_t H, int32_t dk, int32_t dv,
+                      int32_t group, bool store, kda::StateCacheArgs* a) {
+    if ((code != KDA_CODE_I8 && code != KDA_CODE_E4M3) || N < 0 || n_slots < 1 || H < 1 || dk < 1 || dv < 1 ||
+        group < 1)
+        return KDA_ERR_INVALID_ARGUMENT;
+    if (!supported_d(dk) || !supported_d(dv) || (group != 32 && group != 64 && group != 128) || group > dv)
+        return KDA_ERR_UNSUPPORTED;
+    if (!slots && N > n_slots) return KDA_ERR_INVALID_ARGUMENT;
+    if (N == 0) return KDA_OK;
+    if (!states || !codes || !scales) return KDA_ERR_INVALID_ARGUMENT;
+    if (!aligned16({states, codes}) || !aligned4({scales, slots})) return KDA_ERR_UNSUPPORTED;
+    const int64_t per_seq = int64_t(H) * dk * dv;
+    // a grid of 256-lane workgroups must stay within 2^32 lanes (8192 elements a workgroup)
+    if ((per_seq + 8191) / 8192 * N > (int64_t(1) << 24) - 1) return KDA_ERR_UNSUPPORTED;
+    const Range r_st = range(states, N * per_seq * 4), r_sl = range(slots, slots ? int64_t(N) * 4 : 0);
+    const Range r_c = range(codes, n_slots * per_seq), r_sc = range(scales, n_slots * (per_seq / group) * 4);
+    if (store ? !disjoint({r_c, r_sc}, {r_st, r_sl}) : !disjoint({r_st}, {r_c, r_sc, r_sl}))
+        return KDA_ERR_INVALID_ARGUMENT;
+    a->codes = const_cast<void*>(codes); a->scales = const_cast<float*>(scales); a->slots = slots;
+    a->code = code; a->N = N; a->n_slots = n_slots; a->H = H; a->dk = dk; a->dv = dv; a->group = group;
+    return KDA_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int kda_linear_chunk_fwd(const void* q, const void* k, const void* v, int in_dtype, const float* g,
+                         const float* initial_state, float* final_state, const int32_t* cu_seqlens,
+                         void* o, int o_dtype, int32_t B, int64_t T, int32_t n_seqs, int32_t H,
+                         int32_t dk, int32_t dv, float scale, void* workspace,
+                         size_t workspace_bytes, void* stream) {
+    if (!valid_dtype(o_dtype)) return KDA_ERR_INVALID_ARGUMENT;
+    const int st = linear_sizes(in_dtype, cu_seqlens, B, T, n_seqs, H, dk, dv, scale);
+    if (st != KDA_OK) return st;
+    const int64_t ntok = int64_t(B) * T, rows = ntok * H;
+    if (ntok > 0 && (!q || !k || !v || !g || !o)) return KDA_ERR_INVALID_ARGUMENT;
+    if (!aligned16({q, k, v, o, initial_state, final_state, workspace}) || !aligned4({g, cu_seqlens}))
+        return KDA_ERR_UNSUPPORTED;
+    const size_t need = kda::linear_workspace_bytes(n_seqs, ntok, H, dk, dv, in_dtype, false);
+    if (workspace_bytes < need || (need > 0 && !workspace)) return KDA_ERR_WORKSPACE;
+    const int64_t es = esize(in_dtype), state_bytes = int64_t(n_seqs) * H * dk * dv * 4;
+    const Range r_h0 = range(initial_state, initial_state ? state_bytes : 0);
+    const Range r_hT = range(final_state, final_state ? state_bytes : 0);
+    const Range r_q = range(q, rows * dk * es), r_k = range(k, rows * dk * es), r_v = range(v, rows * dv * es);
+    const Range r_g = range(g, ntok > 0 ? int64_t(H) * 4 : 0), r_o = range(o, rows * dv * esize(o_dtype));
+    const Range r_cu = range(cu_seqlens, cu_seqlens ? int64_t(n_seqs + 1) * 4 : 0);
+    const Range r_ws = range(workspace, workspace ? int64_t(workspace_bytes) : 0);
+    if (!disjoint({r_o, r_hT, r_ws}, {r_q, r_k, r_v, r_g, r_cu}) || overlap(r_o, r_h0) || overlap(r_ws, r_h0))
+        return KDA_ERR_INVALID_ARGUMENT;
+    // the final state may be the initial state itself, but must not partly overlap it
+    if (initial_state != final_state && overlap(r_h0, r_hT)) return KDA_ERR_INVALID_ARGUMENT;
+    const int dbg = linear_debug(g, cu_seqlens, n_seqs, ntok, H, stream);
+    if (dbg != KDA_OK) return dbg;
+    kda::LinearArgs a{};
+    a.q = q; a.k = k; a.v = v; a.g = g; a.h0 = initial_state; a.hT = final_state; a.cu = cu_seqlens; a.o = o;
+    a.in_dtype = in_dtype; a.o_dtype = o_dtype; a.B = B; a.T = T; a.n_seqs = n_seqs; a.H = H; a.dk = dk;
+    a.dv = dv; a.scale = scale; a.workspace = workspace;
+    return from_hip(kda::launch_linear_fwd(a, static_cast<hipStream_t>(stream)));
+}
+
+int kda_linear_chunk_bwd(const void* q, const void* k, const void* v, int in_dtype, const float* g,
+                         const float* initial_state, const int32_t* cu_seqlens, const void* d_o,
+                         const float* d_final_state, void* dq, void* dk_out, void* dv_out,
+                         float* d_initial_state, int32_t B, int64_t T, int32_t n_seqs, int32_t H,
+                         int32_t dk, int32_t dv, float scale, void* workspace,
+                         size_t workspace_bytes, void* stream) {
+    const int st = linear_sizes(in_dtype, cu_seqlens, B, T, n_seqs, H, dk, dv, scale);
+    if (st != KDA_OK) return st;
+    const int64_t ntok = int64_t(B) * T, rows = ntok * H;
+    if (ntok > 0 && (!q || !k || !v || !g || !d_o || !dq || !dk_out || !dv_out)) return KDA_ERR_INVALID_ARGUMENT;
+    if (!aligned16({q, k, v, d_o, dq, dk_out, dv_out, initial_state, d_final_state, d_initial_state, workspace}) ||
+        !aligned4({g, cu_seqlens}))
+        return KDA_ERR_UNSUPPORTED;
+    const size_t need = kda::linear_workspace_bytes(n_seqs, ntok, H, dk, dv, in_dtype, true);
+    if (workspace_bytes < need || (need > 0 && !workspace)) return KDA_ERR_WORKSPACE;
+    const int64_t es = esize(in_dtype), state_bytes = int64_t(n_seqs) * H * dk * dv * 4;
+    const int64_t kb = rows * dk * es, vb = rows * dv * es;
+    if (!disjoint({range(dq, kb), range(dk_out, kb), range(dv_out, vb),
+                   range(d_initial_state, d_initial_state ? state_bytes : 0),
+                   range(workspace, workspace ? int64_t(workspace_bytes) : 0)},
+                  {range(q, kb), range(k, kb), range(v, vb), range(d_o, vb), range(g, ntok > 0 ? int64_t(H) * 4 : 0),
+                   range(initial_state, initial_state ? state_bytes : 0),
+                   range(d_final_state, d_final_state ? state_bytes : 0),
+                   range(cu_seqlens, cu_seqlens ? int64_t(n_seqs + 1) * 4 : 0)}))
+        return KDA_ERR_INVALID_ARGUMENT;
+    const int dbg = linear_debug(g, cu_seqlens, n_seqs, ntok, H, stream);
+    if (dbg != KDA_OK) return dbg;
+    kda::LinearArgs a{};
+    a.q = q; a.k = k; a.v = v; a.d_o = d_o; a.g = g; a.h0 = initial_state; a.dhT = d_final_state;
+    a.dh0 = d_initial_state; a.cu = cu_seqlens; a.dq = dq; a.dkk = dk_out; a.dvv = dv_out;
+    a.in_dtype = in_dtype; a.o_dtype = in_dtype; a.B = B; a.T = T; a.n_seqs = n_seqs; a.H = H; a.dk = dk;
+    a.dv = dv; a.scale = scale; a.workspace = workspace;
+    return from_hip(kda::launch_linear_bwd(a, static_cast<hipStream_t>(stream)));
+}
+
+int kda_linear_decode_step(const void* q, const void* k, const void* v, int in_dtype,
+                           const float* g, float* state, void* o, int o_dtype, int32_t N, int32_t H,
+                           int32_t dk, int32_t dv, float scale, void* stream) {
+    if (!valid_dtype(in_dtype) || !valid_dtype(o_dtype)) return KDA_ERR_INVALID_ARGUMENT;
+    if (N < 0 || H < 1 || dk < 1 || dv < 1 || !std::isfinite(scale)) return KDA_ERR_INVALID_ARGUMENT;
+    if (!supported_d(dk) || !supported_d(dv)) return KDA_ERR_UNSUPPORTED;
+    if (N == 0) return KDA_OK;
+    if (!q || !k || !v || !g || !state || !o) return KDA_ERR_INVALID_ARGUMENT;
+    if (!aligned16({q, k, v, state, o}) || !aligned4({g})) return KDA_ERR_UNSUPPORTED;
+    const int64_t units = int64_t(N) * H, es = esize(in_dtype);
+    // a grid of 256-lane workgroups must stay within 2^32 lanes
+    if (units > (int64_t(1) << 24) - 1) return KDA_ERR_UNSUPPORTED;
+    if (!disjoint({range(o, units * dv * esize(o_dtype)), range(state, units * dk * dv * 4)},
+                  {range(q, units * dk * es), range(k, units * dk * es), range(v, units * dv * es),
+                   range(g, int64_t(H) * 4)}))
+        return KDA_ERR_INVALID_ARGUMENT;
+    const int dbg = linear_debug(g, nullptr, 0, 1, H, stream);
+    if (dbg != KDA_OK) return dbg;
+    return from_hip(kda::launch_linear_decode(q, k, v, in_dtype, g, state, o, o_dtype, N, H, dk, dv, scale,
+                                              static_cast<hipStream_t>(stream)));
+}
+
+// ---- 8-bit state cache -----------------------------------------------------------------------
+
+int kda_state_store(const float* states, const int32_t* slots, void* codes, int code, float* scales,
+                    int32_t N, int32_t n_slots, int32_t H, int32_t dk, int32_t dv, int32_t group,
+                    void* stream) {
+    kda::StateCacheArgs a{};
+    const int st = state_cache_check(states, slots, codes, code, scales, N, n_slots, H, dk, dv, group, true, &a);
+    if (st != KDA_OK || N == 0) return st;
+    return from_hip(kda::launch_state_store(a, states, static_cast<hipStream_t>(stream)));
+}
+
+int kda_state_load(const void* codes, int code, const float* scales, const int32_t* slots,
+                   float* states, int32_t N, int32_t n_slots, int32_t H, int32_t dk, int32_t dv,
+                   int32_t group, void* stream) {
+    kda::StateCacheArgs a{};
+    const int st = state_cache_check(states, slots, codes, code, scales, N, n_slots, H, dk, dv, group, false, &a);
+    if (st != KDA_OK || N == 0) return st;
+    return from_hip(kda::launch_state_load(a, states, static_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -5,7 +5,8 @@
 // log-decay g lies in [-5, 0] -- the bound on the forget gate that keeps every 16-token block's
 // decay factors inside the floating range ([habr] "Как устроена Kimi K3: …", § "Последовательность:
 // три KDA на один глобальный MLA") -- and a packed batch's cu_seqlens start at 0, never decrease
-// and end at the token count.  With the check on, a call first runs small kernels that test them,
+// and end at the token count.  The linear-attention entry points do so with their own g <= 0 (no lower
+// bound) and cu_seqlens.  With the check on, a call first runs small kernels that test them,
 // waits for their result (a host synchronisation on the caller's stream) and reports a violation
 // as KDA_ERR_INVALID_ARGUMENT before any other work is enqueued.  The result lives in one word
 // of library-owned device memory; calls that overlap on one device share it.  Not for use under
@@ -23,12 +24,12 @@ __device__ unsigned int validate_word;   // bit 0: g out of range; bit 1: cu_seq
 __global__ void clear_word_kernel(unsigned int* w) { *w = 0u; }
 
 template <int DT>
-__global__ void __launch_bounds__(256) check_g_kernel(const void* g, int64_t n, unsigned int* w) {
+__global__ void __launch_bounds__(256) check_g_kernel(const void* g, int64_t n, float lo, unsigned int* w) {
     bool bad = false;
     for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < n;
          i += static_cast<int64_t>(gridDim.x) * 256) {
         const float x = load_as_f32<DT>(g, i);
-        bad |= !(x >= -5.0f && x <= 0.0f);     // NaN fails too
+        bad |= !(x >= lo && x <= 0.0f);     // NaN fails too
     }
     if (bad) atomicOr(w, 1u);
 }
@@ -47,7 +48,7 @@ bool debug_validation_enabled() {
 }
 
 hipError_t debug_validate(const void* g, int g_dtype, int64_t g_elems, const int32_t* cu,
-                          int32_t n_seqs, int64_t total, hipStream_t stream, bool* ok) {
+                          int32_t n_seqs, int64_t total, hipStream_t stream, bool* ok, float g_lo) {
     *ok = true;
     unsigned int* w = nullptr;
     hipError_t e = hipGetSymbolAddress(reinterpret_cast<void**>(&w), HIP_SYMBOL(validate_word));
@@ -57,9 +58,9 @@ hipError_t debug_validate(const void* g, int g_dtype, int64_t g_elems, const int
         const int64_t blocks = (g_elems + 255) / 256;
         const unsigned grid = static_cast<unsigned>(blocks < 4096 ? blocks : 4096);
         if (g_dtype == KDA_F32)
-            hipLaunchKernelGGL(check_g_kernel<KDA_F32>, dim3(grid), dim3(256), 0, stream, g, g_elems, w);
+            hipLaunchKernelGGL(check_g_kernel<KDA_F32>, dim3(grid), dim3(256), 0, stream, g, g_elems, g_lo, w);
         else
-            hipLaunchKernelGGL(check_g_kernel<KDA_BF16>, dim3(grid), dim3(256), 0, stream, g, g_elems, w);
+            hipLaunchKernelGGL(check_g_kernel<KDA_BF16>, dim3(grid), dim3(256), 0, stream, g, g_elems, g_lo, w);
     }
     if (cu != nullptr)
         hipLaunchKernelGGL(check_cu_kernel, dim3(1), dim3(256), 0, stream, cu, n_seqs, total, w);

@@ -72,6 +72,22 @@ def load_library(path: Optional[str] = None):
     lib.kda_decode_commit.argtypes = [vp, vp, vp, vp, ctypes.c_int, vp, ctypes.c_int, vp, vp,
                                       i32, i32, i32, i32, i32, vp]
     lib.kda_decode_commit.restype = ctypes.c_int
+    lib.kda_linear_chunk_workspace_size.argtypes = [i32, i64, i32, i32, i32, ctypes.c_int,
+                                                    ctypes.c_int]
+    lib.kda_linear_chunk_workspace_size.restype = sz
+    lib.kda_linear_chunk_fwd.argtypes = [vp, vp, vp, ctypes.c_int, vp, vp, vp, vp, vp, ctypes.c_int,
+                                         i32, i64, i32, i32, i32, i32, f32, vp, sz, vp]
+    lib.kda_linear_chunk_fwd.restype = ctypes.c_int
+    lib.kda_linear_chunk_bwd.argtypes = [vp, vp, vp, ctypes.c_int, vp, vp, vp, vp, vp, vp, vp, vp,
+                                         vp, i32, i64, i32, i32, i32, i32, f32, vp, sz, vp]
+    lib.kda_linear_chunk_bwd.restype = ctypes.c_int
+    lib.kda_linear_decode_step.argtypes = [vp, vp, vp, ctypes.c_int, vp, vp, vp, ctypes.c_int, i32,
+                                           i32, i32, i32, f32, vp]
+    lib.kda_linear_decode_step.restype = ctypes.c_int
+    lib.kda_state_store.argtypes = [vp, vp, vp, ctypes.c_int, vp, i32, i32, i32, i32, i32, i32, vp]
+    lib.kda_state_store.restype = ctypes.c_int
+    lib.kda_state_load.argtypes = [vp, ctypes.c_int, vp, vp, vp, i32, i32, i32, i32, i32, i32, vp]
+    lib.kda_state_load.restype = ctypes.c_int
     if path == lib_path():
         _lib = lib
     return lib
@@ -80,7 +96,8 @@ def load_library(path: Optional[str] = None):
 EXPORTED = ["kda_status_string", "kda_version", "kda_gate", "kda_chunk_fwd_workspace_size",
             "kda_chunk_fwd", "kda_chunk_fwd_gated", "kda_chunk_fwd_gated_noalloc",
             "kda_chunk_fwd_checkpointed", "kda_decode_step", "kda_decode_verify",
-            "kda_decode_commit"]
+            "kda_decode_commit", "kda_linear_chunk_workspace_size", "kda_linear_chunk_fwd",
+            "kda_linear_chunk_bwd", "kda_linear_decode_step", "kda_state_store", "kda_state_load"]
 
 # Size of the library's static prefill workspace used by kda_chunk_fwd_gated_noalloc.
 NOALLOC_SCRATCH_BYTES = 256 << 20
@@ -422,3 +439,222 @@ def kda_decode_commit(q, k, v, beta, g, state, accepted, stream=None):
         _ptr(q), _ptr(k), _ptr(v), _ptr(beta), _dt(q), _ptr(g), _dt(g), _ptr(state),
         _ptr(accepted), N, Kd, H, dk, dv, _sptr(ts)))
     return state
+
+
+# ---- linear attention with one decay per head ---------------------------------------------------
+
+def _launch(fn: str, dev: torch.device, stream, call):
+    """Run call(stream pointer) with `dev` current and check its status."""
+    sp = _sptr(_torch_stream(stream, dev))
+    if torch.cuda.current_device() == dev.index:
+        status = call(sp)
+    else:
+        with torch.cuda.device(dev):
+            status = call(sp)
+    _check(fn, status)
+
+
+def _alloc(ts, shape, dtype, dev):
+    """A new tensor on the launch stream `ts`."""
+    if ts == torch.cuda.current_stream(dev):
+        return torch.empty(shape, dtype=dtype, device=dev)
+    with torch.cuda.stream(ts):
+        return torch.empty(shape, dtype=dtype, device=dev)
+
+
+def kda_linear_chunk_workspace_size(n_seqs: int, total_tokens: int, H: int, dk: int, dv: int,
+                                    in_dtype: torch.dtype = torch.bfloat16,
+                                    backward: bool = False) -> int:
+    return int(load_library().kda_linear_chunk_workspace_size(n_seqs, total_tokens, H, dk, dv,
+                                                              _DT[in_dtype], int(backward)))
+
+
+def _check_linear(fn, q, k, v, g, cu_seqlens, workspace, states, like_q, like_v):
+    """Shapes, dtypes and devices of a linear-attention prefill or backward call.  `states`,
+    `like_q` and `like_v` map argument names to tensors shaped as a state, q or v.  Returns
+    (B, T, N, H, dk, dv, device)."""
+    if not isinstance(q, torch.Tensor) or q.dim() != 4:
+        raise ValueError(f"{fn}: q must be a [B, T, H, dk] tensor")
+    B, T, H, dk = q.shape
+    if not isinstance(v, torch.Tensor) or v.dim() != 4:
+        raise ValueError(f"{fn}: v must be a [B, T, H, dv] tensor")
+    dv = v.shape[-1]
+    _expect(fn, "q", q, (B, T, H, dk), _FLOATS)
+    _expect(fn, "k", k, (B, T, H, dk), _FLOATS)
+    _expect(fn, "v", v, (B, T, H, dv), _FLOATS)
+    _same_dtype(fn, q=q, k=k, v=v)
+    _expect(fn, "g", g, (H,), (torch.float32,))
+    N = B
+    if cu_seqlens is not None:
+        if B != 1:
+            raise ValueError(f"{fn}: cu_seqlens needs B == 1 (a packed batch)")
+        _expect(fn, "cu_seqlens", cu_seqlens, (None,), (torch.int32,))
+        N = cu_seqlens.numel() - 1
+        if N < 1:
+            raise ValueError(f"{fn}: cu_seqlens needs at least two offsets")
+    for name, t in states.items():
+        _expect(fn, name, t, (N, H, dk, dv), (torch.float32,))
+    for name, t in like_q.items():
+        _expect(fn, name, t, (B, T, H, dk), (q.dtype,))
+    for name, t in like_v.items():
+        _expect(fn, name, t, (B, T, H, dv), _FLOATS if name == "o" else (q.dtype,))
+    if workspace is not None and not workspace.is_contiguous():
+        raise ValueError(f"{fn}: workspace must be contiguous")
+    dev = _one_device(fn, q=q, k=k, v=v, g=g, cu_seqlens=cu_seqlens, workspace=workspace, **states,
+                      **like_q, **like_v)
+    return B, T, N, H, dk, dv, dev
+
+
+def _linear_workspace(ts, workspace, N, ntok, H, dk, dv, dtype, backward, dev):
+    """The workspace (allocated on `ts` where none is given and one is needed) and its bytes."""
+    if workspace is None:
+        need = kda_linear_chunk_workspace_size(N, ntok, H, dk, dv, dtype, backward)
+        if need == 0:
+            return None, 0
+        workspace = _alloc(ts, (need,), torch.uint8, dev)
+    return workspace, workspace.numel() * workspace.element_size()
+
+
+def kda_linear_chunk_fwd(q, k, v, g, initial_state=None, final_state=None, cu_seqlens=None, o=None,
+                         o_dtype=None, scale: float = 1.0, output_final_state: bool = True,
+                         workspace=None, stream=None):
+    """Chunked prefill of linear attention, S_t = e^g S_{t-1} + k_t v_t^T, o_t = scale S_t^T q_t:
+    q, k [B, T, H, dk]; v [B, T, H, dv]; g [H] fp32 log-decay (<= 0); initial_state
+    [N, H, dk, dv] fp32 or None; cu_seqlens device int32 [N+1] or None (B == 1).  Returns
+    (o, final_state); final_state is allocated when output_final_state and not given."""
+    fn = "kda_linear_chunk_fwd"
+    B, T, N, H, dk, dv, dev = _check_linear(
+        fn, q, k, v, g, cu_seqlens, workspace,
+        dict(initial_state=initial_state, final_state=final_state), {}, dict(o=o))
+    ts = _torch_stream(stream, dev)
+    if o is None:
+        o = _alloc(ts, (B, T, H, dv), o_dtype or q.dtype, dev)
+    if final_state is None and output_final_state:
+        final_state = _alloc(ts, (N, H, dk, dv), torch.float32, dev)
+    workspace, ws_bytes = _linear_workspace(ts, workspace, N, B * T, H, dk, dv, q.dtype, False, dev)
+    lib = load_library()
+    _launch(fn, dev, ts, lambda sp: lib.kda_linear_chunk_fwd(
+        _ptr(q), _ptr(k), _ptr(v), _dt(q), _ptr(g), _ptr(initial_state), _ptr(final_state),
+        _ptr(cu_seqlens), _ptr(o), _dt(o), B, T, N, H, dk, dv, float(scale), _ptr(workspace),
+        ws_bytes, sp))
+    return o, final_state
+
+
+def kda_linear_chunk_bwd(q, k, v, g, do, initial_state=None, d_final_state=None, cu_seqlens=None,
+                         dq=None, dk=None, dv=None, d_initial_state=None, scale: float = 1.0,
+                         output_d_initial_state: Optional[bool] = None, workspace=None,
+                         stream=None):
+    """Gradients of kda_linear_chunk_fwd: do [B, T, H, dv] in q's dtype, d_final_state
+    [N, H, dk, dv] fp32 or None (zeros), the other inputs as there.  Returns (dq, dk, dv,
+    d_initial_state); the last is allocated when output_d_initial_state (default: when
+    initial_state is given) and not given, else None."""
+    fn = "kda_linear_chunk_bwd"
+    if not isinstance(do, torch.Tensor):
+        raise TypeError(f"{fn}: do must be a torch.Tensor")
+    B, T, N, H, d_k, d_v, dev = _check_linear(
+        fn, q, k, v, g, cu_seqlens, workspace,
+        dict(initial_state=initial_state, d_final_state=d_final_state,
+             d_initial_state=d_initial_state), dict(dq=dq, dk=dk), dict(do=do, dv=dv))
+    ts = _torch_stream(stream, dev)
+    if dq is None:
+        dq = _alloc(ts, q.shape, q.dtype, dev)
+    if dk is None:
+        dk = _alloc(ts, q.shape, q.dtype, dev)
+    if dv is None:
+        dv = _alloc(ts, v.shape, q.dtype, dev)
+    if output_d_initial_state is None:
+        output_d_initial_state = initial_state is not None
+    if d_initial_state is None and output_d_initial_state:
+        d_initial_state = _alloc(ts, (N, H, d_k, d_v), torch.float32, dev)
+    workspace, ws_bytes = _linear_workspace(ts, workspace, N, B * T, H, d_k, d_v, q.dtype, True, dev)
+    lib = load_library()
+    _launch(fn, dev, ts, lambda sp: lib.kda_linear_chunk_bwd(
+        _ptr(q), _ptr(k), _ptr(v), _dt(q), _ptr(g), _ptr(initial_state), _ptr(cu_seqlens),
+        _ptr(do), _ptr(d_final_state), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(d_initial_state), B, T, N,
+        H, d_k, d_v, float(scale), _ptr(workspace), ws_bytes, sp))
+    return dq, dk, dv, d_initial_state
+
+
+def kda_linear_decode_step(q, k, v, g, state, o=None, o_dtype=None, scale: float = 1.0,
+                           stream=None):
+    """One token of linear attention per sequence: q, k [N, H, dk]; v [N, H, dv]; g [H] fp32;
+    state [N, H, dk, dv] fp32 updated in place.  Returns o [N, H, dv]."""
+    fn = "kda_linear_decode_step"
+    if not isinstance(q, torch.Tensor) or q.dim() != 3:
+        raise ValueError(f"{fn}: q must be a [N, H, dk] tensor")
+    if not isinstance(v, torch.Tensor) or v.dim() != 3:
+        raise ValueError(f"{fn}: v must be a [N, H, dv] tensor")
+    N, H, dk = q.shape
+    dv = v.shape[-1]
+    _expect(fn, "q", q, (N, H, dk), _FLOATS)
+    _expect(fn, "k", k, (N, H, dk), _FLOATS)
+    _expect(fn, "v", v, (N, H, dv), _FLOATS)
+    _same_dtype(fn, q=q, k=k, v=v)
+    _expect(fn, "g", g, (H,), (torch.float32,))
+    _expect(fn, "state", state, (N, H, dk, dv), (torch.float32,))
+    _expect(fn, "o", o, (N, H, dv), _FLOATS)
+    dev = _one_device(fn, q=q, k=k, v=v, g=g, state=state, o=o)
+    ts = _torch_stream(stream, dev)
+    if o is None:
+        o = _alloc(ts, (N, H, dv), o_dtype or q.dtype, dev)
+    lib = load_library()
+    _launch(fn, dev, ts, lambda sp: lib.kda_linear_decode_step(
+        _ptr(q), _ptr(k), _ptr(v), _dt(q), _ptr(g), _ptr(state), _ptr(o), _dt(o), N, H, dk, dv,
+        float(scale), sp))
+    return o
+
+
+# ---- 8-bit state cache --------------------------------------------------------------------------
+
+KDA_CODE_I8, KDA_CODE_E4M3 = 0, 1
+_CODES = {torch.int8: KDA_CODE_I8, torch.float8_e4m3fn: KDA_CODE_E4M3}
+
+
+def _check_cache(fn, codes, scales, slots, states):
+    """Shapes, dtypes and devices of a state-cache call; states may be None (to be allocated).
+    Returns (N, n_slots, H, dk, dv, group, device)."""
+    if not isinstance(codes, torch.Tensor) or codes.dim() != 4:
+        raise ValueError(f"{fn}: codes must be a [n_slots, H, dk, dv] tensor")
+    n_slots, H, dk, dv = codes.shape
+    _expect(fn, "codes", codes, (n_slots, H, dk, dv), tuple(_CODES))
+    if not isinstance(scales, torch.Tensor):
+        raise TypeError(f"{fn}: scales must be a torch.Tensor")
+    _expect(fn, "scales", scales, (n_slots, H, dk, None), (torch.float32,))
+    if scales.shape[-1] < 1 or dv % scales.shape[-1] != 0:
+        raise ValueError(f"{fn}: scales must end in dv / group, got {scales.shape[-1]} for dv = {dv}")
+    _expect(fn, "slots", slots, (None,), (torch.int32,))
+    N = slots.numel() if slots is not None else (n_slots if states is None else states.shape[0])
+    _expect(fn, "states", states, (N, H, dk, dv), (torch.float32,))
+    dev = _one_device(fn, codes=codes, scales=scales, slots=slots, states=states)
+    return N, n_slots, H, dk, dv, dv // scales.shape[-1], dev
+
+
+def kda_state_store(states, codes, scales, slots=None, stream=None):
+    """Writes states [N, H, dk, dv] fp32 into slots slots[n] (device int32 [N]; None: slot n) of the
+    8-bit state cache: codes [n_slots, H, dk, dv] (torch.int8 or torch.float8_e4m3fn) and scales
+    [n_slots, H, dk, dv / group] fp32, group 32, 64 or 128.  Slots outside the cache are skipped; of
+    several states for one slot the last is stored.  Returns (codes, scales)."""
+    fn = "kda_state_store"
+    if not isinstance(states, torch.Tensor) or states.dim() != 4:
+        raise ValueError(f"{fn}: states must be a [N, H, dk, dv] tensor")
+    N, n_slots, H, dk, dv, group, dev = _check_cache(fn, codes, scales, slots, states)
+    lib = load_library()
+    _launch(fn, dev, stream, lambda sp: lib.kda_state_store(
+        _ptr(states), _ptr(slots), _ptr(codes), _CODES[codes.dtype], _ptr(scales), N, n_slots, H,
+        dk, dv, group, sp))
+    return codes, scales
+
+
+def kda_state_load(codes, scales, slots=None, states=None, stream=None):
+    """Reads states back: states[n] = codes * scales of slot slots[n] (None: slot n), zeros where the
+    slot lies outside the cache (-1: no cached prefix).  Returns states [N, H, dk, dv] fp32."""
+    fn = "kda_state_load"
+    N, n_slots, H, dk, dv, group, dev = _check_cache(fn, codes, scales, slots, states)
+    ts = _torch_stream(stream, dev)
+    if states is None:
+        states = _alloc(ts, (N, H, dk, dv), torch.float32, dev)
+    lib = load_library()
+    _launch(fn, dev, ts, lambda sp: lib.kda_state_load(
+        _ptr(codes), _CODES[codes.dtype], _ptr(scales), _ptr(slots), _ptr(states), N, n_slots, H,
+        dk, dv, group, sp))
+    return states

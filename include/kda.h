@@ -1,6 +1,8 @@
 /*
  * kda.h -- C ABI of libkda.so, the MI355X (gfx950) implementation of the Kimi Delta Attention
- * (KDA) forward pass: the forget gate, chunked prefill and the single-token decode step.
+ * (KDA) forward pass: the forget gate, chunked prefill and the single-token decode step; and of its
+ * siblings: linear attention with one decay per head (prefill, gradients, decode step) and an 8-bit
+ * cache of recurrent states.
  *
  * Pages the operations come from (titles as published):
  *   [bagrov] "Архитектура Kimi K3: как открытая модель с миллионным контекстом конкурирует с
@@ -267,6 +269,111 @@ int kda_decode_verify(const void *q, const void *k, const void *v, const void *b
 int kda_decode_commit(const void *q, const void *k, const void *v, const void *beta, int in_dtype,
                       const void *g, int g_dtype, float *state, const int32_t *accepted, int32_t N,
                       int32_t K, int32_t H, int32_t dk, int32_t dv, void *stream);
+
+/*
+ * ---- Linear attention with one decay per head ------------------------------------------------
+ * The recurrent sibling of KDA: the same d_k x d_v state per (sequence, head), which each token only
+ * decays and adds to (no erase along the key, no per-channel gate):
+ *     S_t = e^g S_{t-1} + k_t v_t^T,   o_t = scale * S_t^T q_t,
+ * with g = g[h] <= 0 one log-decay per head, a constant of the model (0 = plain linear attention,
+ * -inf = each token sees itself alone).  Layouts, streams, workspaces and errors are those stated at
+ * the top of this file; further, for the calls from here to the end of this file:
+ *   - every tensor pointer must be aligned to 16 bytes except g, cu_seqlens, slots, scales (4)
+ *     (KDA_ERR_UNSUPPORTED);
+ *   - the stream must belong to the current device;
+ *   - g is device memory and its sign the caller's contract, tested by KDA_DEBUG_VALIDATE;
+ *     positive values grow the state instead of failing.
+ *
+ * kda_linear_chunk_workspace_size -- workspace bytes of kda_linear_chunk_fwd (backward = 0) or
+ * kda_linear_chunk_bwd (backward != 0) for n_seqs sequences of total_tokens tokens (B*T).  May be
+ * 0 (a NULL workspace is then accepted).  Never fails; 0 for invalid sizes.
+ */
+size_t kda_linear_chunk_workspace_size(int32_t n_seqs, int64_t total_tokens, int32_t H, int32_t dk,
+                                       int32_t dv, int in_dtype, int backward);
+
+/*
+ * kda_linear_chunk_fwd -- chunked prefill of the recurrence above.
+ *   q, k, v       : inputs in in_dtype (KDA_F32 or KDA_BF16), layouts at the top of this file.
+ *   g             : [H] fp32 log-decay.
+ *   initial_state, final_state, cu_seqlens, o, o_dtype, B, T, n_seqs, dk, dv, scale, workspace :
+ *                   as in kda_chunk_fwd (T = 0 and empty sequences pass the state through).
+ *   workspace     : at least kda_linear_chunk_workspace_size(..., 0) bytes.
+ * Sums and states are fp32; bf16 inputs enter the products exactly, and values formed on the way
+ * (the states, the decayed scores) as two or more bf16 terms, so that o is the fp32 result rounded
+ * once to o_dtype (error of an fp32 o: about 1e-5 of its size for bf16 inputs) and the final state
+ * holds fp32 accuracy.
+ */
+int kda_linear_chunk_fwd(const void *q, const void *k, const void *v, int in_dtype, const float *g,
+                         const float *initial_state, float *final_state, const int32_t *cu_seqlens,
+                         void *o, int o_dtype, int32_t B, int64_t T, int32_t n_seqs, int32_t H,
+                         int32_t dk, int32_t dv, float scale, void *workspace,
+                         size_t workspace_bytes, void *stream);
+
+/*
+ * kda_linear_chunk_bwd -- gradients of kda_linear_chunk_fwd.  With G_t the gradient of S_t
+ * (G_T = d_final_state + scale q_T do_T^T, G_t = e^g G_{t+1} + scale q_t do_t^T):
+ *     dq_t = scale * S_t do_t,   dk_t = G_t v_t,   dv_t = G_t^T k_t,   d_initial_state = e^g G_1.
+ * The states are recomputed from q, k, v; nothing has to be kept from the forward call.  The decays
+ * are constants: no gradient of g is formed.
+ *   d_o             : [B, T, H, d_v] in in_dtype.
+ *   d_final_state   : [N, H, d_k, d_v] fp32 or NULL (= zeros).
+ *   dq, dk_out, dv_out : gradients of q, k, v, same shapes, in in_dtype.
+ *   d_initial_state : [N, H, d_k, d_v] fp32 or NULL (not wanted).
+ * No output may overlap an input, the workspace or another output; initial_state may be NULL
+ * (= zeros).  workspace: at least kda_linear_chunk_workspace_size(..., 1) bytes.
+ */
+int kda_linear_chunk_bwd(const void *q, const void *k, const void *v, int in_dtype, const float *g,
+                         const float *initial_state, const int32_t *cu_seqlens, const void *d_o,
+                         const float *d_final_state, void *dq, void *dk_out, void *dv_out,
+                         float *d_initial_state, int32_t B, int64_t T, int32_t n_seqs, int32_t H,
+                         int32_t dk, int32_t dv, float scale, void *workspace,
+                         size_t workspace_bytes, void *stream);
+
+/*
+ * kda_linear_decode_step -- one token of the recurrence for N independent sequences, each state
+ * updated in place (read once, written once).
+ *   q, k : [N, H, d_k]; v : [N, H, d_v] in in_dtype; g : [H] fp32; state : [N, H, d_k, d_v] fp32;
+ *   o    : [N, H, d_v] in o_dtype; must not overlap any input or the state.
+ *   N >= 0 (0 is a no-op).
+ */
+int kda_linear_decode_step(const void *q, const void *k, const void *v, int in_dtype,
+                           const float *g, float *state, void *o, int o_dtype, int32_t N, int32_t H,
+                           int32_t dk, int32_t dv, float scale, void *stream);
+
+/*
+ * ---- 8-bit state cache -------------------------------------------------------------------------
+ * A pool of n_slots slots, each holding one sequence's states [H, d_k, d_v] as 8-bit codes with one
+ * fp32 scale per group of `group` neighbouring value channels of a state row.  It keeps the states
+ * a recurrent layer's prefix cache or scheduler puts aside ([habr, § Как обслуживать два разных
+ * кеша]) -- final states, or the checkpoints of kda_chunk_fwd_checkpointed -- in about a quarter of
+ * their fp32 size; KDA and linear-attention states alike.
+ *   codes  : [n_slots, H, d_k, d_v], one byte each: KDA_CODE_I8 (signed integers -127 .. 127) or
+ *            KDA_CODE_E4M3 (8-bit floats of 4 exponent and 3 mantissa bits, largest 448, no
+ *            infinities).
+ *   scales : [n_slots, H, d_k, d_v / group] fp32.
+ *   group  : 32, 64 or 128, at most d_v.
+ *   slots  : device int32 [N], the slot of each of the N sequences, or NULL (sequence n in slot n;
+ *            then N <= n_slots is required).
+ *
+ * kda_state_store -- writes states [N, H, d_k, d_v] fp32 into their slots:
+ *     scale = max|x| / M (M = 127 or 448) over the group, in fp32; code = x / scale rounded to the
+ *     nearest code, ties to even (exact: the quotient is never rounded twice).
+ * A group of zeros gets scale 0 and codes 0; a group with an infinity or a NaN gets a NaN scale and
+ * codes 0, and reads back as NaN.  Sequences whose slot is outside [0, n_slots) are not stored; of
+ * several sequences with one slot the last is.  Other slots are left as they were.
+ *
+ * kda_state_load -- states[n] = code * scale of slots[n] (fp32, rounded once); a slot outside
+ * [0, n_slots) gives zeros, the state of a sequence without a cached prefix.
+ */
+typedef enum { KDA_CODE_I8 = 0, KDA_CODE_E4M3 = 1 } kda_code;
+
+int kda_state_store(const float *states, const int32_t *slots, void *codes, int code,
+                    float *scales, int32_t N, int32_t n_slots, int32_t H, int32_t dk, int32_t dv,
+                    int32_t group, void *stream);
+
+int kda_state_load(const void *codes, int code, const float *scales, const int32_t *slots,
+                   float *states, int32_t N, int32_t n_slots, int32_t H, int32_t dk, int32_t dv,
+                   int32_t group, void *stream);
 
 #ifdef __cplusplus
 }

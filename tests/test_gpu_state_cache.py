@@ -1,0 +1,246 @@
+"""The 8-bit state cache against its definition in fp64 (linear_ref.quantise).  Codes and scales have
+to be equal: the quotient x / scale is rounded once, to the nearest code, ties to even."""
+import numpy as np
+import pytest
+import torch
+
+import linear_ref as R
+from gated_delta_rule_60_amd import kda as K
+from kda_testutil import DEV, say
+
+pytestmark = pytest.mark.gpu
+CODES = [torch.int8, torch.float8_e4m3fn]
+
+
+def pool(n_slots, H, dk, dv, group, dtype, byte=0x55):
+    codes = torch.full((n_slots, H, dk, dv), byte, dtype=torch.uint8, device=DEV).view(dtype)
+    return codes, torch.full((n_slots, H, dk, dv // group), 3.0, device=DEV)
+
+
+def states(N, H, dk, dv, seed=0):
+    gen = torch.Generator("cpu").manual_seed(seed)
+    return torch.randn((N, H, dk, dv), generator=gen) * \
+        torch.exp2(-12 * torch.rand((N, H, dk, 1), generator=gen))
+
+
+def expect_slot(codes, scales, slot, x, group):
+    c, s = R.quantise(x.numpy(), group, codes.dtype)
+    assert np.array_equal(R.code_values(codes[slot]), c)
+    assert np.array_equal(scales[slot].cpu().numpy().view(np.uint32) & 0x7fffffff,
+                          s.view(np.uint32) & 0x7fffffff) or \
+        np.array_equal(scales[slot].cpu().numpy(), s, equal_nan=True)
+
+
+@pytest.mark.parametrize("dtype", CODES)
+@pytest.mark.parametrize("dk,dv,group", [(128, 128, 128), (128, 128, 64), (128, 128, 32), (64, 64, 64),
+                                         (64, 64, 32), (64, 128, 128), (128, 64, 32)])
+@pytest.mark.parametrize("N,H", [(1, 1), (3, 5)])
+def test_store_and_load(N, H, dk, dv, group, dtype):
+    x = states(N, H, dk, dv, seed=N + dk)
+    codes, scales = pool(7, H, dk, dv, group, dtype)
+    slots = torch.tensor([5, 0, 6][:N], dtype=torch.int32, device=DEV)
+    K.kda_state_store(x.to(DEV), codes, scales, slots)
+    back = K.kda_state_load(codes, scales, slots)
+    torch.cuda.synchronize()
+    for n in range(N):
+        expect_slot(codes, scales, int(slots[n]), x[n], group)
+    c, s = R.quantise(x.numpy(), group, dtype)
+    want = (c.astype(np.float32).reshape(s.shape + (group,)) * s[..., None]).reshape(x.shape)
+    assert np.array_equal(back.cpu().numpy(), want)
+    # the other slots stay as they were
+    for m in set(range(7)) - set(slots.tolist()):
+        assert bool((codes[m].view(torch.uint8) == 0x55).all()) and bool((scales[m] == 3.0).all())
+    # off by at most half a code: 1/2 of the scale, or half a step of the value and of the smallest
+    err = np.abs(back.double().cpu().numpy() - x.double().numpy()).reshape(s.shape + (group,))
+    sc = s[..., None].astype(np.float64)
+    v = np.abs(x.double().numpy()).reshape(err.shape)
+    step = 0.5 * sc if dtype == torch.int8 else np.maximum(2.0 ** -4 * v, 2.0 ** -10 * sc)
+    assert np.all(err <= step * (1 + 2.0 ** -20))
+
+
+@pytest.mark.parametrize("dtype", CODES)
+def test_ties_and_extremes(dtype):
+    """Quotients on and next to the borders between codes, zeros, the smallest and largest floats."""
+    most = R.MOST[dtype]
+    vals = R.e4m3_values()
+    grid = np.arange(-127, 128) if dtype == torch.int8 else np.sort(np.unique(vals[np.isfinite(vals)]))
+    mids = (grid[1:] + grid[:-1]) / 2
+    x = np.zeros((1, 1, 64, 128), np.float32)
+    rng = np.random.default_rng(4)
+    for r in range(64):
+        scale = np.float32(2.0 ** int(rng.integers(-20, 20))) if r < 24 else np.float32(rng.uniform(1e-3, 1e3))
+        pick = rng.choice(np.concatenate([mids, grid]), 128) * np.float64(scale)
+        row = pick.astype(np.float32)
+        nudge = rng.integers(-1, 2, 128)
+        row = np.where(nudge == 1, np.nextafter(row, np.float32(np.inf), dtype=np.float32), row)
+        row = np.where(nudge == -1, np.nextafter(row, np.float32(-np.inf), dtype=np.float32), row)
+        row[0] = np.float32(most) * scale
+        x[0, 0, r] = row
+    x[0, 0, 60] = 0.0
+    x[0, 0, 61] = rng.standard_normal(128).astype(np.float32) * np.float32(1e-43)     # subnormal
+    x[0, 0, 62] = rng.standard_normal(128).astype(np.float32) * np.float32(1e-38)
+    x[0, 0, 63] = np.clip(rng.standard_normal(128), -3, 3).astype(np.float32) * np.float32(1e38)
+    x = torch.from_numpy(x)
+    codes, scales = pool(1, 1, 64, 128, 128, dtype)
+    K.kda_state_store(x.to(DEV), codes, scales)
+    back = K.kda_state_load(codes, scales)
+    torch.cuda.synchronize()
+    c, s = R.quantise(x.numpy(), 128, dtype)
+    got = R.code_values(codes)
+    bad = np.argwhere(got != c)
+    say("  differing codes:", len(bad), bad[:5].tolist())
+    assert len(bad) == 0 and np.array_equal(scales.cpu().numpy(), s)
+    assert np.array_equal(back.cpu().numpy(), (c.astype(np.float32) * s[0, 0][None, None]))
+
+
+@pytest.mark.parametrize("dtype", CODES)
+def test_infinities_and_nans_stay_in_their_group(dtype):
+    x = states(1, 2, 64, 128, seed=3)
+    x[0, 0, 3, 5], x[0, 1, 7, 127], x[0, 0, 9, 40] = float("inf"), float("nan"), float("-inf")
+    codes, scales = pool(1, 2, 64, 128, 32, dtype)
+    K.kda_state_store(x.to(DEV), codes, scales)
+    back = K.kda_state_load(codes, scales).cpu()
+    c, s = R.quantise(x.numpy(), 32, dtype)
+    assert np.array_equal(R.code_values(codes), c) and np.array_equal(scales.cpu().numpy(), s, equal_nan=True)
+    nan = torch.isnan(back)
+    want = torch.zeros_like(nan)
+    want[0, 0, 3, 0:32] = want[0, 1, 7, 96:128] = want[0, 0, 9, 32:64] = True
+    assert torch.equal(nan, want)
+
+
+@pytest.mark.parametrize("dtype", CODES)
+def test_slots_outside_and_repeated(dtype):
+    N, H, dk, dv, group, n_slots = 600, 1, 64, 64, 64, 5
+    x = states(N, H, dk, dv, seed=8)
+    gen = torch.Generator("cpu").manual_seed(9)
+    slots = torch.randint(-2, n_slots + 2, (N,), generator=gen, dtype=torch.int32)
+    slots[slots == 3] = 2                             # slot 3 is never written
+    slots[0], slots[1] = 2 ** 31 - 1, -2 ** 31
+    codes, scales = pool(n_slots, H, dk, dv, group, dtype)
+    K.kda_state_store(x.to(DEV), codes, scales, slots.to(DEV))
+    torch.cuda.synchronize()
+    for m in range(n_slots):
+        who = (slots == m).nonzero().flatten().tolist()
+        if m == 3:
+            assert not who and bool((codes[m].view(torch.uint8) == 0x55).all())
+        else:
+            expect_slot(codes, scales, m, x[who[-1]], group)
+    back = K.kda_state_load(codes, scales, slots.to(DEV)).cpu()
+    outside = (slots < 0) | (slots >= n_slots)
+    assert bool((back[outside] == 0).all())
+    whole = K.kda_state_load(codes, scales).cpu()
+    assert torch.equal(back[~outside], whole[slots[~outside].long()])
+
+
+def test_no_sequences_and_given_buffer():
+    codes, scales = pool(2, 1, 64, 64, 64, torch.int8)
+    none = torch.empty((0,), dtype=torch.int32, device=DEV)
+    K.kda_state_store(torch.empty((0, 1, 64, 64), device=DEV), codes, scales, none)
+    assert K.kda_state_load(codes, scales, none).shape == (0, 1, 64, 64)
+    out = torch.full((1, 1, 64, 64), 9.0, device=DEV)
+    codes.view(torch.uint8).fill_(2)
+    assert K.kda_state_load(codes, scales, states=out) is out
+    assert bool((out == 6.0).all())
+
+
+def test_pool_beyond_four_gigabytes():
+    """Slots whose codes lie past 2^32 bytes, and scales past 2^30 elements' bytes."""
+    H, dk, dv, group = 8, 128, 128, 32
+    n_slots = (1 << 32) // (H * dk * dv) + 40
+    codes = torch.empty((n_slots, H, dk, dv), dtype=torch.int8, device=DEV)
+    scales = torch.empty((n_slots, H, dk, dv // group), device=DEV)
+    x = states(3, H, dk, dv, seed=17)
+    slots = torch.tensor([n_slots - 1, 0, n_slots - 39], dtype=torch.int32, device=DEV)
+    codes[-2:].zero_()
+    K.kda_state_store(x.to(DEV), codes, scales, slots)
+    back = K.kda_state_load(codes, scales, slots).cpu()
+    for n in range(3):
+        expect_slot(codes, scales, int(slots[n]), x[n], group)
+    c, s = R.quantise(x.numpy(), group, torch.int8)
+    assert np.array_equal(back.numpy(), (c.astype(np.float32).reshape(s.shape + (group,)) *
+                                         s[..., None]).reshape(x.shape))
+
+
+def test_captured_replays():
+    x = states(4, 2, 64, 64, seed=5).to(DEV)
+    codes, scales = pool(4, 2, 64, 64, 64, torch.int8)
+    out = torch.empty_like(x)
+    K.kda_state_store(x, codes, scales)
+    want = K.kda_state_load(codes, scales).clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        K.kda_state_store(x, codes, scales)
+        K.kda_state_load(codes, scales, states=out)
+    for _ in range(3):
+        codes.view(torch.uint8).zero_(), out.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want)
+        K.kda_state_load(codes, scales)
+        torch.cuda.synchronize()
+
+
+def test_prefix_chain():
+    """The operators together: a shared prefix is prefilled once, its state parked in the cache; two
+    requests resume it (a third starts without a prefix), prefill their own prompts and decode.  The
+    difference from running without the cache is the stored state's error carried through."""
+    H, d, P, T, steps = 3, 128, 150, 70, 3
+    gen = torch.Generator("cpu").manual_seed(21)
+    rn = lambda *s: (torch.randn(s, generator=gen) / d ** 0.5).to(torch.bfloat16).to(DEV)   # noqa: E731
+    g = torch.tensor([-0.002, -0.05, -0.5], device=DEV)
+    pre, own = [rn(1, P, H, d) for _ in range(3)], [rn(3, T, H, d) for _ in range(3)]
+    tok = [[rn(3, H, d) for _ in range(3)] for _ in range(steps)]
+    _, S = K.kda_linear_chunk_fwd(*pre, g)
+    for dtype in CODES:
+        codes, scales = pool(4, H, d, d, 32, dtype)
+        K.kda_state_store(S, codes, scales, torch.tensor([2], dtype=torch.int32, device=DEV))
+        start = K.kda_state_load(codes, scales, torch.tensor([2, -1, 2], dtype=torch.int32, device=DEV))
+        exact = torch.zeros_like(start)
+        exact[0] = exact[2] = S[0]
+        ref_in = [x.double().cpu().numpy() for x in own]
+        for n in range(steps):
+            ref_in = [np.concatenate([a, t.double().cpu().numpy()[:, None]], 1)
+                      for a, t in zip(ref_in, tok[n])]
+        def run(h):
+            o, hT = K.kda_linear_chunk_fwd(*own, g, initial_state=h, o_dtype=torch.float32)
+            out = [o] + [K.kda_linear_decode_step(*t, g, hT, o_dtype=torch.float32)[:, None] for t in tok]
+            return torch.cat(out, 1).double().cpu().numpy(), hT.double().cpu().numpy()
+        o, hT = run(start)
+        ref = R.forward(*ref_in, g.double().cpu().numpy(), R.np64(exact))
+        # error of the stored state: half a code
+        _, s = R.quantise(R.np64(S).astype(np.float32), 32, dtype)
+        s = np.repeat(s.astype(np.float64), 32, -1)
+        half = 0.5 * s if dtype == torch.int8 else np.maximum(2.0 ** -4 * np.abs(R.np64(S)), 2.0 ** -10 * s)
+        off = np.zeros(exact.shape)
+        off[0] = off[2] = half[0]
+        zeros = [np.abs(ref_in[0]), np.zeros_like(ref_in[1]), np.zeros_like(ref_in[2])]
+        bound = R.forward(*zeros, g.double().cpu().numpy(), off)
+        mag = R.forward_abs(*ref_in, g.double().cpu().numpy(), R.np64(exact) + off)
+        t = (2 * (T + steps) + 640) * 2.0 ** -24
+        assert np.all(np.abs(o - ref[0]) <= bound[0] * 1.0001 + (t + 2 * 2.0 ** -16) * mag[0])
+        assert np.all(np.abs(hT - ref[1]) <= bound[1] * 1.0001 + t * mag[1])
+
+
+def test_kda_checkpoints_resume_from_the_cache():
+    """KDA's own prefix cache: the checkpoints of kda_chunk_fwd_checkpointed stored as 8-bit codes; a
+    prefill resumed from one stays within the stored state's error of one resumed from fp32."""
+    from gated_delta_rule_60_amd import inputs
+    d = inputs.make_prefill(inputs.config("prefill_bf16", B=1, H=2, T=256))
+    x = {n: d[n].to(DEV) for n in ("q", "k", "v", "beta", "A", "z", "S0")}
+    cut = lambda n, lo, hi: x[n][:, lo:hi].contiguous()                            # noqa: E731
+    names = ("q", "k", "v", "beta")
+    _, _, ck = K.kda_chunk_fwd_checkpointed(*(cut(n, 0, 128) for n in names), 64, A=x["A"],
+                                            z=cut("z", 0, 128), initial_state=x["S0"])
+    codes, scales = pool(3, 2, 128, 128, 64, torch.int8)
+    slots = torch.tensor([2, 0], dtype=torch.int32, device=DEV)
+    K.kda_state_store(ck, codes, scales, slots)
+    back = K.kda_state_load(codes, scales, slots[1:].contiguous())
+    half = 0.5 * float(scales[0].max())
+    assert float((back - ck[1:]).abs().max()) <= half * (1 + 2.0 ** -20)
+    rest = lambda h: K.kda_chunk_fwd_gated(*(cut(n, 128, 256) for n in names), x["A"],   # noqa: E731
+                                           cut("z", 128, 256), initial_state=h, o_dtype=torch.float32)[1]
+    a, b = rest(ck[1:].contiguous()), rest(back)
+    # transitions do not expand a state (|k| = 1, beta in [0, 1], decay <= 1) in the 2-norm of a value
+    # column; 2e-3 is the prefill's own tolerance
+    n2 = (back - ck[1:]).double().norm(dim=2).max()
+    assert float((a - b).double().norm(dim=2).max()) <= float(n2) * 1.01 + 2 * 2e-3 * float(a.abs().max()) * 128 ** 0.5
