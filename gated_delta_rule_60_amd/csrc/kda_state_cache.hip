@@ -1,7 +1,7 @@
 // kda_state_cache.hip -- recurrent states in a pool of 8-bit codes: kda_state_store, kda_state_load.
 //
 // A state row (one key channel) is cut into groups of GROUP value channels; a group has one fp32
-// scale, max|x| / M with M the largest code (127, or 448 for e4m3), and its codes are x / scale
+// scale, max|x| times 1 / M with M the largest code (127, or 448 for e4m3), and its codes are x / scale
 // rounded to nearest even.  The quotient must not be rounded twice (an fp32 quotient next to the
 // border of two codes could fall on it), which costs a few VALU operations only:
 //   integers: c = rint(x * (1/scale)) is off by at most one; e = x - c scale is exact in fp32 (both
@@ -82,7 +82,7 @@ __global__ void __launch_bounds__(256) store_kernel(const float* __restrict__ st
         for (int32_t m = n + 1 + static_cast<int32_t>(threadIdx.x); m < N; m += 256) later |= slots[m] == slot;
         if (__syncthreads_or(later)) return;
     }
-    constexpr float most = CODE == KDA_CODE_I8 ? 127.f : 448.f;
+    constexpr float inv_most = 1.f / (CODE == KDA_CODE_I8 ? 127.f : 448.f);
     const int64_t e0 = static_cast<int64_t>(part) * (PASSES * 1024) + 4 * threadIdx.x;
     const float* src = states + n * per_seq;
     uint8_t* dst = codes + slot * per_seq;
@@ -101,7 +101,7 @@ __global__ void __launch_bounds__(256) store_kernel(const float* __restrict__ st
             bad += __shfl_xor(bad, off, 64);
         }
         const bool ok = bad == 0.f;
-        const float scale = ok ? a / most : __uint_as_float(0x7fc00000u);
+        const float scale = ok ? a * inv_most : __uint_as_float(0x7fc00000u);
         uint32_t w = 0;
         if (scale > 0.f) w = encode4<CODE>(make_float4(x[0], x[1], x[2], x[3]), scale);
         *reinterpret_cast<uint32_t*>(dst + e) = w;

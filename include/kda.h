@@ -356,8 +356,9 @@ int kda_linear_decode_step(const void *q, const void *k, const void *v, int in_d
  *            then N <= n_slots is required).
  *
  * kda_state_store -- writes states [N, H, d_k, d_v] fp32 into their slots:
- *     scale = max|x| / M (M = 127 or 448) over the group, in fp32; code = x / scale rounded to the
- *     nearest code, ties to even (exact: the quotient is never rounded twice).
+ *     scale = max|x| * (1 / M) (M = 127 or 448) over the group, each operation rounded to fp32;
+ *     code = x / scale rounded to the nearest code, ties to even (the exact quotient, rounded once),
+ *     at most M.
  * A group of zeros gets scale 0 and codes 0; a group with an infinity or a NaN gets a NaN scale and
  * codes 0, and reads back as NaN.  Sequences whose slot is outside [0, n_slots) are not stored; of
  * several sequences with one slot the last is.  Other slots are left as they were.

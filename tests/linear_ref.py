@@ -86,14 +86,15 @@ def e4m3_values():
 
 
 def quantise(x, group, dtype):
-    """(values of the codes, fp32 scales) of fp32 states x [..., dv]: nearest code, ties to even."""
+    """(values of the codes, fp32 scales) of fp32 states x [..., dv]: scale = max|x| times the fp32
+    reciprocal of the largest code; nearest code, ties to even."""
     x = np.asarray(x, dtype=np.float32)
     most = MOST[dtype]
     y = x.reshape(x.shape[:-1] + (-1, group))
     with np.errstate(invalid="ignore", over="ignore"):
         amax = np.abs(y).max(-1)
         bad = ~np.isfinite(y).all(-1)
-        scale = np.where(bad, np.float32(np.nan), (amax / np.float32(most)).astype(np.float32))
+        scale = np.where(bad, np.float32(np.nan), (amax * (np.float32(1) / np.float32(most))).astype(np.float32))
         div = np.where(np.isfinite(scale) & (scale > 0), scale, 1.0).astype(np.float64)[..., None]
         r = np.where((bad | (scale == 0))[..., None], 0.0, y.astype(np.float64)) / div
     if dtype == torch.int8:
