@@ -9,8 +9,7 @@
 //   dk : a = v,  b = do, c = q, backward, ub = scale, M from the final state's gradient transposed
 //   dv : a = k,  b = q,  c = do, backward, ub = scale, M from the final state's gradient, to the
 //        initial state's gradient
-#include "kda_common.hpp"
-#include "kda_internal.hpp"
+#include "kda_chunk_util.hpp"
 
 #include <algorithm>
 #include <type_traits>
@@ -23,74 +22,75 @@ struct Pass {
     void* out;
     const float* m_in;       // [N, H, DA, DC], or [N, H, DC, DA] with m_transposed; nullptr = zeros
     float* m_out;            // [N, H, DA, DC] or nullptr
+    float* seg_states;       // [slots, H, DA, DC] (or transposed); nullptr: whole sequences
+    float so, ub;
+    int32_t back;            // backward in time
+    int32_t m_transposed;    // m_in and seg_states are
+    int32_t exact;           // the segment states end in a state that is handed out
+};
+constexpr int MAX_PASSES = 3;
+
+// A launch covers (sequence, segment) slots times heads times passes.  A segment is 2^seg_shift tokens.
+// Fixed-length batches: n_seg slots per sequence; packed ones: slot (cu[n] >> seg_shift) + n + s for
+// segment s of sequence n, which leaves unused slots between sequences.
+struct Launch {
+    Pass pass[MAX_PASSES];
     const float* g;
     const int32_t* cu;
     int64_t T;
-    int32_t n_seqs, H;
-    float so, ub;
-    int32_t m_transposed;    // also of seg_states
-    int64_t seg;             // tokens per segment (>= T: whole sequences)
-    float* seg_states;       // [slots, H, DA, DC] (or transposed), segmented launches only
+    int32_t n_seqs, H, slots;
+    int32_t seg_shift;       // 40: whole sequences
+    int32_t n_seg;           // of a fixed-length sequence
+    int32_t passes;
 };
+constexpr int WHOLE = 40;
 
-// A launch covers (sequence, segment) slots times heads.  Fixed-length batches: ceil(T / seg) slots per
-// sequence; packed ones: slot floor(cu[n] / seg) + n + s for segment s of sequence n, which leaves
-// unused slots between sequences.  seg >= T gives one slot per sequence.
 struct Where {
     int32_t n, s, n_seg;     // sequence, segment, segments of the sequence
     int64_t lo, hi;          // tokens of the segment
 };
-__device__ __forceinline__ void seq_range(const Pass& p, int32_t n, int64_t& lo, int64_t& hi) {
-    if (p.cu == nullptr) {
-        lo = n * p.T;
-        hi = lo + p.T;
+__device__ __forceinline__ void seq_range(const Launch& L, int32_t n, int64_t& lo, int64_t& hi) {
+    if (L.cu == nullptr) {
+        lo = n * L.T;
+        hi = lo + L.T;
     } else {
-        const int64_t x = p.cu[n], y = p.cu[n + 1];
-        lo = x < 0 ? 0 : (x > p.T ? p.T : x);
-        hi = y < lo ? lo : (y > p.T ? p.T : y);
+        const int64_t x = L.cu[n], y = L.cu[n + 1];
+        lo = x < 0 ? 0 : (x > L.T ? L.T : x);
+        hi = y < lo ? lo : (y > L.T ? L.T : y);
     }
 }
-__device__ __forceinline__ int32_t slot_base(const Pass& p, int32_t n) {
+__device__ __forceinline__ int32_t first_slot(const Launch& L, int32_t n) {
     int64_t lo, hi;
-    seq_range(p, n, lo, hi);
-    return static_cast<int32_t>(lo / p.seg) + n;
+    seq_range(L, n, lo, hi);
+    return static_cast<int32_t>(lo >> L.seg_shift) + n;
 }
-__device__ __forceinline__ int32_t segments(const Pass& p, int64_t len) {
-    return len <= p.seg ? 1 : static_cast<int32_t>((len + p.seg - 1) / p.seg);
+__device__ __forceinline__ int32_t segments(const Launch& L, int64_t len) {
+    const int64_t one = int64_t(1) << L.seg_shift;
+    return len <= one ? 1 : static_cast<int32_t>((len + one - 1) >> L.seg_shift);
 }
-__device__ __forceinline__ bool locate(const Pass& p, int32_t slot, Where& w) {
-    int32_t first;
-    if (p.cu == nullptr) {
-        const int32_t per = segments(p, p.T);
-        w.n = slot / per;
-        first = w.n * per;
+__device__ __forceinline__ bool locate(const Launch& L, int32_t slot, Where& w) {
+    int64_t lo, hi;
+    if (L.cu == nullptr) {
+        w.n = slot / L.n_seg;
+        w.s = slot - w.n * L.n_seg;
+        seq_range(L, w.n, lo, hi);
     } else {
-        int32_t a = 0, b = p.n_seqs - 1;          // the last sequence whose first slot is <= slot
+        int32_t a = 0, b = L.n_seqs - 1;          // the last sequence whose first slot is <= slot
         while (a < b) {
             const int32_t m = (a + b + 1) / 2;
-            if (slot_base(p, m) <= slot) a = m; else b = m - 1;
+            if (first_slot(L, m) <= slot) a = m; else b = m - 1;
         }
         w.n = a;
-        first = slot_base(p, a);
+        w.s = slot - first_slot(L, a);
+        seq_range(L, a, lo, hi);
     }
-    int64_t lo, hi;
-    seq_range(p, w.n, lo, hi);
-    w.n_seg = segments(p, hi - lo);
-    w.s = slot - first;
+    w.n_seg = segments(L, hi - lo);
     if (w.s < 0 || w.s >= w.n_seg) return false;
-    w.lo = lo + w.s * p.seg;
-    w.hi = w.lo + p.seg < hi ? w.lo + p.seg : hi;
+    w.lo = lo + (static_cast<int64_t>(w.s) << L.seg_shift);
+    const int64_t end = w.lo + (int64_t(1) << L.seg_shift);
+    w.hi = end < hi ? end : hi;
     return true;
 }
-
-typedef float f32x4 __attribute__((ext_vector_type(4)));
-typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
-typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
-typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
-typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
-typedef float f32x2 __attribute__((ext_vector_type(2)));
-typedef short s16x4 __attribute__((ext_vector_type(4)));
-typedef __attribute__((address_space(3))) uint8_t lds_u8;
 
 __device__ __forceinline__ f32x4 mfma_bf16(u32x4 a, u32x4 b, f32x4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c,
@@ -101,16 +101,10 @@ __device__ __forceinline__ f32x4 mfma_f32(float a, float b, f32x4 c) {
 }
 // Two floats as bf16 (nearest even), x in the low half.
 __device__ __forceinline__ uint32_t pack_bf16(float x, float y) {
-    const f32x2 v = {x, y};
-    return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, bf16x2));
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{x, y}, bf16x2));
 }
 __device__ __forceinline__ float lo_f32(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float hi_f32(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
-// x, y as two bf16 terms each: hi + lo, off by at most 2^-16 of the value.
-__device__ __forceinline__ void split2(float x, float y, uint32_t& hi, uint32_t& lo) {
-    hi = pack_bf16(x, y);
-    lo = pack_bf16(x - lo_f32(hi), y - hi_f32(hi));
-}
 // Three bf16 terms, each a truncation: 24 bits, exact.
 __device__ __forceinline__ void split3(float x, float y, uint32_t& h, uint32_t& m, uint32_t& l) {
     const uint32_t ux = __float_as_uint(x), uy = __float_as_uint(y);
@@ -122,546 +116,595 @@ __device__ __forceinline__ void split3(float x, float y, uint32_t& h, uint32_t& 
     l = __builtin_amdgcn_perm(__float_as_uint(y2), __float_as_uint(x2), 0x07060302u);
 }
 
-// A [TOK][DIM] tile in LDS, row-major in 16-byte units.  Units are XOR-ed with the row so that 16 rows'
-// equal units (fragments along the channels) and 16 rows' neighbouring units (fragments along the
-// tokens) both spread over all banks.
+template <typename T>
+__device__ __forceinline__ T lds_get(const void* sm, uint32_t byte) {
+    typedef T __attribute__((may_alias)) T_ma;
+    return *reinterpret_cast<const T_ma*>(static_cast<const uint8_t*>(sm) + byte);
+}
+template <typename T>
+__device__ __forceinline__ void lds_put(void* sm, uint32_t byte, T x) {
+    typedef T __attribute__((may_alias)) T_ma;
+    *reinterpret_cast<T_ma*>(static_cast<uint8_t*>(sm) + byte) = x;
+}
+// The transposing read gives lane i of each 16 channel i of the 4 tokens whose 8-byte pieces the lanes
+// point at (lane 4 r + s: token r, channels 4 s .. 4 s + 3).
+__device__ __forceinline__ u32x2 lds_transpose(const uint8_t* sm) {
+    return __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)sm));
+}
+// Workgroup barrier for LDS: this wave's LDS accesses are done; loads and stores may stay in flight (a
+// __syncthreads would wait for them).
+__device__ __forceinline__ void lds_barrier() {
+    wave_fence();
+    __builtin_amdgcn_s_waitcnt(0xC07F);              // lgkmcnt(0)
+    __builtin_amdgcn_s_barrier();
+    wave_fence();
+}
+
+// A tile of token rows in LDS.  A row's 16-byte units are XOR-ed with bits of the row inside groups of
+// eight, and every 1 KB of rows (R of them) is followed by PAD bytes, such that
+//   16 rows' equal units (operands along the channels) fill all 64 banks;
+//   fp32: so do 4 neighbouring units of every fourth row (operands along the tokens);
+//   16 bits: 8 rows' 4 neighbouring half units (transposing reads, half a wavefront at a time) fill half
+//   of them, in two turns -- the halves of a unit cannot be told apart by a swizzle of whole units;
+// while 16 tokens, and groups of eight units, stay a constant apart.
 template <int DIM, int ES>
 struct Tile {
-    static constexpr int UPR = DIM * ES / 16;              // units per row
+    static constexpr int RB = DIM * ES, UPR = RB / 16, R = 1024 / RB;
+    static constexpr int PAD = ES == 2 ? (R == 4 ? 128 : 0) : (R == 4 ? 64 : 32), PIECE = 1024 + PAD;
+    static constexpr int ROWS16 = 16 / R * PIECE;
+    static __device__ __forceinline__ int mix(int row) {
+        if constexpr (ES == 2) return 2 * ((R == 4 ? row : row >> 1) & 3);
+        else return row % R;
+    }
     static __device__ __forceinline__ uint32_t at(int row, int unit) {
-        const int x = UPR >= 16 ? (row & 15) : ((row >> 1) & 7);
-        return static_cast<uint32_t>((row * UPR + (unit ^ x)) * 16);
+        return (row / R) * PIECE + (row % R) * RB + (unit & ~7) * 16 + ((unit & 7) ^ mix(row)) * 16;
     }
 };
 
-// 4 tokens x 16 channels, transposed: lane i of each 16 gets channel i of the 4 tokens whose 8-byte
-// pieces the lanes point at (lane 4 r + s: token r, piece s).
-__device__ __forceinline__ u32x2 lds_tr(const lds_u8* p) {
-    return __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                                         (__attribute__((address_space(3))) s16x4*)(p)));
+// 16 bytes per lane from a buffer to 1 KB of LDS.
+__device__ __forceinline__ void transfer16(__amdgpu_buffer_rsrc_t r, uint32_t offset, uint8_t* sm) {
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)sm, 16, offset, 0, 0, 0);
+}
+// A chunk's rows of one head (n tokens from tok0) straight into a tile, 1 KB per wave instruction; a
+// lane's 16 bytes come from wherever the tile's layout wants them.  Rows past the n-th lie outside the
+// buffer range and read as zeros.
+template <typename TT, int TOK, int WAVES>
+__device__ __forceinline__ void fetch_tile(uint8_t* sm, const void* base, int64_t tok0, int n, int32_t H, int32_t h,
+                                           int wave, int lane) {
+    const uint32_t row = static_cast<uint32_t>(H) * TT::RB;
+    const __amdgpu_buffer_rsrc_t r = make_rsrc_u(static_cast<const uint8_t*>(base) + (tok0 * H + h) * TT::RB,
+                                                 (n - 1) * row + TT::RB);
+    const int r0 = wave * TT::R + lane / TT::UPR, un = lane % TT::UPR;     // WAVES R rows on: the same units
+    const uint32_t at = r0 * row + ((un & ~7) | ((un & 7) ^ TT::mix(r0))) * 16;
+#pragma unroll
+    for (int i = 0; i < TOK / TT::R / WAVES; ++i)
+        transfer16(r, at + WAVES * i * TT::R * row, sm + TT::PIECE * (WAVES * i + wave));
 }
 
-// The pass in chunks of TOK tokens; one workgroup of four waves per (segment, head), wave w with the
-// output columns [w DC / 4, (w + 1) DC / 4).  With lam^p = e^(p g), i and j tokens of a chunk of n:
-//     out_i = so lam^(i+1) M^T a_i + so sum_{j <= i} lam^(i-j) (b_j . a_i) c_j,
-//     M    <- lam^n M + ub sum_j lam^(n-1-j) b_j c_j^T                         (forward; backward:
-//     j >= i, lam^(j-i), lam^(n-1-i) for the state's part and lam^(j+1) for the update).
-// All three products are MFMAs computed transposed (out^T = M^T a^T, scores^T = b a^T), which makes
-// every accumulator the next product's operand without a shuffle: an accumulator holds four
-// neighbouring rows per lane, and an operand wants eight values along the contraction per lane -- any
-// eight, as long as both operands take the same ones.  So M's tiles feed out^T = M^T a^T from the
-// registers that M = b^T c left them in, and the scores likewise.  The decays multiply accumulators
-// (fp32) wherever they can; only the update's sits inside a contraction, on c.
-//   16-bit inputs: M and the scores are read as two bf16 terms, the decayed c as three (exact).
-//   fp32 inputs: 16x16x4 fp32 MFMAs throughout.
-// STATE_ONLY: just M from zero, the segment's own contribution.
-template <int DT, int ODT, int DA, int DC, bool BACK, bool STATE_ONLY>
-__global__ void __launch_bounds__(256) linear_chunk_kernel(Pass p) {
-    constexpr bool BF = DT == KDA_BF16;
-    constexpr int ES = BF ? 2 : 4;
-    constexpr int TOK = BF ? 64 : 32;                // tokens per chunk
-    constexpr int IT = TOK / 16;                     // token tiles
-    constexpr int MT = DA / 16;                      // state row tiles
-    constexpr int NT = DC / 64;                      // column tiles of a wave
-    constexpr int UA = TOK * DA * ES / 16 / 256, UC = TOK * DC * ES / 16 / 256;   // units per lane
+// The groups (token tile it, 32 tokens tg) of scores on the near side of the diagonal, 0 .. 5.
+template <bool BACK>
+__device__ __forceinline__ constexpr int score_group(int it, int tg) {
+    if (BACK) return tg == 1 ? it : 4 + it;          // group 1: tiles 0 .. 3, group 0: tiles 0, 1
+    return tg == 0 ? it : 2 + it;                    // group 0: tiles 0 .. 3, group 1: tiles 2, 3
+}
+
+// The workgroup's LDS.
+template <int DT, int DA, int DC, bool STATE_ONLY>
+struct ChunkLds {
+    static constexpr int ES = DT == KDA_BF16 ? 2 : 4, TOK = DT == KDA_BF16 ? 64 : 32;
     using TA = Tile<DA, ES>;
     using TC = Tile<DC, ES>;
-    constexpr int SA = TOK * DA * ES, SC = TOK * DC * ES;
-    __shared__ __align__(16) uint8_t smem[(STATE_ONLY ? 0 : SA) + SA + SC];
-    __shared__ float s_lam[TOK + 1], s_lam_lo[TOK + 1], s_rd[TOK];
-    __shared__ __align__(16) float s_up[TOK];
-    uint8_t* const smB = smem;
-    uint8_t* const smC = smem + SA;
-    uint8_t* const smA = smem + SA + SC;
+    __align__(16) uint8_t b[TOK / TA::R * TA::PIECE];
+    __align__(16) uint8_t c[TOK / TC::R * TC::PIECE];
+    __align__(16) uint8_t a[STATE_ONLY ? 16 : TOK / TA::R * TA::PIECE];
+    // scores: 16-bit hi and lo operands per group, or fp32 tiles
+    __align__(16) uint8_t p[STATE_ONLY ? 16 : (ES == 2 ? 12 : 3) * 1024];
+    __align__(16) float rd[TOK];                     // decays of the state's part and of the update
+    __align__(16) float up[TOK];
+    // so ub lam^(i-j) of a lane's scores: tile on the diagonal (masked), tile next to it
+    f32x4 on_diag[STATE_ONLY ? 1 : 64], next[STATE_ONLY ? 1 : 64];
+    double lam[TOK + 1];
+    double lam_full_inv;
+};
+
+// The pass in chunks of TOK tokens; one workgroup per (segment, head), wave w with the output columns
+// 16 w .. 16 w + 15.  With lam^p = e^(p g), i and j tokens of a chunk of n:
+//     out_i = so lam^(i+1) M^T a_i + so ub sum_{j <= i} lam^(i-j) (b_j . a_i) c_j,
+//     M    <- lam^n M + ub sum_j lam^(n-1-j) b_j c_j^T                         (forward; backward:
+//     j >= i, lam^(j-i), lam^(n-1-i) for the state's part and lam^(j+1) for the update).
+// All products are MFMAs computed transposed (out^T = M^T a^T, scores^T = b a^T), which makes every
+// accumulator the next product's operand without a shuffle: an accumulator holds four neighbouring rows
+// per lane, and an operand wants eight (fp32: one) values along the contraction per lane -- any, as
+// long as both operands take the same ones.  So M's tiles feed out^T = M^T a^T from the registers that
+// M = b^T c left them in, and the scores likewise (through LDS, since all waves need all scores).  The
+// decays multiply accumulators (fp32) where they can; only the update's sits inside a contraction, on c.
+//   16-bit inputs: M and the scores are read as two bf16 terms (2^-16); the decayed c as three (exact)
+//   where M ends in a state that is handed out in fp32, as two where it only feeds 16-bit outputs.
+//   fp32 inputs: 16x16x4 fp32 MFMAs throughout.
+// Sixteen waves fill a CU (two workgroups; 128 registers and 68 KB of LDS each), and one workgroup's
+// transfers run under the other's products.
+// STATE_ONLY: just M from zero, the segment's own contribution.
+template <int DT, int ODT, int DA, int DC, bool BACK, bool STATE_ONLY>
+__device__ __forceinline__ void chunk_pass(const Launch& L, const Pass& p, int32_t slot, int32_t h,
+                                           ChunkLds<DT, DA, DC, STATE_ONLY>& lds) {
+    using Lds = ChunkLds<DT, DA, DC, STATE_ONLY>;
+    using TA = typename Lds::TA;
+    using TC = typename Lds::TC;
+    constexpr bool BF = DT == KDA_BF16;
+    constexpr int TOK = Lds::TOK, WAVES = DC / 16;
+    constexpr int IT = TOK / 16, MT = DA / 16;       // token tiles, state row tiles
+    constexpr int KK = DA / 32, JG = TOK / 32;       // 16 bits: contraction steps over channels, tokens
 
     Where w;
-    const int32_t h = static_cast<int32_t>(blockIdx.x % p.H);
-    const int32_t slot = static_cast<int32_t>(blockIdx.x / p.H);
-    if (!locate(p, slot, w)) return;
+    if (!locate(L, slot, w)) return;
     if (STATE_ONLY && w.s == (BACK ? 0 : w.n_seg - 1)) return;    // nothing follows it
-    const int t = threadIdx.x, lane = t & 63, wave = t >> 6, q = lane >> 4, l16 = lane & 15;
+    const int t = threadIdx.x, lane = t & 63, q = lane >> 4, l16 = lane & 15;
+    const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
     const int64_t len = w.hi - w.lo;
     const int n_chunks = static_cast<int>((len + TOK - 1) / TOK);
+    const int64_t unit = static_cast<int64_t>(w.n) * L.H + h;
 
-    // ---- decays
-    if (t <= TOK && len > 0) {
-        const double x = t == 0 ? 1.0 : exp(static_cast<double>(t) * static_cast<double>(p.g[h]));
-        const float f = static_cast<float>(x);
-        s_lam[t] = f;
-        s_lam_lo[t] = f < 3.4e38f ? static_cast<float>(x - static_cast<double>(f)) : 0.f;
-    }
-    __syncthreads();
+    auto load = [&](int c) {
+        const int64_t off = static_cast<int64_t>(BACK ? n_chunks - 1 - c : c) * TOK;
+        const int n = static_cast<int>(len - off < TOK ? len - off : TOK);
+        fetch_tile<TA, TOK, WAVES>(lds.b, p.b, w.lo + off, n, L.H, h, wave, lane);
+        fetch_tile<TC, TOK, WAVES>(lds.c, p.c, w.lo + off, n, L.H, h, wave, lane);
+        if constexpr (!STATE_ONLY) fetch_tile<TA, TOK, WAVES>(lds.a, p.a, w.lo + off, n, L.H, h, wave, lane);
+    };
+    if (n_chunks > 0) load(0);
 
-    // ---- the state: tile (mt, nt), register r holds row 16 mt + 4 q + r, column col(nt)
-    const int wcol = wave * (DC / 4);
-    auto col = [&](int nt) { return wcol + (NT == 2 ? 8 * (l16 >> 2) + (l16 & 3) + 4 * nt : l16); };
-    const int64_t unit = static_cast<int64_t>(w.n) * p.H + h;
-    f32x4 M[MT][NT];
+    // ---- the state: tile mt, register r of lane (l16, q) holds row row(mt) + r, column 16 wave + l16
+    auto row = [&](int mt) { return BF ? 32 * (mt >> 1) + 8 * q + 4 * (mt & 1) : 16 * mt + 4 * q; };
+    const int col = 16 * wave + l16;
+    f32x4 M[MT];
     {
-        const float* src = nullptr;
+        const float* src = nullptr;                  // none: an empty range, which reads as zeros
         if constexpr (!STATE_ONLY) {
-            if (p.seg_states) src = p.seg_states + (static_cast<int64_t>(slot) * p.H + h) * (DA * DC);
+            if (p.seg_states) src = p.seg_states + (static_cast<int64_t>(slot) * L.H + h) * (DA * DC);
             else if (p.m_in) src = p.m_in + unit * (DA * DC);
         }
+        const __amdgpu_buffer_rsrc_t rs = make_rsrc_u(src, src ? DA * DC * 4 : 0);
+        if (p.m_transposed) {
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
+            for (int mt = 0; mt < MT; ++mt)
+                M[mt] = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(rs, (col * DA + row(mt)) * 4, 0, 0));
+        } else {
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                const int r0 = 16 * mt + 4 * q, c = col(nt);
-                f32x4 x = {0.f, 0.f, 0.f, 0.f};
-                if (src) {
-                    if (p.m_transposed) x = *reinterpret_cast<const f32x4*>(src + c * DA + r0);
-                    else
+            for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-                        for (int r = 0; r < 4; ++r) x[r] = src[(r0 + r) * DC + c];
-                }
-                M[mt][nt] = x;
-            }
+                for (int r = 0; r < 4; ++r)
+                    M[mt][r] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rs, ((row(mt) + r) * DC + col) * 4, 0, 0));
+        }
     }
 
-    // lam^(i-j) of the score tiles on the diagonal (masked) and of those next to it
-    f32x4 Dd = {0.f, 0.f, 0.f, 0.f}, Dn = Dd;
+    // ---- decays lam^p
+    if (len > 0) {
+        const double g = static_cast<double>(L.g[h]);
+        if (t <= TOK) lds.lam[t] = t == 0 ? 1.0 : exp(t * g);
+        if (t == TOK + 1) lds.lam_full_inv = exp(-TOK * g);
+    }
+    lds_barrier();
     if constexpr (!STATE_ONLY) {
-        if (len > 0)
+        if (len > 0 && t < 64) {
+            f32x4 d, e;
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
-                const int e = BACK ? 4 * q + r - l16 : l16 - 4 * q - r;
-                Dd[r] = e < 0 ? 0.f : p.so * p.ub * s_lam[e < 0 ? 0 : e];
-                Dn[r] = p.so * p.ub * s_lam[16 + e];
+                const int x = BACK ? 4 * q + r - l16 : l16 - 4 * q - r;
+                d[r] = x < 0 ? 0.f : p.so * p.ub * static_cast<float>(lds.lam[x < 0 ? 0 : x]);
+                e[r] = p.so * p.ub * static_cast<float>(lds.lam[16 + x]);
             }
+            lds.on_diag[lane] = d;
+            lds.next[lane] = e;
+        }
     }
 
-    // ---- tiles: global -> registers -> LDS
-    u32x4 ra[UA], rb[UA], rc[UC];
-    const int64_t row_a = static_cast<int64_t>(p.H) * DA * ES, row_c = static_cast<int64_t>(p.H) * DC * ES;
-    auto fetch = [&](u32x4* reg, const void* base, auto dim, int64_t row_bytes, int64_t tok0, int n) {
-        constexpr int DIM = decltype(dim)::value, UPR = DIM * ES / 16, U = TOK * UPR / 256;
-        const uint8_t* src = static_cast<const uint8_t*>(base) + tok0 * row_bytes + static_cast<int64_t>(h) * DIM * ES;
+    // ---- operands' byte offsets.  16 bits, along the channels: channels 32 kk + 8 q .. + 7 of token
+    // 16 it + l16; along the tokens: tokens 32 tg + 4 q .. + 3 and 32 tg + 16 + 4 q .. + 3, of state row
+    // tile mt's rows (channels 32 (mt / 2) + 8 s + 4 (mt % 2) .. + 3 in piece s) or of the wave's columns.
+    uint32_t chan[2], tok[2];
 #pragma unroll
-        for (int i = 0; i < U; ++i) {
-            const int u = t + 256 * i, row = u / UPR, un = u % UPR;
-            u32x4 x = {0u, 0u, 0u, 0u};
-            if (row < n) x = *reinterpret_cast<const u32x4*>(src + row * row_bytes + un * 16);
-            reg[i] = x;
-        }
+    for (int x = 0; x < 2; ++x) {
+        chan[x] = TA::at(l16, 4 * x + q);
+        tok[x] = TA::at(4 * q + (l16 >> 2), 4 * x + (l16 & 3));
+    }
+    const uint32_t tok_c = TC::at(4 * q + (l16 >> 2), 2 * wave + ((l16 & 3) >> 1)) + 8 * (l16 & 1);
+    auto channels = [&](const uint8_t* sm, int it, int kk) {
+        return lds_get<u32x4>(sm, chan[kk & 1] + it * TA::ROWS16 + (kk >> 1) * 128);
     };
-    auto chunk_range = [&](int c, int64_t& tok0, int& n) {
-        const int64_t off = static_cast<int64_t>(BACK ? n_chunks - 1 - c : c) * TOK;
-        tok0 = w.lo + off;
-        n = static_cast<int>(len - off < TOK ? len - off : TOK);
+    auto tokens = [&](uint32_t at, const uint8_t* sm, int rows16) {
+        const u32x2 x = lds_transpose(sm + at), y = lds_transpose(sm + at + rows16);
+        return u32x4{x[0], x[1], y[0], y[1]};
     };
-    using ic_a = std::integral_constant<int, DA>;
-    using ic_c = std::integral_constant<int, DC>;
-    auto fetch_all = [&](int c) {
-        int64_t tok0;
-        int n;
-        chunk_range(c, tok0, n);
-        fetch(rb, p.b, ic_a{}, row_a, tok0, n);
-        fetch(rc, p.c, ic_c{}, row_c, tok0, n);
-        if constexpr (!STATE_ONLY) fetch(ra, p.a, ic_a{}, row_a, tok0, n);
-    };
-    if (n_chunks > 0) fetch_all(0);
 
+    // The state is held as f times the registers, so that most chunks need not multiply it; f and 1 / f
+    // are fp64, and the registers take f over before it leaves [2^-12, 2^12].
+    double f = 1.0, f_inv = 1.0;
+    const bool exact = STATE_ONLY ? p.exact != 0 : p.m_out && w.s == (BACK ? 0 : w.n_seg - 1);
     int table_n = -1;
     for (int c = 0; c < n_chunks; ++c) {
-        int64_t tok0;
-        int n;
-        chunk_range(c, tok0, n);
-        if (c > 0) __syncthreads();                  // the last chunk's tiles have been read
-#pragma unroll
-        for (int i = 0; i < UA; ++i) {
-            const int u = t + 256 * i, row = u / TA::UPR, un = u % TA::UPR;
-            *reinterpret_cast<u32x4*>(smB + TA::at(row, un)) = rb[i];
-            if constexpr (!STATE_ONLY) {
-                if constexpr (BF) {
-                    // a's channels in operand order: unit 4 G + q holds channels 32 G + 4 q .. + 3 and
-                    // 32 G + 16 + 4 q .. + 3
-                    const int d = (un & ~3) + 2 * (un & 1), half = (un >> 1) & 1;
-                    *reinterpret_cast<u32x2*>(smA + TA::at(row, d) + 8 * half) = u32x2{ra[i][0], ra[i][1]};
-                    *reinterpret_cast<u32x2*>(smA + TA::at(row, d + 1) + 8 * half) = u32x2{ra[i][2], ra[i][3]};
-                } else {
-                    *reinterpret_cast<u32x4*>(smA + TA::at(row, un)) = ra[i];
-                }
-            }
-        }
-#pragma unroll
-        for (int i = 0; i < UC; ++i) {
-            const int u = t + 256 * i, row = u / TC::UPR, un = u % TC::UPR;
-            *reinterpret_cast<u32x4*>(smC + TC::at(row, un)) = rc[i];
-        }
+        const int64_t off = static_cast<int64_t>(BACK ? n_chunks - 1 - c : c) * TOK;
+        const int64_t tok0 = w.lo + off;
+        const int n = static_cast<int>(len - off < TOK ? len - off : TOK);
         if (n != table_n) {
             table_n = n;
             if (t < TOK) {
                 const int from_end = n - 1 - t;
-                s_rd[t] = p.so * s_lam[BACK ? (from_end < 0 ? 0 : from_end) : t + 1];
-                s_up[t] = p.ub * s_lam[BACK ? t + 1 : (from_end < 0 ? 0 : from_end)];
+                lds.rd[t] = p.so * static_cast<float>(lds.lam[BACK ? (from_end < 0 ? 0 : from_end) : t + 1]);
+                lds.up[t] = p.ub * static_cast<float>(lds.lam[BACK ? t + 1 : (from_end < 0 ? 0 : from_end)]);
             }
         }
-        __syncthreads();
-        if (c + 1 < n_chunks) fetch_all(c + 1);
+        __builtin_amdgcn_s_waitcnt(vmcnt_imm(0));
+        lds_barrier();                               // the tiles are there
 
-        const float lam_n = s_lam[n], lam_n_lo = s_lam_lo[n];
-        f32x4 O[IT][NT];
+        f32x4 O[IT];
         if constexpr (!STATE_ONLY) {
+            // ---- scores, shared out over the waves
+            if constexpr (BF) {
+                for (int grp = wave; grp < 6; grp += WAVES) {
+                    // (it, tg) with score_group(it, tg) == grp
+                    const int tg = BACK ? (grp < 4) : (grp >= 4), it = BACK ? (grp & 3) : (grp < 4 ? grp : grp - 2);
+                    u32x4 hi, lo;
+                    f32x4 P[2] = {zero4(), zero4()};
+#pragma unroll
+                    for (int kk = 0; kk < KK; ++kk) {
+                        const u32x4 a = channels(lds.a, it, kk);
+#pragma unroll
+                        for (int hh = 0; hh < 2; ++hh) P[hh] = mfma_bf16(channels(lds.b, 2 * tg + hh, kk), a, P[hh]);
+                    }
+#pragma unroll
+                    for (int hh = 0; hh < 2; ++hh) {
+                        const int jt = 2 * tg + hh, dist = BACK ? jt - it : it - jt;
+                        if (dist < 0) P[hh] = zero4();
+                        else if (dist == 0) P[hh] *= lds.on_diag[lane];
+                        else P[hh] *= lds.next[lane] * static_cast<float>(lds.lam[16 * (dist - 1)]);
+                        uint32_t h0, o0, h1, o1;
+                        split_pair(P[hh][0], P[hh][1], h0, o0);
+                        split_pair(P[hh][2], P[hh][3], h1, o1);
+                        hi[2 * hh] = h0; hi[2 * hh + 1] = h1;
+                        lo[2 * hh] = o0; lo[2 * hh + 1] = o1;
+                    }
+                    lds_put(lds.p, grp * 2048 + lane * 16, hi);
+                    lds_put(lds.p, grp * 2048 + 1024 + lane * 16, lo);
+                }
+            } else if (wave < 3) {
+                // tiles (out, in): (0, 0), (1, 1) and (1, 0), backward (0, 1)
+                const int it = BACK ? (wave == 1) : (wave > 0), jt = BACK ? (wave > 0) : (wave == 1);
+                f32x4 P = zero4();
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt) {
+                    const f32x4 a = lds_get<f32x4>(lds.a, TA::at(16 * it + l16, 4 * mt + q));
+                    const f32x4 b = lds_get<f32x4>(lds.b, TA::at(16 * jt + l16, 4 * mt + q));
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) P = mfma_f32(b[r], a[r], P);
+                }
+                P *= wave < 2 ? lds.on_diag[lane] : lds.next[lane];
+                lds_put(lds.p, wave * 1024 + lane * 16, P);
+            }
             // ---- the state's part
 #pragma unroll
-            for (int it = 0; it < IT; ++it)
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) O[it][nt] = f32x4{0.f, 0.f, 0.f, 0.f};
+            for (int it = 0; it < IT; ++it) O[it] = zero4();
             if constexpr (BF) {
 #pragma unroll
-                for (int kk = 0; kk < DA / 32; ++kk) {
-                    u32x4 hi[NT], lo[NT];
+                for (int kk = 0; kk < KK; ++kk) {
+                    u32x4 hi, lo, a[IT];
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
+                    for (int it = 0; it < IT; ++it) a[it] = channels(lds.a, it, kk);
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const f32x4& m = M[2 * kk + (e >> 1)][nt];
-                            uint32_t x, y;
-                            split2(m[2 * (e & 1)], m[2 * (e & 1) + 1], x, y);
-                            hi[nt][e] = x;
-                            lo[nt][e] = y;
-                        }
-#pragma unroll
-                    for (int it = 0; it < IT; ++it) {
-                        const u32x4 a = *reinterpret_cast<const u32x4*>(smA + TA::at(16 * it + l16, 4 * kk + q));
-#pragma unroll
-                        for (int nt = 0; nt < NT; ++nt) {
-                            O[it][nt] = mfma_bf16(hi[nt], a, O[it][nt]);
-                            O[it][nt] = mfma_bf16(lo[nt], a, O[it][nt]);
-                        }
+                    for (int e = 0; e < 4; ++e) {
+                        const f32x4& m = M[2 * kk + (e >> 1)];
+                        uint32_t x, y;
+                        split_pair(m[2 * (e & 1)], m[2 * (e & 1) + 1], x, y);
+                        hi[e] = x;
+                        lo[e] = y;
                     }
+#pragma unroll
+                    for (int it = 0; it < IT; ++it) O[it] = mfma_bf16(hi, a[it], O[it]);
+#pragma unroll
+                    for (int it = 0; it < IT; ++it) O[it] = mfma_bf16(lo, a[it], O[it]);
                 }
             } else {
 #pragma unroll
                 for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
                     for (int it = 0; it < IT; ++it) {
-                        const f32x4 a = *reinterpret_cast<const f32x4*>(smA + TA::at(16 * it + l16, 4 * mt + q));
+                        const f32x4 a = lds_get<f32x4>(lds.a, TA::at(16 * it + l16, 4 * mt + q));
 #pragma unroll
-                        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                            for (int r = 0; r < 4; ++r) O[it][nt] = mfma_f32(M[mt][nt][r], a[r], O[it][nt]);
+                        for (int r = 0; r < 4; ++r) O[it] = mfma_f32(M[mt][r], a[r], O[it]);
                     }
             }
+            const float ff = static_cast<float>(f);
 #pragma unroll
-            for (int it = 0; it < IT; ++it) {
-                const float rd = s_rd[16 * it + l16];
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) O[it][nt] *= rd;
-            }
+            for (int it = 0; it < IT; ++it) O[it] *= lds.rd[16 * it + l16] * ff;
         }
-        // ---- decay (lam^n as hi + lo: its rounding would act the same way chunk after chunk)
+        // ---- decay
+        const double fn = f * lds.lam[n];
+        if (n == TOK && fn >= 0x1p-12 && fn <= 0x1p12) {
+            f = fn;
+            f_inv *= lds.lam_full_inv;
+        } else {
+            const float x = static_cast<float>(fn);
+            f = f_inv = 1.0;
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
+            for (int mt = 0; mt < MT; ++mt) M[mt] *= x;
+        }
+        const float up_scale = static_cast<float>(f_inv);
+
+        // ---- c along the tokens
+        constexpr int CJ = BF ? JG : IT;
+        u32x4 vf[CJ];
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
+        for (int j = 0; j < CJ; ++j) {
+            if constexpr (BF) vf[j] = tokens(tok_c + 2 * j * TC::ROWS16, lds.c, TC::ROWS16);
+            else
 #pragma unroll
                 for (int r = 0; r < 4; ++r)
-                    M[mt][nt][r] = __builtin_fmaf(M[mt][nt][r], lam_n_lo, M[mt][nt][r] * lam_n);
-
-        if constexpr (BF) {
-            constexpr int TG = TOK / 32;
-            // c along the tokens: group tg, tokens 32 tg + 4 q .. + 3 and 32 tg + 16 + 4 q .. + 3
-            u32x4 vf[TG][NT];
-#pragma unroll
-            for (int tg = 0; tg < TG; ++tg)
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    const int row = 32 * tg + 4 * q + (l16 >> 2), s = l16 & 3;
-                    const int un = wcol / 8 + (NT == 2 ? s : s >> 1), half = NT == 2 ? nt : (s & 1);
-                    const u32x2 x = lds_tr((const lds_u8*)(smC + TC::at(row, un) + 8 * half));
-                    const u32x2 y = lds_tr((const lds_u8*)(smC + TC::at(row + 16, un) + 8 * half));
-                    vf[tg][nt] = u32x4{x[0], x[1], y[0], y[1]};
-                }
-            // ---- scores and their part of the output
-            if constexpr (!STATE_ONLY) {
-                const float l16p = s_lam[16], l32p = s_lam[32];
-#pragma unroll
-                for (int it = 0; it < IT; ++it) {
-                    u32x4 a[DA / 32];
-#pragma unroll
-                    for (int kk = 0; kk < DA / 32; ++kk)
-                        a[kk] = *reinterpret_cast<const u32x4*>(smA + TA::at(16 * it + l16, 4 * kk + q));
-#pragma unroll
-                    for (int tg = 0; tg < TG; ++tg) {
-                        if (BACK ? 2 * tg + 1 < it : 2 * tg > it) continue;
-                        u32x4 hi = {0u, 0u, 0u, 0u}, lo = hi;
-#pragma unroll
-                        for (int hh = 0; hh < 2; ++hh) {
-                            const int jt = 2 * tg + hh, dist = BACK ? jt - it : it - jt;
-                            if (dist < 0) continue;
-                            f32x4 P = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                            for (int kk = 0; kk < DA / 32; ++kk) {
-                                const int row = 16 * jt + l16, un = 4 * kk + (q >> 1), half = 8 * (q & 1);
-                                const u32x2 x = *reinterpret_cast<const u32x2*>(smB + TA::at(row, un) + half);
-                                const u32x2 y = *reinterpret_cast<const u32x2*>(smB + TA::at(row, un + 2) + half);
-                                P = mfma_bf16(u32x4{x[0], x[1], y[0], y[1]}, a[kk], P);
-                            }
-                            f32x4 D = dist == 0 ? Dd : Dn;
-                            if (dist == 2) D *= l16p;
-                            if (dist == 3) D *= l32p;
-                            P *= D;
-                            uint32_t h0, o0, h1, o1;
-                            split2(P[0], P[1], h0, o0);
-                            split2(P[2], P[3], h1, o1);
-                            hi[2 * hh] = h0; hi[2 * hh + 1] = h1;
-                            lo[2 * hh] = o0; lo[2 * hh + 1] = o1;
-                        }
-#pragma unroll
-                        for (int nt = 0; nt < NT; ++nt) {
-                            O[it][nt] = mfma_bf16(vf[tg][nt], hi, O[it][nt]);
-                            O[it][nt] = mfma_bf16(vf[tg][nt], lo, O[it][nt]);
-                        }
-                    }
-                }
-            }
-            // ---- update
-#pragma unroll
-            for (int tg = 0; tg < TG; ++tg) {
-                const f32x4 w0 = *reinterpret_cast<const f32x4*>(s_up + 32 * tg + 4 * q);
-                const f32x4 w1 = *reinterpret_cast<const f32x4*>(s_up + 32 * tg + 16 + 4 * q);
-                u32x4 ch[NT], cm[NT], cl[NT];
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const f32x4& ww = e < 2 ? w0 : w1;
-                        uint32_t x, y, z;
-                        split3(lo_f32(vf[tg][nt][e]) * ww[2 * (e & 1)], hi_f32(vf[tg][nt][e]) * ww[2 * (e & 1) + 1], x, y, z);
-                        ch[nt][e] = x;
-                        cm[nt][e] = y;
-                        cl[nt][e] = z;
-                    }
-#pragma unroll
-                for (int mt = 0; mt < MT; ++mt) {
-                    const int row = 32 * tg + 4 * q + (l16 >> 2), s = l16 & 3;
-                    const u32x2 x = lds_tr((const lds_u8*)(smB + TA::at(row, 2 * mt + (s >> 1)) + 8 * (s & 1)));
-                    const u32x2 y = lds_tr((const lds_u8*)(smB + TA::at(row + 16, 2 * mt + (s >> 1)) + 8 * (s & 1)));
-                    const u32x4 kt = {x[0], x[1], y[0], y[1]};
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {
-                        M[mt][nt] = mfma_bf16(kt, cl[nt], M[mt][nt]);
-                        M[mt][nt] = mfma_bf16(kt, cm[nt], M[mt][nt]);
-                        M[mt][nt] = mfma_bf16(kt, ch[nt], M[mt][nt]);
-                    }
-                }
-            }
-        } else {
-            auto element = [&](const uint8_t* sm, auto tile, int row, int ch) {
-                using TT = decltype(tile);
-                return *reinterpret_cast<const float*>(sm + TT::at(row, ch >> 2) + 4 * (ch & 3));
-            };
-            f32x4 vf[IT][NT];
-#pragma unroll
-            for (int jt = 0; jt < IT; ++jt)
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) vf[jt][nt][r] = element(smC, TC{}, 16 * jt + 4 * q + r, col(nt));
-            if constexpr (!STATE_ONLY) {
+                    vf[j][r] = lds_get<uint32_t>(lds.c, TC::at(16 * j + 4 * q + r, 4 * wave + (l16 >> 2)) + 4 * (l16 & 3));
+        }
+        if constexpr (!STATE_ONLY) {
+            lds_barrier();                           // the scores are there
+            if constexpr (BF) {
 #pragma unroll
                 for (int it = 0; it < IT; ++it)
 #pragma unroll
-                    for (int jt = 0; jt < IT; ++jt) {
-                        const int dist = BACK ? jt - it : it - jt;
-                        if (dist < 0) continue;
-                        f32x4 P = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                        for (int mt = 0; mt < MT; ++mt) {
-                            const f32x4 a = *reinterpret_cast<const f32x4*>(smA + TA::at(16 * it + l16, 4 * mt + q));
-                            const f32x4 b = *reinterpret_cast<const f32x4*>(smB + TA::at(16 * jt + l16, 4 * mt + q));
-#pragma unroll
-                            for (int r = 0; r < 4; ++r) P = mfma_f32(b[r], a[r], P);
-                        }
-                        P *= dist == 0 ? Dd : Dn;
-#pragma unroll
-                        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                            for (int r = 0; r < 4; ++r) O[it][nt] = mfma_f32(vf[jt][nt][r], P[r], O[it][nt]);
+                    for (int tg = 0; tg < JG; ++tg) {
+                        if (BACK ? 2 * tg + 1 < it : 2 * tg > it) continue;
+                        const uint32_t at = score_group<BACK>(it, tg) * 2048 + lane * 16;
+                        O[it] = mfma_bf16(vf[tg], lds_get<u32x4>(lds.p, at), O[it]);
+                        O[it] = mfma_bf16(vf[tg], lds_get<u32x4>(lds.p, at + 1024), O[it]);
                     }
-            }
+            } else {
 #pragma unroll
-            for (int jt = 0; jt < IT; ++jt) {
-                const f32x4 ww = *reinterpret_cast<const f32x4*>(s_up + 16 * jt + 4 * q);
+                for (int tile = 0; tile < 3; ++tile) {
+                    const int it = BACK ? (tile == 1) : (tile > 0), jt = BACK ? (tile > 0) : (tile == 1);
+                    const f32x4 P = lds_get<f32x4>(lds.p, tile * 1024 + lane * 16);
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) vf[jt][nt] *= ww;
-#pragma unroll
-                for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        const float k = element(smB, TA{}, 16 * jt + 4 * q + r, 16 * mt + l16);
-#pragma unroll
-                        for (int nt = 0; nt < NT; ++nt) M[mt][nt] = mfma_f32(k, vf[jt][nt][r], M[mt][nt]);
-                    }
-            }
-        }
-        // ---- out: lane l16 holds token 16 it + l16, four (eight) neighbouring columns
-        if constexpr (!STATE_ONLY) {
-            constexpr int OS = ODT == KDA_BF16 ? 2 : 4;
-#pragma unroll
-            for (int it = 0; it < IT; ++it) {
-                const int i = 16 * it + l16;
-                if (i < n) {
-                    uint8_t* dst = static_cast<uint8_t*>(p.out) +
-                                   (((tok0 + i) * p.H + h) * DC + wcol + 4 * NT * q) * OS;
-                    if constexpr (ODT == KDA_BF16) {
-                        uint32_t x[2 * NT];
-#pragma unroll
-                        for (int nt = 0; nt < NT; ++nt) {
-                            x[2 * nt] = pack_bf16(O[it][nt][0], O[it][nt][1]);
-                            x[2 * nt + 1] = pack_bf16(O[it][nt][2], O[it][nt][3]);
-                        }
-                        if constexpr (NT == 2) *reinterpret_cast<u32x4*>(dst) = u32x4{x[0], x[1], x[2], x[3]};
-                        else *reinterpret_cast<u32x2*>(dst) = u32x2{x[0], x[1]};
-                    } else {
-#pragma unroll
-                        for (int nt = 0; nt < NT; ++nt) *reinterpret_cast<f32x4*>(dst + 16 * nt) = O[it][nt];
-                    }
+                    for (int r = 0; r < 4; ++r) O[it] = mfma_f32(__uint_as_float(vf[jt][r]), P[r], O[it]);
                 }
             }
+            // ---- out: lane l16 holds token 16 it + l16, four neighbouring columns
+            constexpr int OS = ODT == KDA_BF16 ? 2 : 4;
+            const uint32_t orow = static_cast<uint32_t>(L.H) * DC * OS;
+            const __amdgpu_buffer_rsrc_t ro = make_rsrc_u(static_cast<uint8_t*>(p.out) + (tok0 * L.H + h) * DC * OS,
+                                                          (n - 1) * orow + DC * OS);
+#pragma unroll
+            for (int it = 0; it < IT; ++it) {
+                const uint32_t at = (16 * it + l16) * orow + (16 * wave + 4 * q) * OS;
+                if constexpr (ODT == KDA_BF16)
+                    __builtin_amdgcn_raw_buffer_store_b64(u32x2{pack_bf16(O[it][0], O[it][1]), pack_bf16(O[it][2], O[it][3])},
+                                                          ro, at, 0, 0);
+                else __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, O[it]), ro, at, 0, 0);
+            }
+        }
+        // ---- update
+        if constexpr (BF) {
+            // the decayed c in three terms (exact) where the state leaves in fp32, else in two
+            auto update = [&](auto three) {
+                constexpr bool THREE = decltype(three)::value;
+#pragma unroll
+                for (int tg = 0; tg < JG; ++tg) {
+                    const f32x4 w0 = lds_get<f32x4>(lds.up, 4 * (32 * tg + 4 * q)) * up_scale;
+                    const f32x4 w1 = lds_get<f32x4>(lds.up, 4 * (32 * tg + 16 + 4 * q)) * up_scale;
+                    u32x4 ch, cm, cl;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const f32x4& ww = e < 2 ? w0 : w1;
+                        const float c0 = lo_f32(vf[tg][e]) * ww[2 * (e & 1)], c1 = hi_f32(vf[tg][e]) * ww[2 * (e & 1) + 1];
+                        uint32_t x, y, z = 0;
+                        if constexpr (THREE) split3(c0, c1, x, y, z);
+                        else split_pair(c0, c1, x, y);
+                        ch[e] = x;
+                        cm[e] = y;
+                        cl[e] = z;
+                    }
+#pragma unroll
+                    for (int mt = 0; mt < MT; ++mt) {
+                        const u32x4 kt = tokens(tok[(mt >> 1) & 1] + 2 * tg * TA::ROWS16 + (mt >> 2) * 128 + 8 * (mt & 1), lds.b,
+                                                TA::ROWS16);
+                        if constexpr (THREE) M[mt] = mfma_bf16(kt, cl, M[mt]);
+                        M[mt] = mfma_bf16(kt, cm, M[mt]);
+                        M[mt] = mfma_bf16(kt, ch, M[mt]);
+                    }
+                }
+            };
+            if (exact) update(std::true_type{});
+            else update(std::false_type{});
+        } else {
+#pragma unroll
+            for (int jt = 0; jt < IT; ++jt) {
+                const f32x4 ww = lds_get<f32x4>(lds.up, 4 * (16 * jt + 4 * q)) * up_scale;
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const float cw = __uint_as_float(vf[jt][r]) * ww[r];
+#pragma unroll
+                    for (int mt = 0; mt < MT; ++mt)
+                        M[mt] = mfma_f32(lds_get<float>(lds.b, TA::at(16 * jt + 4 * q + r, 4 * mt + (l16 >> 2)) + 4 * (l16 & 3)),
+                                         cw, M[mt]);
+                }
+            }
+        }
+        if (c + 1 < n_chunks) {
+            lds_barrier();                           // the tiles have been read
+            load(c + 1);
         }
     }
 
     float* dst = nullptr;
-    if constexpr (STATE_ONLY) dst = p.seg_states + (static_cast<int64_t>(slot) * p.H + h) * (DA * DC);
+    if constexpr (STATE_ONLY) dst = p.seg_states + (static_cast<int64_t>(slot) * L.H + h) * (DA * DC);
     else if (p.m_out && w.s == (BACK ? 0 : w.n_seg - 1)) dst = p.m_out + unit * (DA * DC);
-    if (dst)
+    if (dst) {
+        const float ff = static_cast<float>(f);
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int r = 0; r < 4; ++r) dst[(16 * mt + 4 * q + r) * DC + col(nt)] = M[mt][nt][r];
+            for (int r = 0; r < 4; ++r) dst[(row(mt) + r) * DC + col] = M[mt][r] * ff;
+    }
+}
+
+// Workgroups are handed to the 8 XCDs in turn, and each XCD has an L2 whose channels interleave by a few
+// hundred bytes -- about one head's row.  So an XCD takes a contiguous range of (slot, head) units, heads
+// fastest, which spreads its rows over all its channels (heads dealt out to the XCDs one by one would
+// leave each XCD the same few channels of every token).  All passes of a unit follow one another there and
+// share the L2's copies of its rows.
+template <int DT, int ODT, int DA, int DC, bool STATE_ONLY>
+__global__ void __launch_bounds__(DC * 4, DA > DC ? 2 : 4) linear_chunk_kernel(Launch L) {
+    __shared__ ChunkLds<DT, DA, DC, STATE_ONLY> lds;
+    const uint32_t units = static_cast<uint32_t>(L.slots) * L.H, per_xcd = (units + 7) / 8;
+    const uint32_t j = blockIdx.x / 8, x = blockIdx.x % 8 * per_xcd + j / L.passes;
+    if (j / L.passes >= per_xcd || x >= units) return;
+    const int32_t slot = static_cast<int32_t>(x / L.H), h = static_cast<int32_t>(x % L.H);
+    const Pass& p = L.pass[j % L.passes];
+    if (p.back) chunk_pass<DT, ODT, DA, DC, true, STATE_ONLY>(L, p, slot, h, lds);
+    else chunk_pass<DT, ODT, DA, DC, false, STATE_ONLY>(L, p, slot, h, lds);
 }
 
 // Segment states: from each segment's own contribution to the state it starts from, in place.
-// Grid (sequence * H + head, element blocks of 1024); each lane carries four elements along.
-template <bool BACK>
-__device__ __forceinline__ void scan_states(const Pass& p, int32_t elems) {
-    const int32_t n = blockIdx.x / p.H, h = blockIdx.x % p.H;
+// Grid (sequence * H + head, element blocks of 1024, pass); each lane carries four elements along.
+__global__ void __launch_bounds__(256) linear_scan_kernel(Launch L, int32_t elems) {
+    const Pass& p = L.pass[blockIdx.z];
+    const int32_t n = blockIdx.x / L.H, h = blockIdx.x % L.H;
     const int32_t e = blockIdx.y * 1024 + threadIdx.x * 4;
     int64_t lo, hi;
-    seq_range(p, n, lo, hi);
+    seq_range(L, n, lo, hi);
     const int64_t len = hi - lo;
-    const int32_t n_seg = segments(p, len);
-    const int32_t first = p.cu ? slot_base(p, n) : n * n_seg;
-    const double g = len > 0 ? static_cast<double>(p.g[h]) : 0.0;
-    f32x4 x = {0.f, 0.f, 0.f, 0.f};
-    if (p.m_in) x = *reinterpret_cast<const f32x4*>(p.m_in + (static_cast<int64_t>(n) * p.H + h) * elems + e);
-    float* at = p.seg_states + (static_cast<int64_t>(first) * p.H + h) * elems + e;
-    const int64_t step = static_cast<int64_t>(p.H) * elems;
-    const double full = exp(static_cast<double>(p.seg) * g);
-    const double part = exp(static_cast<double>(len - (n_seg - 1) * p.seg) * g);
+    const int32_t n_seg = segments(L, len);
+    const int32_t first = L.cu ? first_slot(L, n) : n * n_seg;
+    const double g = len > 0 ? static_cast<double>(L.g[h]) : 0.0;
+    f32x4 x = zero4();
+    if (p.m_in) x = *reinterpret_cast<const f32x4*>(p.m_in + (static_cast<int64_t>(n) * L.H + h) * elems + e);
+    float* at = p.seg_states + (static_cast<int64_t>(first) * L.H + h) * elems + e;
+    const int64_t step = static_cast<int64_t>(L.H) * elems;
+    // decay over a segment as hi + lo: its rounding would act the same way segment after segment
+    const int64_t part = len - (static_cast<int64_t>(n_seg - 1) << L.seg_shift);
+    const double full_d = n_seg > 1 ? exp(static_cast<double>(int64_t(1) << L.seg_shift) * g) : 1.0;
+    const double part_d = part > 0 ? exp(static_cast<double>(part) * g) : 1.0;
     for (int32_t i = 0; i < n_seg; ++i) {
-        const int32_t s = BACK ? n_seg - 1 - i : i;
+        const int32_t s = p.back ? n_seg - 1 - i : i;
         f32x4* slot = reinterpret_cast<f32x4*>(at + s * step);
-        f32x4 own = {0.f, 0.f, 0.f, 0.f};
+        f32x4 own = zero4();
         if (i < n_seg - 1) own = *slot;
         *slot = x;
-        const double l = s == n_seg - 1 ? part : full;
+        const double l = s == n_seg - 1 ? part_d : full_d;
         const float l_hi = static_cast<float>(l), l_lo = static_cast<float>(l - static_cast<double>(l_hi));
 #pragma unroll
         for (int r = 0; r < 4; ++r) x[r] = __builtin_fmaf(x[r], l_hi, __builtin_fmaf(x[r], l_lo, own[r]));
     }
 }
-__global__ void __launch_bounds__(256) linear_scan_kernel(Pass f, Pass b, int32_t elems) {
-    if (blockIdx.z == 0) scan_states<false>(f, elems);
-    else scan_states<true>(b, elems);
-}
 
 // ---------------------------------------------------------------- host side
 
-// Tokens per segment: whole sequences where (sequence, head) units alone give every CU two workgroups,
-// else so that all segments together do, but no shorter than 512 tokens.
-int64_t segment_tokens(int32_t n_seqs, int64_t total, int32_t H) {
-    const int64_t units = int64_t(n_seqs) * H;
-    if (units >= 512) return int64_t(1) << 40;
-    const int64_t want = (total * H + 511) / 512;                     // tokens of one of 512 equal shares
-    const int64_t seg = std::max<int64_t>(512, (want + 63) / 64 * 64);
-    return seg * n_seqs >= total ? int64_t(1) << 40 : seg;
+// log2 of the tokens per segment.  Whole sequences where (sequence, head) units alone give every CU a
+// workgroup (16 x 4096 tokens x 16 heads, bf16, d = 128: 337 us whole, 388 us in two segments each; 4 x 4096
+// x 16 in eight segments: 118 us) or where none is long (below 1024 tokens two more launches cost what the
+// shorter chains save).  Else as many segments as give every CU two workgroups, but no shorter than 256
+// tokens (fp32, whose chunks take longer: 128), so that a segment's state, read and written about four times,
+// stays small against its rows (8192 tokens x 8 heads: 57 us with 256-token segments, 68 us with 512).
+int segment_shift(int32_t n_seqs, int64_t total, int32_t H, int32_t in_dtype, bool packed) {
+    const int64_t units = int64_t(n_seqs) * H, longest = packed ? total : total / n_seqs;
+    if (units >= 256 || longest < 1024) return WHOLE;
+    const int64_t want = total * H / 512;                             // tokens of one of 512 equal shares
+    int shift = in_dtype == KDA_BF16 ? 8 : 7;
+    while ((int64_t(1) << (shift + 1)) <= want) ++shift;
+    return (int64_t(1) << shift) >= longest ? WHOLE : shift;
 }
-int64_t segment_slots(int32_t n_seqs, int64_t total, int64_t seg, bool packed) {
-    if (packed) return total / seg + n_seqs;
-    const int64_t T = total / n_seqs;
-    return n_seqs * std::max<int64_t>(1, (T + seg - 1) / seg);
+int64_t segment_slots(int32_t n_seqs, int64_t total, int shift, bool packed) {
+    if (packed) return (total >> shift) + n_seqs;
+    const int64_t T = total / n_seqs, one = int64_t(1) << shift;
+    return n_seqs * std::max<int64_t>(1, (T + one - 1) >> shift);
 }
 
-template <int DT, int ODT, bool BACK, bool STATE_ONLY>
-hipError_t launch_pass(const Pass& p, int64_t slots, int32_t da, int32_t dc, hipStream_t stream) {
-    const dim3 grid(static_cast<unsigned>(slots * p.H));
+template <int DT, int ODT, bool STATE_ONLY>
+hipError_t launch_chunks(const Launch& L, int32_t da, int32_t dc, hipStream_t stream) {
+    const int64_t groups = (int64_t(L.slots) * L.H + 7) / 8;
     auto go = [&](auto kernel) {
-        hipLaunchKernelGGL(kernel, grid, dim3(256), 0, stream, p);
+        hipLaunchKernelGGL(kernel, dim3(static_cast<unsigned>(groups * 8 * L.passes)), dim3(dc * 4), 0, stream, L);
         return hipGetLastError();
     };
-    if (da == 128 && dc == 128) return go(linear_chunk_kernel<DT, ODT, 128, 128, BACK, STATE_ONLY>);
-    if (da == 128) return go(linear_chunk_kernel<DT, ODT, 128, 64, BACK, STATE_ONLY>);
-    if (dc == 128) return go(linear_chunk_kernel<DT, ODT, 64, 128, BACK, STATE_ONLY>);
-    return go(linear_chunk_kernel<DT, ODT, 64, 64, BACK, STATE_ONLY>);
+    if (da == 128 && dc == 128) return go(linear_chunk_kernel<DT, ODT, 128, 128, STATE_ONLY>);
+    if (da == 128) return go(linear_chunk_kernel<DT, ODT, 128, 64, STATE_ONLY>);
+    if (dc == 128) return go(linear_chunk_kernel<DT, ODT, 64, 128, STATE_ONLY>);
+    return go(linear_chunk_kernel<DT, ODT, 64, 64, STATE_ONLY>);
 }
-
-Pass base_pass(const LinearArgs& a, int64_t seg) {
-    Pass p{};
-    p.g = a.g; p.cu = a.cu; p.T = a.T; p.n_seqs = a.n_seqs; p.H = a.H; p.so = 1.f; p.ub = 1.f; p.seg = seg;
-    return p;
-}
-
-hipError_t launch_scan(const Pass& f, const Pass& b, int passes, int32_t elems, hipStream_t stream) {
-    const dim3 grid(static_cast<unsigned>(f.n_seqs * f.H), static_cast<unsigned>(elems / 1024), static_cast<unsigned>(passes));
-    hipLaunchKernelGGL(linear_scan_kernel, grid, dim3(256), 0, stream, f, b, elems);
+hipError_t launch_scan(const Launch& L, int32_t elems, hipStream_t stream) {
+    const dim3 grid(static_cast<unsigned>(L.n_seqs * L.H), static_cast<unsigned>(elems / 1024), static_cast<unsigned>(L.passes));
+    hipLaunchKernelGGL(linear_scan_kernel, grid, dim3(256), 0, stream, L, elems);
     return hipGetLastError();
 }
 
-constexpr int64_t kWhole = int64_t(1) << 40;
+Launch base_launch(const LinearArgs& a) {
+    Launch L{};
+    const int64_t total = int64_t(a.B) * a.T;
+    L.g = a.g; L.cu = a.cu; L.T = a.T; L.n_seqs = a.n_seqs; L.H = a.H;
+    L.seg_shift = segment_shift(a.n_seqs, total, a.H, a.in_dtype, a.cu != nullptr);
+    L.slots = static_cast<int32_t>(segment_slots(a.n_seqs, total, L.seg_shift, a.cu != nullptr));
+    L.n_seg = L.slots / a.n_seqs;
+    return L;
+}
+Pass make_pass(const void* a, const void* b, const void* c, void* out, bool back, float so, float ub,
+               const float* m_in, bool transposed, float* m_out) {
+    Pass p{};
+    p.a = a; p.b = b; p.c = c; p.out = out; p.back = back; p.so = so; p.ub = ub; p.m_in = m_in;
+    p.m_transposed = transposed; p.m_out = m_out;
+    return p;
+}
 
 template <int DT, int ODT>
 hipError_t forward(const LinearArgs& a, hipStream_t stream) {
-    const int64_t total = int64_t(a.B) * a.T, seg = segment_tokens(a.n_seqs, total, a.H);
-    const int64_t slots = segment_slots(a.n_seqs, total, seg, a.cu != nullptr);
-    Pass p = base_pass(a, seg);
-    p.a = a.q; p.b = a.k; p.c = a.v; p.out = a.o; p.so = a.scale; p.m_in = a.h0; p.m_out = a.hT;
-    if (seg < kWhole) {
-        p.seg_states = static_cast<float*>(a.workspace);
-        hipError_t e = launch_pass<DT, ODT, false, true>(p, slots, a.dk, a.dv, stream);
-        if (e == hipSuccess) e = launch_scan(p, p, 1, a.dk * a.dv, stream);
+    Launch L = base_launch(a);
+    L.passes = 1;
+    L.pass[0] = make_pass(a.q, a.k, a.v, a.o, false, a.scale, 1.f, a.h0, false, a.hT);
+    if (L.seg_shift < WHOLE) {
+        L.pass[0].seg_states = static_cast<float*>(a.workspace);
+        L.pass[0].exact = a.hT != nullptr;
+        hipError_t e = launch_chunks<DT, DT, true>(L, a.dk, a.dv, stream);
+        if (e == hipSuccess) e = launch_scan(L, a.dk * a.dv, stream);
         if (e != hipSuccess) return e;
     }
-    return launch_pass<DT, ODT, false, false>(p, slots, a.dk, a.dv, stream);
+    return launch_chunks<DT, ODT, false>(L, a.dk, a.dv, stream);
 }
 
 template <int DT>
 hipError_t backward(const LinearArgs& a, hipStream_t stream) {
-    const int64_t total = int64_t(a.B) * a.T, seg = segment_tokens(a.n_seqs, total, a.H);
-    const int64_t slots = segment_slots(a.n_seqs, total, seg, a.cu != nullptr);
-    Pass q = base_pass(a, seg), k = q, v = q;
-    q.a = a.d_o; q.b = a.v; q.c = a.k; q.out = a.dq; q.so = a.scale; q.m_in = a.h0; q.m_transposed = 1;
-    k.a = a.v; k.b = a.d_o; k.c = a.q; k.out = a.dkk; k.ub = a.scale; k.m_in = a.dhT; k.m_transposed = 1;
-    v.a = a.k; v.b = a.q; v.c = a.d_o; v.out = a.dvv; v.ub = a.scale; v.m_in = a.dhT; v.m_out = a.dh0;
+    const Launch base = base_launch(a);
+    Pass q = make_pass(a.d_o, a.v, a.k, a.dq, false, a.scale, 1.f, a.h0, true, nullptr);
+    Pass k = make_pass(a.v, a.d_o, a.q, a.dkk, true, 1.f, a.scale, a.dhT, true, nullptr);
+    Pass v = make_pass(a.k, a.q, a.d_o, a.dvv, true, 1.f, a.scale, a.dhT, false, a.dh0);
     hipError_t e = hipSuccess;
-    if (seg < kWhole) {
-        // the forward states S (b = k, c = v) and their gradients G (b = q, c = do)
-        Pass s = q, g = v;
-        s.b = a.k; s.c = a.v; s.m_transposed = 0;
-        s.seg_states = q.seg_states = static_cast<float*>(a.workspace);
-        g.seg_states = k.seg_states = v.seg_states = s.seg_states + slots * a.H * a.dk * a.dv;
-        e = launch_pass<DT, DT, false, true>(s, slots, a.dk, a.dv, stream);
-        if (e == hipSuccess) e = launch_pass<DT, DT, true, true>(g, slots, a.dk, a.dv, stream);
-        if (e == hipSuccess) e = launch_scan(s, g, 2, a.dk * a.dv, stream);
+    if (base.seg_shift < WHOLE) {
+        // the forward states (b = k, c = v) and their gradients (b = q, c = do)
+        Launch L = base;
+        L.passes = 2;
+        L.pass[0] = make_pass(nullptr, a.k, a.v, nullptr, false, 1.f, 1.f, a.h0, false, nullptr);
+        L.pass[1] = v;
+        L.pass[1].exact = a.dh0 != nullptr;
+        L.pass[0].seg_states = q.seg_states = static_cast<float*>(a.workspace);
+        L.pass[1].seg_states = k.seg_states = v.seg_states =
+            static_cast<float*>(a.workspace) + int64_t(L.slots) * a.H * a.dk * a.dv;
+        e = launch_chunks<DT, DT, true>(L, a.dk, a.dv, stream);
+        if (e == hipSuccess) e = launch_scan(L, a.dk * a.dv, stream);
     }
-    if (e == hipSuccess) e = launch_pass<DT, DT, false, false>(q, slots, a.dv, a.dk, stream);
-    if (e == hipSuccess) e = launch_pass<DT, DT, true, false>(k, slots, a.dv, a.dk, stream);
-    if (e == hipSuccess) e = launch_pass<DT, DT, true, false>(v, slots, a.dk, a.dv, stream);
+    Launch L = base;
+    L.pass[0] = q; L.pass[1] = k; L.pass[2] = v;
+    L.passes = a.dk == a.dv ? 3 : 2;
+    if (e == hipSuccess) e = launch_chunks<DT, DT, false>(L, a.dv, a.dk, stream);
+    if (a.dk != a.dv) {
+        L.pass[0] = v;
+        L.passes = 1;
+        if (e == hipSuccess) e = launch_chunks<DT, DT, false>(L, a.dk, a.dv, stream);
+    }
     return e;
 }
 
 }  // namespace
 
-size_t linear_workspace_bytes(int32_t n_seqs, int64_t total, int32_t H, int32_t dk, int32_t dv, int32_t, bool backward) {
-    const int64_t seg = segment_tokens(n_seqs, total, H);
-    if (seg >= kWhole) return 0;
-    // packed batches may use one slot more per sequence than fixed-length ones
-    return static_cast<size_t>(segment_slots(n_seqs, total, seg, true)) * H * dk * dv * 4 * (backward ? 2 : 1);
+size_t linear_workspace_bytes(int32_t n_seqs, int64_t total, int32_t H, int32_t dk, int32_t dv,
+                              int32_t in_dtype, bool backward) {
+    // what a packed batch of these sizes needs, or fixed-length sequences: whichever is more
+    int64_t slots = 0;
+    for (const bool packed : {false, true}) {
+        const int shift = segment_shift(n_seqs, total, H, in_dtype, packed);
+        if (shift < WHOLE) slots = std::max(slots, segment_slots(n_seqs, total, shift, packed));
+    }
+    return static_cast<size_t>(slots) * H * dk * dv * 4 * (backward ? 2 : 1);
 }
 
 hipError_t launch_linear_fwd(const LinearArgs& a, hipStream_t stream) {
@@ -684,10 +727,9 @@ __global__ void __launch_bounds__(256) linear_decode_kernel(const void* __restri
                                                             const void* __restrict__ v, const float* __restrict__ g,
                                                             float* __restrict__ state, void* __restrict__ o,
                                                             int32_t H, float scale) {
-    typedef float f32x4_t __attribute__((ext_vector_type(4)));
     constexpr int CG = DV / 4, RG = 256 / CG, RPT = DK / RG;
     __shared__ float sq[DK], sk[DK];
-    __shared__ f32x4_t red[RG][CG];
+    __shared__ f32x4 red[RG][CG];
     const int64_t unit = blockIdx.x;
     const int t = threadIdx.x, cg = t % CG, rg = t / CG;
     float xq = 0.f, xk = 0.f;
@@ -698,18 +740,18 @@ __global__ void __launch_bounds__(256) linear_decode_kernel(const void* __restri
     const float4 vv = load4_as_f32<DT>(v, unit * DV + 4 * cg);
     const float gg = g[unit % H];
     float* S = state + unit * (DK * DV) + 4 * cg;
-    f32x4_t s[RPT];
+    f32x4 s[RPT];
 #pragma unroll
     for (int i = 0; i < RPT; ++i)
-        s[i] = __builtin_nontemporal_load(reinterpret_cast<const f32x4_t*>(S + (rg * RPT + i) * DV));
+        s[i] = __builtin_nontemporal_load(reinterpret_cast<const f32x4*>(S + (rg * RPT + i) * DV));
     if (t < DK) {
         sq[t] = xq;
         sk[t] = xk;
     }
     const float lam = expf(gg);
     __syncthreads();
-    f32x4_t acc = {0.f, 0.f, 0.f, 0.f};
-    const f32x4_t c = {vv.x, vv.y, vv.z, vv.w};
+    f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+    const f32x4 c = {vv.x, vv.y, vv.z, vv.w};
 #pragma unroll
     for (int i = 0; i < RPT; ++i) {
         const int r = rg * RPT + i;
@@ -719,12 +761,12 @@ __global__ void __launch_bounds__(256) linear_decode_kernel(const void* __restri
             s[i][e] = __builtin_fmaf(kr, c[e], lam * s[i][e]);
             acc[e] = __builtin_fmaf(qr, s[i][e], acc[e]);
         }
-        __builtin_nontemporal_store(s[i], reinterpret_cast<f32x4_t*>(S + r * DV));
+        __builtin_nontemporal_store(s[i], reinterpret_cast<f32x4*>(S + r * DV));
     }
     red[rg][cg] = acc;
     __syncthreads();
     if (rg == 0) {
-        f32x4_t sum = red[0][cg];
+        f32x4 sum = red[0][cg];
 #pragma unroll
         for (int r = 1; r < RG; ++r) sum += red[r][cg];
         store4_from_f32<ODT>(o, unit * DV + 4 * cg,
