@@ -380,6 +380,9 @@ int linear_sizes(int in_dtype, const int32_t* cu, int32_t B, int64_t T, int32_t 
         return KDA_ERR_INVALID_ARGUMENT;
     if (cu ? (B != 1) : (n_seqs != B)) return KDA_ERR_INVALID_ARGUMENT;
     if (!supported_d(dk) || !supported_d(dv)) return KDA_ERR_UNSUPPORTED;
+    // 64 token rows of all heads must stay within a 2 GiB buffer range (a token row of all heads:
+    // H * 512 bytes at most)
+    if (H > 32768) return KDA_ERR_UNSUPPORTED;
     // a grid of 256-lane workgroups (up to six per (sequence, head)) must stay within 2^32 lanes
     if (int64_t(n_seqs) * H > (int64_t(1) << 21)) return KDA_ERR_UNSUPPORTED;
     return KDA_OK;

@@ -128,6 +128,8 @@ def _expect(fn: str, name: str, t, shape, dtypes=None):
         return
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{fn}: {name} must be a torch.Tensor")
+    if t.shape == shape and (dtypes is None or t.dtype in dtypes) and t.is_contiguous():
+        return
     if len(t.shape) != len(shape) or any(w is not None and int(a) != int(w)
                                          for a, w in zip(t.shape, shape)):
         want = tuple("*" if w is None else int(w) for w in shape)
@@ -443,23 +445,36 @@ def kda_decode_commit(q, k, v, beta, g, state, accepted, stream=None):
 
 # ---- linear attention with one decay per head ---------------------------------------------------
 
-def _launch(fn: str, dev: torch.device, stream, call):
-    """Run call(stream pointer) with `dev` current and check its status."""
-    sp = _sptr(_torch_stream(stream, dev))
+def _launch_stream(stream, dev):
+    """(torch stream or None for the current one of `dev`, its raw pointer)."""
+    if stream is None:
+        return None, torch._C._cuda_getCurrentRawStream(dev.index)
+    ts = _torch_stream(stream, dev)
+    return ts, ts.cuda_stream
+
+
+def _launch(fn: str, dev: torch.device, call, *args):
+    """call(*args) with `dev` current; raises for a status other than KDA_OK."""
     if torch.cuda.current_device() == dev.index:
-        status = call(sp)
+        status = call(*args)
     else:
         with torch.cuda.device(dev):
-            status = call(sp)
-    _check(fn, status)
+            status = call(*args)
+    if status != KDA_OK:
+        raise KDAError(fn, status)
 
 
 def _alloc(ts, shape, dtype, dev):
-    """A new tensor on the launch stream `ts`."""
-    if ts == torch.cuda.current_stream(dev):
+    """A new tensor on the launch stream `ts` (None: the current one)."""
+    if ts is None:
         return torch.empty(shape, dtype=dtype, device=dev)
     with torch.cuda.stream(ts):
         return torch.empty(shape, dtype=dtype, device=dev)
+
+
+def _addr(t: Optional[torch.Tensor]):
+    """Address of a tensor that has passed _expect."""
+    return None if t is None else t.data_ptr()
 
 
 def kda_linear_chunk_workspace_size(n_seqs: int, total_tokens: int, H: int, dk: int, dv: int,
@@ -526,17 +541,15 @@ def kda_linear_chunk_fwd(q, k, v, g, initial_state=None, final_state=None, cu_se
     B, T, N, H, dk, dv, dev = _check_linear(
         fn, q, k, v, g, cu_seqlens, workspace,
         dict(initial_state=initial_state, final_state=final_state), {}, dict(o=o))
-    ts = _torch_stream(stream, dev)
+    ts, sp = _launch_stream(stream, dev)
     if o is None:
         o = _alloc(ts, (B, T, H, dv), o_dtype or q.dtype, dev)
     if final_state is None and output_final_state:
         final_state = _alloc(ts, (N, H, dk, dv), torch.float32, dev)
     workspace, ws_bytes = _linear_workspace(ts, workspace, N, B * T, H, dk, dv, q.dtype, False, dev)
-    lib = load_library()
-    _launch(fn, dev, ts, lambda sp: lib.kda_linear_chunk_fwd(
-        _ptr(q), _ptr(k), _ptr(v), _dt(q), _ptr(g), _ptr(initial_state), _ptr(final_state),
-        _ptr(cu_seqlens), _ptr(o), _dt(o), B, T, N, H, dk, dv, float(scale), _ptr(workspace),
-        ws_bytes, sp))
+    _launch(fn, dev, load_library().kda_linear_chunk_fwd, _addr(q), _addr(k), _addr(v), _dt(q),
+            _addr(g), _addr(initial_state), _addr(final_state), _addr(cu_seqlens), _addr(o), _dt(o),
+            B, T, N, H, dk, dv, float(scale), _addr(workspace), ws_bytes, sp)
     return o, final_state
 
 
@@ -555,7 +568,7 @@ def kda_linear_chunk_bwd(q, k, v, g, do, initial_state=None, d_final_state=None,
         fn, q, k, v, g, cu_seqlens, workspace,
         dict(initial_state=initial_state, d_final_state=d_final_state,
              d_initial_state=d_initial_state), dict(dq=dq, dk=dk), dict(do=do, dv=dv))
-    ts = _torch_stream(stream, dev)
+    ts, sp = _launch_stream(stream, dev)
     if dq is None:
         dq = _alloc(ts, q.shape, q.dtype, dev)
     if dk is None:
@@ -567,11 +580,10 @@ def kda_linear_chunk_bwd(q, k, v, g, do, initial_state=None, d_final_state=None,
     if d_initial_state is None and output_d_initial_state:
         d_initial_state = _alloc(ts, (N, H, d_k, d_v), torch.float32, dev)
     workspace, ws_bytes = _linear_workspace(ts, workspace, N, B * T, H, d_k, d_v, q.dtype, True, dev)
-    lib = load_library()
-    _launch(fn, dev, ts, lambda sp: lib.kda_linear_chunk_bwd(
-        _ptr(q), _ptr(k), _ptr(v), _dt(q), _ptr(g), _ptr(initial_state), _ptr(cu_seqlens),
-        _ptr(do), _ptr(d_final_state), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(d_initial_state), B, T, N,
-        H, d_k, d_v, float(scale), _ptr(workspace), ws_bytes, sp))
+    _launch(fn, dev, load_library().kda_linear_chunk_bwd, _addr(q), _addr(k), _addr(v), _dt(q),
+            _addr(g), _addr(initial_state), _addr(cu_seqlens), _addr(do), _addr(d_final_state),
+            _addr(dq), _addr(dk), _addr(dv), _addr(d_initial_state), B, T, N, H, d_k, d_v,
+            float(scale), _addr(workspace), ws_bytes, sp)
     return dq, dk, dv, d_initial_state
 
 
@@ -594,13 +606,11 @@ def kda_linear_decode_step(q, k, v, g, state, o=None, o_dtype=None, scale: float
     _expect(fn, "state", state, (N, H, dk, dv), (torch.float32,))
     _expect(fn, "o", o, (N, H, dv), _FLOATS)
     dev = _one_device(fn, q=q, k=k, v=v, g=g, state=state, o=o)
-    ts = _torch_stream(stream, dev)
+    ts, sp = _launch_stream(stream, dev)
     if o is None:
         o = _alloc(ts, (N, H, dv), o_dtype or q.dtype, dev)
-    lib = load_library()
-    _launch(fn, dev, ts, lambda sp: lib.kda_linear_decode_step(
-        _ptr(q), _ptr(k), _ptr(v), _dt(q), _ptr(g), _ptr(state), _ptr(o), _dt(o), N, H, dk, dv,
-        float(scale), sp))
+    _launch(fn, dev, load_library().kda_linear_decode_step, _addr(q), _addr(k), _addr(v), _dt(q),
+            _addr(g), _addr(state), _addr(o), _dt(o), N, H, dk, dv, float(scale), sp)
     return o
 
 
@@ -638,10 +648,9 @@ def kda_state_store(states, codes, scales, slots=None, stream=None):
     if not isinstance(states, torch.Tensor) or states.dim() != 4:
         raise ValueError(f"{fn}: states must be a [N, H, dk, dv] tensor")
     N, n_slots, H, dk, dv, group, dev = _check_cache(fn, codes, scales, slots, states)
-    lib = load_library()
-    _launch(fn, dev, stream, lambda sp: lib.kda_state_store(
-        _ptr(states), _ptr(slots), _ptr(codes), _CODES[codes.dtype], _ptr(scales), N, n_slots, H,
-        dk, dv, group, sp))
+    _, sp = _launch_stream(stream, dev)
+    _launch(fn, dev, load_library().kda_state_store, _addr(states), _addr(slots), _addr(codes),
+            _CODES[codes.dtype], _addr(scales), N, n_slots, H, dk, dv, group, sp)
     return codes, scales
 
 
@@ -650,11 +659,9 @@ def kda_state_load(codes, scales, slots=None, states=None, stream=None):
     slot lies outside the cache (-1: no cached prefix).  Returns states [N, H, dk, dv] fp32."""
     fn = "kda_state_load"
     N, n_slots, H, dk, dv, group, dev = _check_cache(fn, codes, scales, slots, states)
-    ts = _torch_stream(stream, dev)
+    ts, sp = _launch_stream(stream, dev)
     if states is None:
         states = _alloc(ts, (N, H, dk, dv), torch.float32, dev)
-    lib = load_library()
-    _launch(fn, dev, ts, lambda sp: lib.kda_state_load(
-        _ptr(codes), _CODES[codes.dtype], _ptr(scales), _ptr(slots), _ptr(states), N, n_slots, H,
-        dk, dv, group, sp))
+    _launch(fn, dev, load_library().kda_state_load, _addr(codes), _CODES[codes.dtype],
+            _addr(scales), _addr(slots), _addr(states), N, n_slots, H, dk, dv, group, sp)
     return states
