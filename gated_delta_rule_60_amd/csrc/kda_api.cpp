@@ -411,8 +411,8 @@ int state_cache_check(const float* states, const int32_t* slots, const void* cod
     if (!states || !codes || !scales) return KDA_ERR_INVALID_ARGUMENT;
     if (!aligned16({states, codes}) || !aligned4({scales, slots})) return KDA_ERR_UNSUPPORTED;
     const int64_t per_seq = int64_t(H) * dk * dv;
-    // a grid of 256-lane workgroups must stay within 2^32 lanes (8192 elements a workgroup)
-    if ((per_seq + 8191) / 8192 * N > (int64_t(1) << 24) - 1) return KDA_ERR_UNSUPPORTED;
+    // a grid of 256-lane workgroups must stay within 2^32 lanes (4096 elements a workgroup)
+    if (per_seq / 4096 * N > (int64_t(1) << 24) - 1) return KDA_ERR_UNSUPPORTED;
     const Range r_st = range(states, N * per_seq * 4), r_sl = range(slots, slots ? int64_t(N) * 4 : 0);
     const Range r_c = range(codes, n_slots * per_seq), r_sc = range(scales, n_slots * (per_seq / group) * 4);
     if (store ? !disjoint({r_c, r_sc}, {r_st, r_sl}) : !disjoint({r_st}, {r_c, r_sc, r_sl}))

@@ -5,15 +5,16 @@
 // rounded to nearest even.  The quotient must not be rounded twice (an fp32 quotient next to the
 // border of two codes could fall on it), which costs a few VALU operations only:
 //   integers: c = rint(x * (1/scale)) is off by at most one; e = x - c scale is exact in fp32 (both
-//     are multiples of the smaller ulp, and |e| <= scale), so comparing |e| with scale / 2 decides.
-//   e4m3: q = fl(x / scale) and the exact sign of x - q scale; where q is inexact and its last bit
-//     is even, one ulp towards the true quotient makes the last bit odd, which puts q on the right
-//     side of every border of the coarser format (borders have zeros there).
+//     are multiples of the smaller ulp, and |e| <= scale), so comparing 2 |e| with scale decides.
+//   e4m3: q within one ulp of x / scale, and the exact sign of x - q scale; where q is inexact and its
+//     last bit even, one ulp towards the true quotient makes the last bit odd, and an odd q lies on the
+//     right side of every border of the coarser format (borders have zeros there).
 //
 // Both kernels stream: 5 + 4 / GROUP bytes per state element and no reuse.  A lane owns four
 // neighbouring channels (16-byte accesses to fp32, 4-byte ones to the codes), GROUP / 4
-// neighbouring lanes a group; the maximum crosses them by shuffles.  One workgroup handles 8
-// consecutive 256-lane passes (32 KB of fp32), loads first.
+// neighbouring lanes a group; the maximum crosses them by shuffles.  One workgroup handles 4096
+// elements, which divides every sequence's states, in four passes, loads first.  The fp32 states are
+// streamed past the caches (each is touched once).
 #include "kda_common.hpp"
 #include "kda_internal.hpp"
 
@@ -22,18 +23,26 @@ namespace {
 
 typedef float f32x4_t __attribute__((ext_vector_type(4)));
 
-constexpr int PASSES = 8;                      // 1024-element passes per workgroup
+constexpr int PASSES = 4;                      // of 1024 elements: a sequence has a multiple of 4096
 
 // The four codes of x under `scale` (finite, > 0), one byte each.
 template <int CODE>
-__device__ __forceinline__ uint32_t encode4(float4 x, float scale) {
-    const float xs[4] = {x.x, x.y, x.z, x.w};
+__device__ __forceinline__ uint32_t encode4(f32x4_t x, float scale) {
+    constexpr float most = CODE == KDA_CODE_I8 ? 127.f : 448.f;
+    // a scale whose reciprocal might overflow: scaled up with x, exactly
+    const float lift = scale < 0x1p-100f ? 0x1p64f : 1.f;
+    scale *= lift;
+    x *= lift;
+    const float inv = __builtin_amdgcn_rcpf(scale);                // within one ulp
+    float q[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) q[i] = x[i] * inv;                 // within two ulps
     if constexpr (CODE == KDA_CODE_I8) {
         uint32_t out = 0;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const float c = __builtin_rintf(__builtin_amdgcn_fmed3f(xs[i] / scale, -127.f, 127.f));
-            const float e = __builtin_fmaf(-c, scale, xs[i]);
+            const float c = __builtin_rintf(__builtin_amdgcn_fmed3f(q[i], -most, most));
+            const float e = __builtin_fmaf(-c, scale, x[i]);
             const float d2 = 2.f * __builtin_fabsf(e);
             int ci = static_cast<int>(c);
             if (d2 > scale || (d2 == scale && (ci & 1))) ci += e > 0.f ? 1 : -1;
@@ -42,13 +51,13 @@ __device__ __forceinline__ uint32_t encode4(float4 x, float scale) {
         }
         return out;
     } else {
-        float q[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const float y = __builtin_amdgcn_fmed3f(xs[i] / scale, -448.f, 448.f);
-            const float r = __builtin_fmaf(-y, scale, xs[i]);       // sign of the quotient's rest
+            float y = __builtin_fmaf(__builtin_fmaf(-q[i], scale, x[i]), inv, q[i]);        // within one ulp
+            y = __builtin_amdgcn_fmed3f(y, -most, most);
+            const float r = __builtin_fmaf(-y, scale, x[i]);        // sign of the quotient's rest
             uint32_t u = __float_as_uint(y);
-            if (r != 0.f && !(u & 1u) && __builtin_fabsf(y) < 448.f) u = ((r > 0.f) == (y > 0.f)) ? u + 1u : u - 1u;
+            if (r != 0.f && !(u & 1u) && __builtin_fabsf(y) < most) u = ((r > 0.f) == (y > 0.f)) ? u + 1u : u - 1u;
             // far below half the smallest code (2^-10): zero
             q[i] = __builtin_fabsf(y) < 0x1p-20f ? 0.f : __uint_as_float(u);
         }
@@ -69,9 +78,8 @@ __device__ __forceinline__ float4 decode4(uint32_t w) {
     }
 }
 
-// One workgroup: PASSES * 1024 consecutive elements of one sequence's states (or what is left).
 template <int CODE, int GROUP>
-__global__ void __launch_bounds__(256) store_kernel(const float* __restrict__ states, const int32_t* __restrict__ slots,
+__global__ void __launch_bounds__(256, 8) store_kernel(const float* __restrict__ states, const int32_t* __restrict__ slots,
                                                     uint8_t* __restrict__ codes, float* __restrict__ scales,
                                                     int32_t N, int32_t n_slots, int64_t per_seq, int32_t blocks_per_seq) {
     const int32_t n = blockIdx.x / blocks_per_seq, part = blockIdx.x % blocks_per_seq;
@@ -87,23 +95,25 @@ __global__ void __launch_bounds__(256) store_kernel(const float* __restrict__ st
     const float* src = states + n * per_seq;
     uint8_t* dst = codes + slot * per_seq;
     float* sc = scales + slot * (per_seq / GROUP);
+    f32x4_t x[PASSES];
+#pragma unroll
+    for (int p = 0; p < PASSES; ++p)
+        x[p] = __builtin_nontemporal_load(reinterpret_cast<const f32x4_t*>(src + e0 + p * 1024));
+#pragma unroll
     for (int p = 0; p < PASSES; ++p) {
         const int64_t e = e0 + p * 1024;
-        if (e >= per_seq) break;     // whole wavefronts: per_seq is a multiple of 4096
-        const f32x4_t x = *reinterpret_cast<const f32x4_t*>(src + e);
-        float a = __builtin_fmaxf(__builtin_fmaxf(__builtin_fabsf(x[0]), __builtin_fabsf(x[1])),
-                                  __builtin_fmaxf(__builtin_fabsf(x[2]), __builtin_fabsf(x[3])));
+        float a = __builtin_fmaxf(__builtin_fmaxf(__builtin_fabsf(x[p][0]), __builtin_fabsf(x[p][1])),
+                                  __builtin_fmaxf(__builtin_fabsf(x[p][2]), __builtin_fabsf(x[p][3])));
         // 0 while all values are finite, NaN from the first infinity or NaN on
-        float bad = (x[0] - x[0]) + (x[1] - x[1]) + (x[2] - x[2]) + (x[3] - x[3]);
+        float bad = (x[p][0] - x[p][0]) + (x[p][1] - x[p][1]) + (x[p][2] - x[p][2]) + (x[p][3] - x[p][3]);
 #pragma unroll
         for (int off = 1; off < GROUP / 4; off <<= 1) {
             a = __builtin_fmaxf(a, __shfl_xor(a, off, 64));
             bad += __shfl_xor(bad, off, 64);
         }
-        const bool ok = bad == 0.f;
-        const float scale = ok ? a * inv_most : __uint_as_float(0x7fc00000u);
+        const float scale = bad == 0.f ? a * inv_most : __uint_as_float(0x7fc00000u);
         uint32_t w = 0;
-        if (scale > 0.f) w = encode4<CODE>(make_float4(x[0], x[1], x[2], x[3]), scale);
+        if (scale > 0.f) w = encode4<CODE>(x[p], scale);
         *reinterpret_cast<uint32_t*>(dst + e) = w;
         if (e % GROUP == 0) sc[e / GROUP] = scale;
     }
@@ -120,16 +130,24 @@ __global__ void __launch_bounds__(256) load_kernel(const uint8_t* __restrict__ c
     const uint8_t* src = codes + (have ? slot : 0) * per_seq;
     const float* sc = scales + (have ? slot : 0) * (per_seq / GROUP);
     float* dst = states + n * per_seq;
+    uint32_t w[PASSES];
+    float s[PASSES];
+#pragma unroll
     for (int p = 0; p < PASSES; ++p) {
         const int64_t e = e0 + p * 1024;
-        if (e >= per_seq) break;
-        f32x4_t y = {0.f, 0.f, 0.f, 0.f};
+        w[p] = 0;
+        s[p] = 0.f;
         if (have) {
-            const float4 c = decode4<CODE>(*reinterpret_cast<const uint32_t*>(src + e));
-            const float s = sc[e / GROUP];
-            y = f32x4_t{c.x * s, c.y * s, c.z * s, c.w * s};
+            w[p] = *reinterpret_cast<const uint32_t*>(src + e);
+            s[p] = sc[e / GROUP];
         }
-        *reinterpret_cast<f32x4_t*>(dst + e) = y;
+    }
+#pragma unroll
+    for (int p = 0; p < PASSES; ++p) {
+        const int64_t e = e0 + p * 1024;
+        const float4 c = decode4<CODE>(w[p]);
+        const f32x4_t y = {c.x * s[p], c.y * s[p], c.z * s[p], c.w * s[p]};
+        __builtin_nontemporal_store(y, reinterpret_cast<f32x4_t*>(dst + e));
     }
 }
 
@@ -137,7 +155,7 @@ __global__ void __launch_bounds__(256) load_kernel(const uint8_t* __restrict__ c
 
 hipError_t launch_state_store(const StateCacheArgs& a, const float* states, hipStream_t stream) {
     const int64_t per_seq = int64_t(a.H) * a.dk * a.dv;
-    const int32_t bps = static_cast<int32_t>((per_seq + PASSES * 1024 - 1) / (PASSES * 1024));
+    const int32_t bps = static_cast<int32_t>(per_seq / (PASSES * 1024));
     const dim3 grid(static_cast<unsigned>(int64_t(a.N) * bps));
     auto go = [&](auto kernel) {
         hipLaunchKernelGGL(kernel, grid, dim3(256), 0, stream, states, a.slots, static_cast<uint8_t*>(a.codes), a.scales,
@@ -156,7 +174,7 @@ hipError_t launch_state_store(const StateCacheArgs& a, const float* states, hipS
 
 hipError_t launch_state_load(const StateCacheArgs& a, float* states, hipStream_t stream) {
     const int64_t per_seq = int64_t(a.H) * a.dk * a.dv;
-    const int32_t bps = static_cast<int32_t>((per_seq + PASSES * 1024 - 1) / (PASSES * 1024));
+    const int32_t bps = static_cast<int32_t>(per_seq / (PASSES * 1024));
     const dim3 grid(static_cast<unsigned>(int64_t(a.N) * bps));
     auto go = [&](auto kernel) {
         hipLaunchKernelGGL(kernel, grid, dim3(256), 0, stream, static_cast<const uint8_t*>(a.codes), a.scales, a.slots,
