@@ -221,7 +221,9 @@ struct ChunkLds {
 //   16-bit inputs: M and the scores are read as two bf16 terms (2^-16); the decayed c as three (exact)
 //   where M ends in a state that is handed out in fp32, as two where it only feeds 16-bit outputs.
 //   fp32 inputs: 16x16x4 fp32 MFMAs throughout.
-// Sixteen waves fill a CU (two workgroups; 128 registers and 68 KB of LDS each), and one workgroup's
+//   16-bit outputs leave through LDS as whole rows past the caches (4 x 4096 x 16 heads: 67 us for the
+//   pass, 73 us with each wave's 32-byte pieces stored as they are).
+// Sixteen waves fill a CU (two workgroups; 128 registers and 69 KB of LDS each), and one workgroup's
 // transfers run under the other's products.
 // STATE_ONLY: just M from zero, the segment's own contribution.
 template <int DT, int ODT, int DA, int DC, bool BACK, bool STATE_ONLY>
@@ -234,6 +236,8 @@ __device__ __forceinline__ void chunk_pass(const Launch& L, const Pass& p, int32
     constexpr int TOK = Lds::TOK, WAVES = DC / 16;
     constexpr int IT = TOK / 16, MT = DA / 16;       // token tiles, state row tiles
     constexpr int KK = DA / 32, JG = TOK / 32;       // 16 bits: contraction steps over channels, tokens
+    constexpr int OS = ODT == KDA_BF16 ? 2 : 4;
+    constexpr bool STAGED = BF && OS == 2 && !STATE_ONLY;
 
     Where w;
     if (!locate(L, slot, w)) return;
@@ -244,14 +248,21 @@ __device__ __forceinline__ void chunk_pass(const Launch& L, const Pass& p, int32
     const int n_chunks = static_cast<int>((len + TOK - 1) / TOK);
     const int64_t unit = static_cast<int64_t>(w.n) * L.H + h;
 
-    auto load = [&](int c) {
+    auto load_ab = [&](int c) {
         const int64_t off = static_cast<int64_t>(BACK ? n_chunks - 1 - c : c) * TOK;
         const int n = static_cast<int>(len - off < TOK ? len - off : TOK);
         fetch_tile<TA, TOK, WAVES>(lds.b, p.b, w.lo + off, n, L.H, h, wave, lane);
-        fetch_tile<TC, TOK, WAVES>(lds.c, p.c, w.lo + off, n, L.H, h, wave, lane);
         if constexpr (!STATE_ONLY) fetch_tile<TA, TOK, WAVES>(lds.a, p.a, w.lo + off, n, L.H, h, wave, lane);
     };
-    if (n_chunks > 0) load(0);
+    auto load_c = [&](int c) {
+        const int64_t off = static_cast<int64_t>(BACK ? n_chunks - 1 - c : c) * TOK;
+        const int n = static_cast<int>(len - off < TOK ? len - off : TOK);
+        fetch_tile<TC, TOK, WAVES>(lds.c, p.c, w.lo + off, n, L.H, h, wave, lane);
+    };
+    if (n_chunks > 0) {
+        load_ab(0);
+        load_c(0);
+    }
 
     // ---- the state: tile mt, register r of lane (l16, q) holds row row(mt) + r, column 16 wave + l16
     auto row = [&](int mt) { return BF ? 32 * (mt >> 1) + 8 * q + 4 * (mt & 1) : 16 * mt + 4 * q; };
@@ -461,18 +472,27 @@ __device__ __forceinline__ void chunk_pass(const Launch& L, const Pass& p, int32
                     for (int r = 0; r < 4; ++r) O[it] = mfma_f32(__uint_as_float(vf[jt][r]), P[r], O[it]);
                 }
             }
-            // ---- out: lane l16 holds token 16 it + l16, four neighbouring columns
-            constexpr int OS = ODT == KDA_BF16 ? 2 : 4;
-            const uint32_t orow = static_cast<uint32_t>(L.H) * DC * OS;
-            const __amdgpu_buffer_rsrc_t ro = make_rsrc_u(static_cast<uint8_t*>(p.out) + (tok0 * L.H + h) * DC * OS,
-                                                          (n - 1) * orow + DC * OS);
+            // ---- out, through c's tile (which all waves have read by now): lane l16 holds token 16 it + l16,
+            // four neighbouring columns
+            if constexpr (STAGED) {
+                int ll = l16;
+                asm volatile("" : "+v"(ll));
 #pragma unroll
-            for (int it = 0; it < IT; ++it) {
-                const uint32_t at = (16 * it + l16) * orow + (16 * wave + 4 * q) * OS;
-                if constexpr (ODT == KDA_BF16)
-                    __builtin_amdgcn_raw_buffer_store_b64(u32x2{pack_bf16(O[it][0], O[it][1]), pack_bf16(O[it][2], O[it][3])},
-                                                          ro, at, 0, 0);
-                else __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, O[it]), ro, at, 0, 0);
+                for (int it = 0; it < IT; ++it)
+                    lds_put(lds.c, TC::at(16 * it + ll, 2 * wave + (q >> 1)) + 8 * (q & 1),
+                            u32x2{pack_bf16(O[it][0], O[it][1]), pack_bf16(O[it][2], O[it][3])});
+            } else {
+                const uint32_t orow = static_cast<uint32_t>(L.H) * DC * OS;
+                const __amdgpu_buffer_rsrc_t ro = make_rsrc_u(static_cast<uint8_t*>(p.out) + (tok0 * L.H + h) * DC * OS,
+                                                              (n - 1) * orow + DC * OS);
+#pragma unroll
+                for (int it = 0; it < IT; ++it) {
+                    const uint32_t at = (16 * it + l16) * orow + (16 * wave + 4 * q) * OS;
+                    if constexpr (ODT == KDA_BF16)
+                        __builtin_amdgcn_raw_buffer_store_b64(u32x2{pack_bf16(O[it][0], O[it][1]), pack_bf16(O[it][2], O[it][3])},
+                                                              ro, at, 0, 0);
+                    else __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, O[it]), ro, at, 0, 0);
+                }
             }
         }
         // ---- update
@@ -522,10 +542,22 @@ __device__ __forceinline__ void chunk_pass(const Launch& L, const Pass& p, int32
                 }
             }
         }
-        if (c + 1 < n_chunks) {
-            lds_barrier();                           // the tiles have been read
-            load(c + 1);
+        lds_barrier();                               // the tiles have been read, the output is there
+        if (c + 1 < n_chunks) load_ab(c + 1);
+        if constexpr (STAGED) {
+            const uint32_t orow = static_cast<uint32_t>(L.H) * DC * OS;
+            const __amdgpu_buffer_rsrc_t ro = make_rsrc_u(static_cast<uint8_t*>(p.out) + (tok0 * L.H + h) * DC * OS,
+                                                          (n - 1) * orow + DC * OS);
+            int tt = t;                              // formed anew in each chunk: no registers over the loop
+            asm volatile("" : "+v"(tt));
+#pragma unroll
+            for (int i = 0; i < TOK * TC::UPR / (64 * WAVES); ++i) {
+                const int u = tt + 64 * WAVES * i, r = u / TC::UPR, un = u % TC::UPR;
+                __builtin_amdgcn_raw_buffer_store_b128(lds_get<u32x4>(lds.c, TC::at(r, un)), ro, r * orow + un * 16, 0, CP_NT);
+            }
+            lds_barrier();                           // the output has been read
         }
+        if (c + 1 < n_chunks) load_c(c + 1);
     }
 
     float* dst = nullptr;
