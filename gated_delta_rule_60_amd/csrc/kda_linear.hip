@@ -271,7 +271,7 @@ __device__ __forceinline__ void chunk_pass(const Launch& L, const Pass& p, int32
     {
         const float* src = nullptr;                  // none: an empty range, which reads as zeros
         if constexpr (!STATE_ONLY) {
-            if (p.seg_states) src = p.seg_states + (static_cast<int64_t>(slot) * L.H + h) * (DA * DC);
+            if (w.s != (BACK ? w.n_seg - 1 : 0)) src = p.seg_states + (static_cast<int64_t>(slot) * L.H + h) * (DA * DC);
             else if (p.m_in) src = p.m_in + unit * (DA * DC);
         }
         const __amdgpu_buffer_rsrc_t rs = make_rsrc_u(src, src ? DA * DC * 4 : 0);
@@ -589,8 +589,9 @@ __global__ void __launch_bounds__(DC * 4, DA > DC ? 2 : 4) linear_chunk_kernel(L
     else chunk_pass<DT, ODT, DA, DC, false, STATE_ONLY>(L, p, slot, h, lds);
 }
 
-// Segment states: from each segment's own contribution to the state it starts from, in place.
-// Grid (sequence * H + head, element blocks of 1024, pass); each lane carries four elements along.
+// Segment states: from each segment's own contribution to the state it starts from, in place (the first
+// segment, in the pass's direction, starts from the initial state itself).  Grid (sequence * H + head,
+// element blocks of 1024, pass); each lane carries four elements along, eight segments' loads at a time.
 __global__ void __launch_bounds__(256) linear_scan_kernel(Launch L, int32_t elems) {
     const Pass& p = L.pass[blockIdx.z];
     const int32_t n = blockIdx.x / L.H, h = blockIdx.x % L.H;
@@ -599,26 +600,33 @@ __global__ void __launch_bounds__(256) linear_scan_kernel(Launch L, int32_t elem
     seq_range(L, n, lo, hi);
     const int64_t len = hi - lo;
     const int32_t n_seg = segments(L, len);
+    if (n_seg == 1) return;
     const int32_t first = L.cu ? first_slot(L, n) : n * n_seg;
-    const double g = len > 0 ? static_cast<double>(L.g[h]) : 0.0;
+    const double g = static_cast<double>(L.g[h]);
     f32x4 x = zero4();
     if (p.m_in) x = *reinterpret_cast<const f32x4*>(p.m_in + (static_cast<int64_t>(n) * L.H + h) * elems + e);
     float* at = p.seg_states + (static_cast<int64_t>(first) * L.H + h) * elems + e;
     const int64_t step = static_cast<int64_t>(L.H) * elems;
     // decay over a segment as hi + lo: its rounding would act the same way segment after segment
     const int64_t part = len - (static_cast<int64_t>(n_seg - 1) << L.seg_shift);
-    const double full_d = n_seg > 1 ? exp(static_cast<double>(int64_t(1) << L.seg_shift) * g) : 1.0;
-    const double part_d = part > 0 ? exp(static_cast<double>(part) * g) : 1.0;
-    for (int32_t i = 0; i < n_seg; ++i) {
-        const int32_t s = p.back ? n_seg - 1 - i : i;
-        f32x4* slot = reinterpret_cast<f32x4*>(at + s * step);
-        f32x4 own = zero4();
-        if (i < n_seg - 1) own = *slot;
-        *slot = x;
-        const double l = s == n_seg - 1 ? part_d : full_d;
-        const float l_hi = static_cast<float>(l), l_lo = static_cast<float>(l - static_cast<double>(l_hi));
+    const double full = exp(static_cast<double>(int64_t(1) << L.seg_shift) * g), last = exp(static_cast<double>(part) * g);
+    auto slot = [&](int32_t i) { return reinterpret_cast<f32x4*>(at + (p.back ? n_seg - 1 - i : i) * step); };
+    f32x4 ahead = *slot(0);                       // read before the batch before it writes its place
+    for (int32_t i0 = 0; i0 < n_seg - 1; i0 += 8) {
+        f32x4 own[9];
+        own[0] = ahead;
 #pragma unroll
-        for (int r = 0; r < 4; ++r) x[r] = __builtin_fmaf(x[r], l_hi, __builtin_fmaf(x[r], l_lo, own[r]));
+        for (int32_t j = 1; j < 9; ++j) own[j] = i0 + j < n_seg - 1 ? *slot(i0 + j) : zero4();
+        ahead = own[8];
+#pragma unroll
+        for (int32_t j = 0; j < 8; ++j) {
+            if (i0 + j >= n_seg - 1) break;
+            const double l = p.back && i0 + j == 0 ? last : full;     // only the last segment may be shorter
+            const float l_hi = static_cast<float>(l), l_lo = static_cast<float>(l - static_cast<double>(l_hi));
+#pragma unroll
+            for (int r = 0; r < 4; ++r) x[r] = __builtin_fmaf(x[r], l_hi, __builtin_fmaf(x[r], l_lo, own[j][r]));
+            *slot(i0 + j + 1) = x;                // segment i's end is what segment i + 1 starts from
+        }
     }
 }
 

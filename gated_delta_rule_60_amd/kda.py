@@ -455,13 +455,23 @@ def _launch_stream(stream, dev):
 
 def _launch(fn: str, dev: torch.device, call, *args):
     """call(*args) with `dev` current; raises for a status other than KDA_OK."""
-    if torch.cuda.current_device() == dev.index:
+    if torch._C._cuda_getDevice() == dev.index:
         status = call(*args)
     else:
         with torch.cuda.device(dev):
             status = call(*args)
     if status != KDA_OK:
         raise KDAError(fn, status)
+
+
+def _fit(dev, *specs) -> bool:
+    """Whether every (tensor or None, shape, dtype) of `specs` is as stated, contiguous and on `dev`:
+    the quick form of the checks that _expect and _one_device make (and word) one by one."""
+    for t, shape, dtype in specs:
+        if t is not None and not (t.shape == shape and t.dtype is dtype and t.device == dev and
+                                  t.is_contiguous()):
+            return False
+    return dev.type == "cuda"
 
 
 def _alloc(ts, shape, dtype, dev):
@@ -598,14 +608,18 @@ def kda_linear_decode_step(q, k, v, g, state, o=None, o_dtype=None, scale: float
         raise ValueError(f"{fn}: v must be a [N, H, dv] tensor")
     N, H, dk = q.shape
     dv = v.shape[-1]
-    _expect(fn, "q", q, (N, H, dk), _FLOATS)
-    _expect(fn, "k", k, (N, H, dk), _FLOATS)
-    _expect(fn, "v", v, (N, H, dv), _FLOATS)
-    _same_dtype(fn, q=q, k=k, v=v)
-    _expect(fn, "g", g, (H,), (torch.float32,))
-    _expect(fn, "state", state, (N, H, dk, dv), (torch.float32,))
-    _expect(fn, "o", o, (N, H, dv), _FLOATS)
-    dev = _one_device(fn, q=q, k=k, v=v, g=g, state=state, o=o)
+    dev, dt = q.device, q.dtype
+    if o is not None or dt not in _FLOATS or not _fit(
+            dev, (q, (N, H, dk), dt), (k, (N, H, dk), dt), (v, (N, H, dv), dt), (g, (H,), torch.float32),
+            (state, (N, H, dk, dv), torch.float32)):
+        _expect(fn, "q", q, (N, H, dk), _FLOATS)
+        _expect(fn, "k", k, (N, H, dk), _FLOATS)
+        _expect(fn, "v", v, (N, H, dv), _FLOATS)
+        _same_dtype(fn, q=q, k=k, v=v)
+        _expect(fn, "g", g, (H,), (torch.float32,))
+        _expect(fn, "state", state, (N, H, dk, dv), (torch.float32,))
+        _expect(fn, "o", o, (N, H, dv), _FLOATS)
+        _one_device(fn, q=q, k=k, v=v, g=g, state=state, o=o)
     ts, sp = _launch_stream(stream, dev)
     if o is None:
         o = _alloc(ts, (N, H, dv), o_dtype or q.dtype, dev)
@@ -626,6 +640,14 @@ def _check_cache(fn, codes, scales, slots, states):
     if not isinstance(codes, torch.Tensor) or codes.dim() != 4:
         raise ValueError(f"{fn}: codes must be a [n_slots, H, dk, dv] tensor")
     n_slots, H, dk, dv = codes.shape
+    dev = codes.device
+    groups = scales.shape[-1] if isinstance(scales, torch.Tensor) and scales.dim() == 4 else 0
+    if slots is not None and codes.dtype in _CODES and groups > 0 and dv % groups == 0 and \
+            isinstance(slots, torch.Tensor) and slots.dim() == 1:
+        N = slots.shape[0]
+        if _fit(dev, (codes, (n_slots, H, dk, dv), codes.dtype), (slots, (N,), torch.int32),
+                (scales, (n_slots, H, dk, groups), torch.float32), (states, (N, H, dk, dv), torch.float32)):
+            return N, n_slots, H, dk, dv, dv // groups, dev
     _expect(fn, "codes", codes, (n_slots, H, dk, dv), tuple(_CODES))
     if not isinstance(scales, torch.Tensor):
         raise TypeError(f"{fn}: scales must be a torch.Tensor")
