@@ -10,6 +10,7 @@
 
 #include "../../include/kda.h"
 #include "kda_internal.hpp"
+#include "kda_linear.hpp"
 
 namespace {
 
@@ -392,8 +393,8 @@ int linear_sizes(int in_dtype, const int32_t* cu, int32_t B, int64_t T, int32_t 
 int linear_debug(const float* g, const int32_t* cu, int32_t n_seqs, int64_t ntok, int32_t H, void* stream) {
     if (!kda::debug_validation_enabled() || ntok == 0) return KDA_OK;
     bool ok = true;
-    if (kda::debug_validate(g, KDA_F32, H, cu, n_seqs, ntok, static_cast<hipStream_t>(stream), &ok,
-                            -std::numeric_limits<float>::infinity()) != hipSuccess)
+    if (kda::debug_validate_from(-std::numeric_limits<float>::infinity(), g, KDA_F32, H, cu, n_seqs, ntok,
+                                 static_cast<hipStream_t>(stream), &ok) != hipSuccess)
         return KDA_ERR_HIP;
     return ok ? KDA_OK : KDA_ERR_INVALID_ARGUMENT;
 }

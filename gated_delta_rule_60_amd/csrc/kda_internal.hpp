@@ -26,12 +26,11 @@ hipError_t launch_decode_commit(const void* q, const void* k, const void* v, con
                                 const int32_t* accepted, int32_t N, int32_t K, int32_t H,
                                 int32_t dk, int32_t dv, hipStream_t stream);
 
-// Optional debug check (KDA_DEBUG_VALIDATE): g (g_elems values, or none) within [g_lo, 0] and, for
+// Optional debug check (KDA_DEBUG_VALIDATE): g (g_elems values, or none) within [-5, 0] and, for
 // packed batches, cu_seqlens well formed.  Synchronises the stream; *ok = false on a violation.
 bool debug_validation_enabled();
 hipError_t debug_validate(const void* g, int g_dtype, int64_t g_elems, const int32_t* cu,
-                          int32_t n_seqs, int64_t total, hipStream_t stream, bool* ok,
-                          float g_lo = -5.0f);
+                          int32_t n_seqs, int64_t total, hipStream_t stream, bool* ok);
 
 struct ChunkArgs {
     const void* q;
@@ -85,41 +84,5 @@ hipError_t launch_chunk(const ChunkArgs& a, hipStream_t stream);
 // (sequence, head) units -- whole sequences, records built and consumed in LDS, no workspace.
 bool fused_eligible(int32_t in_dtype, int32_t dk, int32_t dv, int32_t n_seqs, int32_t H);
 hipError_t launch_fused(const ChunkArgs& a, hipStream_t stream);
-
-// Linear attention with one decay per head (kda_linear.hip).
-struct LinearArgs {
-    const void *q, *k, *v, *d_o;     // d_o: backward only
-    const float* g;                  // [H]
-    const float* h0;                 // initial state or nullptr
-    float* hT;                       // final state or nullptr (forward)
-    const float* dhT;                // its gradient or nullptr (backward)
-    float* dh0;                      // the initial state's gradient or nullptr (backward)
-    const int32_t* cu;               // device cu_seqlens or nullptr
-    void* o;                         // forward
-    void *dq, *dkk, *dvv;            // backward: gradients of q, k, v
-    int in_dtype, o_dtype;
-    int32_t B;
-    int64_t T;
-    int32_t n_seqs, H, dk, dv;
-    float scale;
-    void* workspace;
-};
-size_t linear_workspace_bytes(int32_t n_seqs, int64_t total_tokens, int32_t H, int32_t dk, int32_t dv,
-                              int32_t in_dtype, bool backward);
-hipError_t launch_linear_fwd(const LinearArgs& a, hipStream_t stream);
-hipError_t launch_linear_bwd(const LinearArgs& a, hipStream_t stream);
-hipError_t launch_linear_decode(const void* q, const void* k, const void* v, int in_dtype, const float* g,
-                                float* state, void* o, int o_dtype, int32_t N, int32_t H, int32_t dk,
-                                int32_t dv, float scale, hipStream_t stream);
-
-// 8-bit state cache (kda_state_cache.hip).
-struct StateCacheArgs {
-    void* codes;                     // read only by launch_state_load
-    float* scales;
-    const int32_t* slots;            // [N] or nullptr (sequence n in slot n)
-    int32_t code, N, n_slots, H, dk, dv, group;
-};
-hipError_t launch_state_store(const StateCacheArgs& a, const float* states, hipStream_t stream);
-hipError_t launch_state_load(const StateCacheArgs& a, float* states, hipStream_t stream);
 
 }  // namespace kda

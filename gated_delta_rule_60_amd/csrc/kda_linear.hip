@@ -10,6 +10,7 @@
 //   dv : a = k,  b = q,  c = do, backward, ub = scale, M from the final state's gradient, to the
 //        initial state's gradient
 #include "kda_chunk_util.hpp"
+#include "kda_linear.hpp"
 
 #include <algorithm>
 #include <type_traits>

@@ -16,7 +16,7 @@
 // elements, which divides every sequence's states, in four passes, loads first.  The fp32 states are
 // streamed past the caches (each is touched once).
 #include "kda_common.hpp"
-#include "kda_internal.hpp"
+#include "kda_linear.hpp"
 
 namespace kda {
 namespace {

@@ -15,6 +15,7 @@
 
 #include "kda_common.hpp"
 #include "kda_internal.hpp"
+#include "kda_linear.hpp"
 
 namespace kda {
 namespace {
@@ -48,7 +49,12 @@ bool debug_validation_enabled() {
 }
 
 hipError_t debug_validate(const void* g, int g_dtype, int64_t g_elems, const int32_t* cu,
-                          int32_t n_seqs, int64_t total, hipStream_t stream, bool* ok, float g_lo) {
+                          int32_t n_seqs, int64_t total, hipStream_t stream, bool* ok) {
+    return debug_validate_from(-5.0f, g, g_dtype, g_elems, cu, n_seqs, total, stream, ok);
+}
+
+hipError_t debug_validate_from(float g_lo, const void* g, int g_dtype, int64_t g_elems, const int32_t* cu,
+                               int32_t n_seqs, int64_t total, hipStream_t stream, bool* ok) {
     *ok = true;
     unsigned int* w = nullptr;
     hipError_t e = hipGetSymbolAddress(reinterpret_cast<void**>(&w), HIP_SYMBOL(validate_word));
