@@ -272,7 +272,8 @@ __device__ __forceinline__ void chunk_pass(const Launch& L, const Pass& p, int32
     {
         const float* src = nullptr;                  // none: an empty range, which reads as zeros
         if constexpr (!STATE_ONLY) {
-            if (w.s != (BACK ? w.n_seg - 1 : 0)) src = p.seg_states + (static_cast<int64_t>(slot) * L.H + h) * (DA * DC);
+            // (the first segment too: its initial state may be the final state the last one writes)
+            if (w.n_seg > 1) src = p.seg_states + (static_cast<int64_t>(slot) * L.H + h) * (DA * DC);
             else if (p.m_in) src = p.m_in + unit * (DA * DC);
         }
         const __amdgpu_buffer_rsrc_t rs = make_rsrc_u(src, src ? DA * DC * 4 : 0);
@@ -590,9 +591,9 @@ __global__ void __launch_bounds__(DC * 4, DA > DC ? 2 : 4) linear_chunk_kernel(L
     else chunk_pass<DT, ODT, DA, DC, false, STATE_ONLY>(L, p, slot, h, lds);
 }
 
-// Segment states: from each segment's own contribution to the state it starts from, in place (the first
-// segment, in the pass's direction, starts from the initial state itself).  Grid (sequence * H + head,
-// element blocks of 1024, pass); each lane carries four elements along, eight segments' loads at a time.
+// Segment states: from each segment's own contribution to the state it starts from, in place.  Grid
+// (sequence * H + head, element blocks of 1024, pass); each lane carries four elements along, eight
+// segments' loads at a time.
 __global__ void __launch_bounds__(256) linear_scan_kernel(Launch L, int32_t elems) {
     const Pass& p = L.pass[blockIdx.z];
     const int32_t n = blockIdx.x / L.H, h = blockIdx.x % L.H;
@@ -613,6 +614,7 @@ __global__ void __launch_bounds__(256) linear_scan_kernel(Launch L, int32_t elem
     const double full = exp(static_cast<double>(int64_t(1) << L.seg_shift) * g), last = exp(static_cast<double>(part) * g);
     auto slot = [&](int32_t i) { return reinterpret_cast<f32x4*>(at + (p.back ? n_seg - 1 - i : i) * step); };
     f32x4 ahead = *slot(0);                       // read before the batch before it writes its place
+    *slot(0) = x;
     for (int32_t i0 = 0; i0 < n_seg - 1; i0 += 8) {
         f32x4 own[9];
         own[0] = ahead;

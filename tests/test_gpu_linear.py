@@ -217,6 +217,44 @@ def test_in_place_state_and_zero_tokens():
     assert none is None
 
 
+@pytest.mark.parametrize("shape", [dict(B=1, T=2500), dict(B=1, T=0, lens=[1500, 3, 0, 1111])])
+def test_in_place_state_of_a_long_sequence(shape):
+    """The segments of a sequence run at the same time: the last one's final state must not overwrite the
+    initial state that the first one starts from."""
+    d = make(H=2, dk=128, dv=128, dtype=BF, seed=16, **shape)
+    d["g"] = torch.tensor([-1e-3, -0.05])
+    a = [dev(d[n]) for n in ("q", "k", "v", "g")]
+    o, hT = K.kda_linear_chunk_fwd(*a, initial_state=dev(d["h0"]), cu_seqlens=dev(d["cu"]))
+    for _ in range(3):
+        S = dev(d["h0"])
+        o2, _ = K.kda_linear_chunk_fwd(*a, initial_state=S, final_state=S, cu_seqlens=dev(d["cu"]))
+        torch.cuda.synchronize()
+        assert torch.equal(o, o2) and torch.equal(S, hT)
+
+
+def test_debug_validation(monkeypatch):
+    """KDA_DEBUG_VALIDATE refuses positive or NaN decays and malformed offsets, and takes -inf."""
+    d = make(1, 0, 2, 64, 64, BF, lens=[70, 30], seed=32)
+    q, k, v, do = (dev(d[n]) for n in ("q", "k", "v", "do"))
+    S = torch.zeros((1, 2, 64, 64), device=DEV)
+    one = [x[0, :1].contiguous() for x in (q, k, v)]
+    monkeypatch.setenv("KDA_DEBUG_VALIDATE", "1")
+    good = torch.tensor([-0.1, float("-inf")], device=DEV)
+    K.kda_linear_chunk_fwd(q, k, v, good, cu_seqlens=dev(d["cu"]))
+    K.kda_linear_decode_step(*one, good, S)
+    for bad in (0.25, float("nan")):
+        g = torch.tensor([-0.1, bad], device=DEV)
+        for call in (lambda: K.kda_linear_chunk_fwd(q, k, v, g), lambda: K.kda_linear_chunk_bwd(q, k, v, g, do),
+                     lambda: K.kda_linear_decode_step(*one, g, S)):
+            with pytest.raises(K.KDAError) as e:
+                call()
+            assert e.value.status == 1
+    for cu in ([0, 80, 60], [1, 70, 100], [0, 70, 99]):
+        with pytest.raises(K.KDAError) as e:
+            K.kda_linear_chunk_fwd(q, k, v, good, cu_seqlens=torch.tensor(cu, dtype=torch.int32, device=DEV))
+        assert e.value.status == 1
+
+
 def test_split_prefill_continues():
     """Two prefills, the second from the first one's state, against one."""
     d = make(1, 300, 2, 128, 128, F32, seed=14)
