@@ -78,44 +78,49 @@ __device__ __forceinline__ float4 decode4(uint32_t w) {
     }
 }
 
+// One workgroup: `rounds` blocks of 4096 elements of one sequence's states (or what is left of them).
 template <int CODE, int GROUP>
 __global__ void __launch_bounds__(256, 8) store_kernel(const float* __restrict__ states, const int32_t* __restrict__ slots,
-                                                    uint8_t* __restrict__ codes, float* __restrict__ scales,
-                                                    int32_t N, int32_t n_slots, int64_t per_seq, int32_t blocks_per_seq) {
-    const int32_t n = blockIdx.x / blocks_per_seq, part = blockIdx.x % blocks_per_seq;
-    const int32_t slot = slots ? slots[n] : n;
-    if (slot < 0 || slot >= n_slots) return;
-    if (slots) {                     // a later sequence with the same slot takes it
-        bool later = false;
-        for (int32_t m = n + 1 + static_cast<int32_t>(threadIdx.x); m < N; m += 256) later |= slots[m] == slot;
-        if (__syncthreads_or(later)) return;
-    }
+                                                       uint8_t* __restrict__ codes, float* __restrict__ scales,
+                                                       int32_t N, int32_t n_slots, int64_t per_seq, int32_t parts,
+                                                       int32_t rounds) {
     constexpr float inv_most = 1.f / (CODE == KDA_CODE_I8 ? 127.f : 448.f);
-    const int64_t e0 = static_cast<int64_t>(part) * (PASSES * 1024) + 4 * threadIdx.x;
-    const float* src = states + n * per_seq;
-    uint8_t* dst = codes + slot * per_seq;
-    float* sc = scales + slot * (per_seq / GROUP);
+    const int32_t n = blockIdx.x / parts, part = blockIdx.x % parts;
+    const int32_t slot = slots ? slots[n] : n;
+    const int64_t lo = static_cast<int64_t>(part) * rounds * (PASSES * 1024);
+    const int64_t end = lo + static_cast<int64_t>(rounds) * (PASSES * 1024), hi = end < per_seq ? end : per_seq;
+    const float* src = states + n * per_seq + 4 * threadIdx.x;
+    uint8_t* dst = codes + slot * per_seq + 4 * threadIdx.x;        // formed, not used, for a slot outside
+    float* sc = scales + slot * (per_seq / GROUP) + threadIdx.x / (GROUP / 4);
     f32x4_t x[PASSES];
+    for (int64_t e = lo; e < hi; e += PASSES * 1024) {
 #pragma unroll
-    for (int p = 0; p < PASSES; ++p)
-        x[p] = __builtin_nontemporal_load(reinterpret_cast<const f32x4_t*>(src + e0 + p * 1024));
-#pragma unroll
-    for (int p = 0; p < PASSES; ++p) {
-        const int64_t e = e0 + p * 1024;
-        float a = __builtin_fmaxf(__builtin_fmaxf(__builtin_fabsf(x[p][0]), __builtin_fabsf(x[p][1])),
-                                  __builtin_fmaxf(__builtin_fabsf(x[p][2]), __builtin_fabsf(x[p][3])));
-        // 0 while all values are finite, NaN from the first infinity or NaN on
-        float bad = (x[p][0] - x[p][0]) + (x[p][1] - x[p][1]) + (x[p][2] - x[p][2]) + (x[p][3] - x[p][3]);
-#pragma unroll
-        for (int off = 1; off < GROUP / 4; off <<= 1) {
-            a = __builtin_fmaxf(a, __shfl_xor(a, off, 64));
-            bad += __shfl_xor(bad, off, 64);
+        for (int p = 0; p < PASSES; ++p) x[p] = __builtin_nontemporal_load(reinterpret_cast<const f32x4_t*>(src + e + p * 1024));
+        if (e == lo) {               // under the first loads
+            if (slot < 0 || slot >= n_slots) return;
+            if (slots) {             // a later sequence with the same slot takes it
+                bool later = false;
+                for (int32_t m = n + 1 + static_cast<int32_t>(threadIdx.x); m < N; m += 256) later |= slots[m] == slot;
+                if (__syncthreads_or(later)) return;
+            }
         }
-        const float scale = bad == 0.f ? a * inv_most : __uint_as_float(0x7fc00000u);
-        uint32_t w = 0;
-        if (scale > 0.f) w = encode4<CODE>(x[p], scale);
-        *reinterpret_cast<uint32_t*>(dst + e) = w;
-        if (e % GROUP == 0) sc[e / GROUP] = scale;
+#pragma unroll
+        for (int p = 0; p < PASSES; ++p) {
+            float a = __builtin_fmaxf(__builtin_fmaxf(__builtin_fabsf(x[p][0]), __builtin_fabsf(x[p][1])),
+                                      __builtin_fmaxf(__builtin_fabsf(x[p][2]), __builtin_fabsf(x[p][3])));
+            // 0 while all values are finite, NaN from the first infinity or NaN on
+            float bad = (x[p][0] - x[p][0]) + (x[p][1] - x[p][1]) + (x[p][2] - x[p][2]) + (x[p][3] - x[p][3]);
+#pragma unroll
+            for (int off = 1; off < GROUP / 4; off <<= 1) {
+                a = __builtin_fmaxf(a, __shfl_xor(a, off, 64));
+                bad += __shfl_xor(bad, off, 64);
+            }
+            const float scale = bad == 0.f ? a * inv_most : __uint_as_float(0x7fc00000u);
+            uint32_t w = 0;
+            if (scale > 0.f) w = encode4<CODE>(x[p], scale);
+            *reinterpret_cast<uint32_t*>(dst + e + p * 1024) = w;
+            if (threadIdx.x % (GROUP / 4) == 0) sc[(e + p * 1024) / GROUP] = scale;
+        }
     }
 }
 
@@ -155,11 +160,14 @@ __global__ void __launch_bounds__(256) load_kernel(const uint8_t* __restrict__ c
 
 hipError_t launch_state_store(const StateCacheArgs& a, const float* states, hipStream_t stream) {
     const int64_t per_seq = int64_t(a.H) * a.dk * a.dv;
-    const int32_t bps = static_cast<int32_t>(per_seq / (PASSES * 1024));
-    const dim3 grid(static_cast<unsigned>(int64_t(a.N) * bps));
+    // each workgroup looks for a later sequence with its slot, so once there are enough of them to fill the
+    // card they take four blocks each
+    const int64_t blocks = per_seq / (PASSES * 1024);
+    const int32_t rounds = a.N * blocks >= 16384 ? 4 : 1, parts = static_cast<int32_t>((blocks + rounds - 1) / rounds);
+    const dim3 grid(static_cast<unsigned>(int64_t(a.N) * parts));
     auto go = [&](auto kernel) {
         hipLaunchKernelGGL(kernel, grid, dim3(256), 0, stream, states, a.slots, static_cast<uint8_t*>(a.codes), a.scales,
-                           a.N, a.n_slots, per_seq, bps);
+                           a.N, a.n_slots, per_seq, parts, rounds);
         return hipGetLastError();
     };
     if (a.code == KDA_CODE_I8) {

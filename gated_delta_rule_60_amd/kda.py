@@ -468,8 +468,8 @@ def _fit(dev, *specs) -> bool:
     """Whether every (tensor or None, shape, dtype) of `specs` is as stated, contiguous and on `dev`:
     the quick form of the checks that _expect and _one_device make (and word) one by one."""
     for t, shape, dtype in specs:
-        if t is not None and not (t.shape == shape and t.dtype is dtype and t.device == dev and
-                                  t.is_contiguous()):
+        if t is not None and not (isinstance(t, torch.Tensor) and t.shape == shape and
+                                  t.dtype is dtype and t.device == dev and t.is_contiguous()):
             return False
     return dev.type == "cuda"
 
