@@ -78,32 +78,31 @@ __device__ __forceinline__ float4 decode4(uint32_t w) {
     }
 }
 
-// One workgroup: `rounds` blocks of 4096 elements of one sequence's states (or what is left of them).
-template <int CODE, int GROUP>
+// One workgroup: ROUNDS blocks of 4096 elements of one sequence's states (or what is left of them).  Every
+// workgroup looks through the later sequences for its slot, so where there are many, one takes four blocks
+// (16384 sequences of 2 x 64 x 64: 155 us, 206 us with one; 1024 of 32 x 128 x 128: 551 us, 503 us with one).
+template <int CODE, int GROUP, int ROUNDS>
 __global__ void __launch_bounds__(256, 8) store_kernel(const float* __restrict__ states, const int32_t* __restrict__ slots,
                                                        uint8_t* __restrict__ codes, float* __restrict__ scales,
-                                                       int32_t N, int32_t n_slots, int64_t per_seq, int32_t parts,
-                                                       int32_t rounds) {
+                                                       int32_t N, int32_t n_slots, int64_t per_seq, int32_t parts) {
     constexpr float inv_most = 1.f / (CODE == KDA_CODE_I8 ? 127.f : 448.f);
     const int32_t n = blockIdx.x / parts, part = blockIdx.x % parts;
     const int32_t slot = slots ? slots[n] : n;
-    const int64_t lo = static_cast<int64_t>(part) * rounds * (PASSES * 1024);
-    const int64_t end = lo + static_cast<int64_t>(rounds) * (PASSES * 1024), hi = end < per_seq ? end : per_seq;
+    if (slot < 0 || slot >= n_slots) return;
+    if (slots) {                     // a later sequence with the same slot takes it
+        bool later = false;
+        for (int32_t m = n + 1 + static_cast<int32_t>(threadIdx.x); m < N; m += 256) later |= slots[m] == slot;
+        if (__syncthreads_or(later)) return;
+    }
     const float* src = states + n * per_seq + 4 * threadIdx.x;
-    uint8_t* dst = codes + slot * per_seq + 4 * threadIdx.x;        // formed, not used, for a slot outside
+    uint8_t* dst = codes + slot * per_seq + 4 * threadIdx.x;
     float* sc = scales + slot * (per_seq / GROUP) + threadIdx.x / (GROUP / 4);
-    f32x4_t x[PASSES];
-    for (int64_t e = lo; e < hi; e += PASSES * 1024) {
+    for (int32_t r = 0; r < ROUNDS; ++r) {
+        const int64_t e = (static_cast<int64_t>(part) * ROUNDS + r) * (PASSES * 1024);
+        if (ROUNDS > 1 && e >= per_seq) break;
+        f32x4_t x[PASSES];
 #pragma unroll
         for (int p = 0; p < PASSES; ++p) x[p] = __builtin_nontemporal_load(reinterpret_cast<const f32x4_t*>(src + e + p * 1024));
-        if (e == lo) {               // under the first loads
-            if (slot < 0 || slot >= n_slots) return;
-            if (slots) {             // a later sequence with the same slot takes it
-                bool later = false;
-                for (int32_t m = n + 1 + static_cast<int32_t>(threadIdx.x); m < N; m += 256) later |= slots[m] == slot;
-                if (__syncthreads_or(later)) return;
-            }
-        }
 #pragma unroll
         for (int p = 0; p < PASSES; ++p) {
             float a = __builtin_fmaxf(__builtin_fmaxf(__builtin_fabsf(x[p][0]), __builtin_fabsf(x[p][1])),
@@ -160,24 +159,22 @@ __global__ void __launch_bounds__(256) load_kernel(const uint8_t* __restrict__ c
 
 hipError_t launch_state_store(const StateCacheArgs& a, const float* states, hipStream_t stream) {
     const int64_t per_seq = int64_t(a.H) * a.dk * a.dv;
-    // each workgroup looks for a later sequence with its slot, so once there are enough of them to fill the
-    // card they take four blocks each
     const int64_t blocks = per_seq / (PASSES * 1024);
-    const int32_t rounds = a.N * blocks >= 16384 ? 4 : 1, parts = static_cast<int32_t>((blocks + rounds - 1) / rounds);
+    const int32_t rounds = a.slots && a.N >= 2048 ? 4 : 1, parts = static_cast<int32_t>((blocks + rounds - 1) / rounds);
     const dim3 grid(static_cast<unsigned>(int64_t(a.N) * parts));
-    auto go = [&](auto kernel) {
-        hipLaunchKernelGGL(kernel, grid, dim3(256), 0, stream, states, a.slots, static_cast<uint8_t*>(a.codes), a.scales,
-                           a.N, a.n_slots, per_seq, parts, rounds);
+    auto go = [&](auto one, auto four) {
+        hipLaunchKernelGGL(rounds == 1 ? one : four, grid, dim3(256), 0, stream, states, a.slots,
+                           static_cast<uint8_t*>(a.codes), a.scales, a.N, a.n_slots, per_seq, parts);
         return hipGetLastError();
     };
     if (a.code == KDA_CODE_I8) {
-        if (a.group == 32) return go(store_kernel<KDA_CODE_I8, 32>);
-        if (a.group == 64) return go(store_kernel<KDA_CODE_I8, 64>);
-        return go(store_kernel<KDA_CODE_I8, 128>);
+        if (a.group == 32) return go(store_kernel<KDA_CODE_I8, 32, 1>, store_kernel<KDA_CODE_I8, 32, 4>);
+        if (a.group == 64) return go(store_kernel<KDA_CODE_I8, 64, 1>, store_kernel<KDA_CODE_I8, 64, 4>);
+        return go(store_kernel<KDA_CODE_I8, 128, 1>, store_kernel<KDA_CODE_I8, 128, 4>);
     }
-    if (a.group == 32) return go(store_kernel<KDA_CODE_E4M3, 32>);
-    if (a.group == 64) return go(store_kernel<KDA_CODE_E4M3, 64>);
-    return go(store_kernel<KDA_CODE_E4M3, 128>);
+    if (a.group == 32) return go(store_kernel<KDA_CODE_E4M3, 32, 1>, store_kernel<KDA_CODE_E4M3, 32, 4>);
+    if (a.group == 64) return go(store_kernel<KDA_CODE_E4M3, 64, 1>, store_kernel<KDA_CODE_E4M3, 64, 4>);
+    return go(store_kernel<KDA_CODE_E4M3, 128, 1>, store_kernel<KDA_CODE_E4M3, 128, 4>);
 }
 
 hipError_t launch_state_load(const StateCacheArgs& a, float* states, hipStream_t stream) {

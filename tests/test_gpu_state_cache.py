@@ -109,8 +109,9 @@ def test_infinities_and_nans_stay_in_their_group(dtype):
 
 
 @pytest.mark.parametrize("dtype", CODES)
-def test_slots_outside_and_repeated(dtype):
-    N, H, dk, dv, group, n_slots = 600, 1, 64, 64, 64, 5
+@pytest.mark.parametrize("N,H,dk,dv,group", [(600, 1, 64, 64, 64), (2100, 3, 64, 64, 32)])
+def test_slots_outside_and_repeated(N, H, dk, dv, group, dtype):
+    n_slots = 5
     x = states(N, H, dk, dv, seed=8)
     gen = torch.Generator("cpu").manual_seed(9)
     slots = torch.randint(-2, n_slots + 2, (N,), generator=gen, dtype=torch.int32)
