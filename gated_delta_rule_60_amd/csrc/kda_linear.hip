@@ -31,8 +31,8 @@ struct Pass {
 };
 constexpr int MAX_PASSES = 3;
 
-// A launch covers (sequence, segment) slots times heads times passes.  A segment is 2^seg_shift tokens.
-// Fixed-length batches: n_seg slots per sequence; packed ones: slot (cu[n] >> seg_shift) + n + s for
+// A launch covers (sequence, segment) slots times heads times passes.  A segment is `seg` tokens.
+// Fixed-length batches: n_seg slots per sequence; packed ones: slot floor(cu[n] / seg) + n + s for
 // segment s of sequence n, which leaves unused slots between sequences.
 struct Launch {
     Pass pass[MAX_PASSES];
@@ -40,11 +40,11 @@ struct Launch {
     const int32_t* cu;
     int64_t T;
     int32_t n_seqs, H, slots;
-    int32_t seg_shift;       // 40: whole sequences
+    int32_t seg;             // WHOLE: whole sequences
     int32_t n_seg;           // of a fixed-length sequence
     int32_t passes;
 };
-constexpr int WHOLE = 40;
+constexpr int32_t WHOLE = 0x7fffffff;
 
 struct Where {
     int32_t n, s, n_seg;     // sequence, segment, segments of the sequence
@@ -63,11 +63,11 @@ __device__ __forceinline__ void seq_range(const Launch& L, int32_t n, int64_t& l
 __device__ __forceinline__ int32_t first_slot(const Launch& L, int32_t n) {
     int64_t lo, hi;
     seq_range(L, n, lo, hi);
-    return static_cast<int32_t>(lo >> L.seg_shift) + n;
+    return static_cast<int32_t>(static_cast<uint32_t>(lo) / static_cast<uint32_t>(L.seg)) + n;
 }
 __device__ __forceinline__ int32_t segments(const Launch& L, int64_t len) {
-    const int64_t one = int64_t(1) << L.seg_shift;
-    return len <= one ? 1 : static_cast<int32_t>((len + one - 1) >> L.seg_shift);
+    if (L.cu == nullptr) return L.n_seg;
+    return len <= L.seg ? 1 : static_cast<int32_t>((static_cast<uint32_t>(len) - 1u) / static_cast<uint32_t>(L.seg)) + 1;
 }
 __device__ __forceinline__ bool locate(const Launch& L, int32_t slot, Where& w) {
     int64_t lo, hi;
@@ -87,9 +87,8 @@ __device__ __forceinline__ bool locate(const Launch& L, int32_t slot, Where& w) 
     }
     w.n_seg = segments(L, hi - lo);
     if (w.s < 0 || w.s >= w.n_seg) return false;
-    w.lo = lo + (static_cast<int64_t>(w.s) << L.seg_shift);
-    const int64_t end = w.lo + (int64_t(1) << L.seg_shift);
-    w.hi = end < hi ? end : hi;
+    w.lo = lo + static_cast<int64_t>(w.s) * L.seg;
+    w.hi = w.s == w.n_seg - 1 ? hi : w.lo + L.seg;
     return true;
 }
 
@@ -610,8 +609,8 @@ __global__ void __launch_bounds__(256) linear_scan_kernel(Launch L, int32_t elem
     float* at = p.seg_states + (static_cast<int64_t>(first) * L.H + h) * elems + e;
     const int64_t step = static_cast<int64_t>(L.H) * elems;
     // decay over a segment as hi + lo: its rounding would act the same way segment after segment
-    const int64_t part = len - (static_cast<int64_t>(n_seg - 1) << L.seg_shift);
-    const double full = exp(static_cast<double>(int64_t(1) << L.seg_shift) * g), last = exp(static_cast<double>(part) * g);
+    const int64_t part = len - static_cast<int64_t>(n_seg - 1) * L.seg;
+    const double full = exp(static_cast<double>(L.seg) * g), last = exp(static_cast<double>(part) * g);
     auto slot = [&](int32_t i) { return reinterpret_cast<f32x4*>(at + (p.back ? n_seg - 1 - i : i) * step); };
     f32x4 ahead = *slot(0);                       // read before the batch before it writes its place
     *slot(0) = x;
@@ -635,24 +634,24 @@ __global__ void __launch_bounds__(256) linear_scan_kernel(Launch L, int32_t elem
 
 // ---------------------------------------------------------------- host side
 
-// log2 of the tokens per segment.  Whole sequences where (sequence, head) units alone give every CU a
+// Tokens per segment, a multiple of 64.  Whole sequences where (sequence, head) units alone give every CU a
 // workgroup (16 x 4096 tokens x 16 heads, bf16, d = 128: 337 us whole, 388 us in two segments each; 4 x 4096
-// x 16 in eight segments: 118 us) or where none is long (below 1024 tokens two more launches cost what the
-// shorter chains save).  Else as many segments as give every CU two workgroups, but no shorter than 256
-// tokens (fp32, whose chunks take longer: 128), so that a segment's state, read and written about four times,
-// stays small against its rows (8192 tokens x 8 heads: 57 us with 256-token segments, 68 us with 512).
-int segment_shift(int32_t n_seqs, int64_t total, int32_t H, int32_t in_dtype, bool packed) {
+// x 16 in eight segments: 105 us) or where none is long (below 1024 tokens two more launches cost what the
+// shorter chains save).  Else segments for two workgroups a CU, in one round: 512 in all, a few fewer for a
+// packed batch, whose sequences each end in a short one (65536 tokens x 33 heads: 796 us, in 528 segments
+// 1033 us).  No shorter than 256 tokens (fp32, whose chunks take longer: 128), so that a segment's state,
+// read and written about four times, stays small against its rows (16384 x 4 heads, d = 64: 46 us with 256,
+// 62 us with 128).
+int32_t segment_tokens(int32_t n_seqs, int64_t total, int32_t H, int32_t in_dtype, bool packed) {
     const int64_t units = int64_t(n_seqs) * H, longest = packed ? total : total / n_seqs;
     if (units >= 256 || longest < 1024) return WHOLE;
-    const int64_t want = total * H / 512;                             // tokens of one of 512 equal shares
-    int shift = in_dtype == KDA_BF16 ? 8 : 7;
-    while ((int64_t(1) << (shift + 1)) <= want) ++shift;
-    return (int64_t(1) << shift) >= longest ? WHOLE : shift;
+    const int64_t shares = packed ? std::max<int64_t>(1, 512 / H - n_seqs / 2) : 512 / units;   // of `longest`
+    const int64_t seg = std::max<int64_t>(((longest + shares - 1) / shares + 63) / 64 * 64, in_dtype == KDA_BF16 ? 256 : 128);
+    return seg >= longest || seg >= WHOLE ? WHOLE : static_cast<int32_t>(seg);
 }
-int64_t segment_slots(int32_t n_seqs, int64_t total, int shift, bool packed) {
-    if (packed) return (total >> shift) + n_seqs;
-    const int64_t T = total / n_seqs, one = int64_t(1) << shift;
-    return n_seqs * std::max<int64_t>(1, (T + one - 1) >> shift);
+int64_t segment_slots(int32_t n_seqs, int64_t total, int32_t seg, bool packed) {
+    if (packed) return total / seg + n_seqs;
+    return seg == WHOLE ? n_seqs : n_seqs * ((total / n_seqs + seg - 1) / seg);
 }
 
 template <int DT, int ODT, bool STATE_ONLY>
@@ -677,8 +676,8 @@ Launch base_launch(const LinearArgs& a) {
     Launch L{};
     const int64_t total = int64_t(a.B) * a.T;
     L.g = a.g; L.cu = a.cu; L.T = a.T; L.n_seqs = a.n_seqs; L.H = a.H;
-    L.seg_shift = segment_shift(a.n_seqs, total, a.H, a.in_dtype, a.cu != nullptr);
-    L.slots = static_cast<int32_t>(segment_slots(a.n_seqs, total, L.seg_shift, a.cu != nullptr));
+    L.seg = segment_tokens(a.n_seqs, total, a.H, a.in_dtype, a.cu != nullptr);
+    L.slots = static_cast<int32_t>(segment_slots(a.n_seqs, total, L.seg, a.cu != nullptr));
     L.n_seg = L.slots / a.n_seqs;
     return L;
 }
@@ -695,7 +694,7 @@ hipError_t forward(const LinearArgs& a, hipStream_t stream) {
     Launch L = base_launch(a);
     L.passes = 1;
     L.pass[0] = make_pass(a.q, a.k, a.v, a.o, false, a.scale, 1.f, a.h0, false, a.hT);
-    if (L.seg_shift < WHOLE) {
+    if (L.seg < WHOLE) {
         L.pass[0].seg_states = static_cast<float*>(a.workspace);
         L.pass[0].exact = a.hT != nullptr;
         hipError_t e = launch_chunks<DT, DT, true>(L, a.dk, a.dv, stream);
@@ -712,7 +711,7 @@ hipError_t backward(const LinearArgs& a, hipStream_t stream) {
     Pass k = make_pass(a.v, a.d_o, a.q, a.dkk, true, 1.f, a.scale, a.dhT, true, nullptr);
     Pass v = make_pass(a.k, a.q, a.d_o, a.dvv, true, 1.f, a.scale, a.dhT, false, a.dh0);
     hipError_t e = hipSuccess;
-    if (base.seg_shift < WHOLE) {
+    if (base.seg < WHOLE) {
         // the forward states (b = k, c = v) and their gradients (b = q, c = do)
         Launch L = base;
         L.passes = 2;
@@ -744,8 +743,8 @@ size_t linear_workspace_bytes(int32_t n_seqs, int64_t total, int32_t H, int32_t 
     // what a packed batch of these sizes needs, or fixed-length sequences: whichever is more
     int64_t slots = 0;
     for (const bool packed : {false, true}) {
-        const int shift = segment_shift(n_seqs, total, H, in_dtype, packed);
-        if (shift < WHOLE) slots = std::max(slots, segment_slots(n_seqs, total, shift, packed));
+        const int32_t seg = segment_tokens(n_seqs, total, H, in_dtype, packed);
+        if (seg < WHOLE) slots = std::max(slots, segment_slots(n_seqs, total, seg, packed));
     }
     return static_cast<size_t>(slots) * H * dk * dv * 4 * (backward ? 2 : 1);
 }
