@@ -363,6 +363,62 @@ def test_other_stream_and_captured_replays(T):
         torch.cuda.synchronize()
 
 
+def test_two_calls_at_once():
+    """Prefills and gradients of two inputs on two streams, each with workspaces of its own."""
+    ds = [{n: dev(x) for n, x in make(1, T, 2, 128, 128, BF, seed=40 + T).items()} for T in (2100, 1500)]
+    want = [_buffers(d) for d in ds]
+    for d, b in zip(ds, want):
+        _pass(d, torch.empty_like(d["h0"]), b)
+    torch.cuda.synchronize()
+    streams, got = [torch.cuda.Stream() for _ in ds], [_buffers(d) for d in ds]
+    states = [torch.empty_like(d["h0"]) for d in ds]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for st, d, S, b in zip(streams, ds, states, got):
+            with torch.cuda.stream(st):
+                _pass(d, S, b)
+    torch.cuda.synchronize()
+    for a, b in zip(want, got):
+        assert all(torch.equal(a[n], b[n]) for n in a if not n.startswith("ws"))
+
+
+def test_tensors_beyond_four_gigabytes():
+    """One sequence of 2^20 + 5000 tokens x 17 heads (4.6 GB per tensor) under a decay that forgets within
+    some hundred tokens: its last 4096 tokens against a call on them alone, where 1024 tokens in nothing of
+    what came before is left (e^(-0.5 * 1024)).  Both results round the same numbers, so they differ by a
+    half step of each and by the roundings on the way: sums of at most 1 / (1 - e^-0.5) < 2.6 terms of
+    |q.k| <= 1 times |v| < 7, each within (2 * 256 + 640) 2^-24 + 2 * 2^-16 of itself."""
+    T, H, tail, skip = (1 << 20) + 5000, 17, 4096, 1024
+    gen = torch.Generator(DEV).manual_seed(50)
+
+    def unit():
+        x = torch.randn((1, T, H, 128), generator=gen, device=DEV, dtype=BF)
+        for i in range(0, T, 1 << 17):
+            part = x[:, i:i + (1 << 17)].float()
+            x[:, i:i + (1 << 17)] = part / part.norm(dim=-1, keepdim=True)
+        return x
+    q, k = unit(), unit()
+    v, do = (torch.randn((1, T, H, 128), generator=gen, device=DEV, dtype=BF) for _ in range(2))
+    g = torch.full((H,), -0.5, device=DEV)
+    cut = lambda x: x[:, T - tail:].contiguous()                                   # noqa: E731
+    # q and k are rounded to bf16 after normalising: |q.k| <= 1 + 2^-6
+    slack = 2 * 2.6 * 1.02 * 7 * ((2 * 256 + 640) * U + 2 * 2.0 ** -16)
+
+    def same(a, b, lo):
+        a, b = a[:, lo:].float(), b[:, lo:].float()
+        assert bool(((a - b).abs() <= slack + 2 * 2.0 ** -8 * torch.maximum(a.abs(), b.abs())).all())
+    o, S = K.kda_linear_chunk_fwd(q, k, v, g)
+    o1, S1 = K.kda_linear_chunk_fwd(cut(q), cut(k), cut(v), g)
+    same(cut(o), o1, skip)
+    assert float((S - S1).abs().max()) <= slack
+    del o
+    grads = K.kda_linear_chunk_bwd(q, k, v, g, do)
+    # |do| has 128 elements: dq, dk sum |v.do| <= |v| |do| < 16^2 of unit vectors' elements
+    slack *= 16 * 16 / 7
+    for x, y, lo in zip(grads, K.kda_linear_chunk_bwd(*(cut(x) for x in (q, k, v)), g, cut(do)), (skip, 0, 0)):
+        same(cut(x), y, lo)
+
+
 def test_rows_behind_the_sequences_stay():
     """A packed batch whose offsets end before T (malformed, but in bounds): nothing behind the last
     sequence is written."""
