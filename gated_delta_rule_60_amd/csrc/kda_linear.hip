@@ -592,8 +592,8 @@ __global__ void __launch_bounds__(DC * 4, DA > DC ? 2 : 4) linear_chunk_kernel(L
 
 // Segment states: from each segment's own contribution to the state it starts from, in place.  Grid
 // (sequence * H + head, element blocks of 1024, pass); each lane carries four elements along, eight
-// segments' loads at a time (4 x 16 units x 8 segments of 64 KB, read and written: 11 us; 57 segments of
-// eight ragged sequences: 14 us, 19 us with one load at a time).
+// segments' loads at a time: 10.4 us for 4 x 4096 x 16 heads (8 segments of 64 KB each), 11.3 us with one
+// load at a time.
 __global__ void __launch_bounds__(256) linear_scan_kernel(Launch L, int32_t elems) {
     const Pass& p = L.pass[blockIdx.z];
     const int32_t n = blockIdx.x / L.H, h = blockIdx.x % L.H;
@@ -765,8 +765,8 @@ namespace {
 
 // One workgroup per (sequence, head): the state is read once, updated in registers and written once
 // (non-temporal both ways: a step touches it once).  Lane t owns four columns of DK / RG rows.  Bound by
-// HBM: 256 x 32 states of 128 x 128 in 173 us, 6.2 TB/s (a plain copy reaches 4.95); one sequence of 32
-// heads in 3.8 us, launch and one round trip to memory.
+// HBM: 256 x 32 states of 128 x 128 in 173 us, 6.2 TB/s (a large copy reaches 4.95); one sequence of 32
+// heads in 3.8 us.
 template <int DT, int ODT, int DK, int DV>
 __global__ void __launch_bounds__(256) linear_decode_kernel(const void* __restrict__ q, const void* __restrict__ k,
                                                             const void* __restrict__ v, const float* __restrict__ g,
