@@ -793,7 +793,11 @@ __global__ void __launch_bounds__(256) linear_decode_kernel(const void* __restri
         sq[t] = xq;
         sk[t] = xk;
     }
-    const float lam = expf(gg);
+    // e^g as hi + lo: its rounding to one fp32 number would act the same way token after token (up to 2^-25 of
+    // the state each time: 3.0e-4 after 10000 tokens at g = -1.07e-3, 1.3e-6 with both).  0.2 us on a single
+    // sequence, nothing on a batch.
+    const double lam = exp(static_cast<double>(gg));
+    const float lam_hi = static_cast<float>(lam), lam_lo = static_cast<float>(lam - static_cast<double>(lam_hi));
     __syncthreads();
     f32x4 acc = {0.f, 0.f, 0.f, 0.f};
     const f32x4 c = {vv.x, vv.y, vv.z, vv.w};
@@ -803,7 +807,7 @@ __global__ void __launch_bounds__(256) linear_decode_kernel(const void* __restri
         const float kr = sk[r], qr = sq[r];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            s[i][e] = __builtin_fmaf(kr, c[e], lam * s[i][e]);
+            s[i][e] = __builtin_fmaf(lam_hi, s[i][e], __builtin_fmaf(kr, c[e], lam_lo * s[i][e]));
             acc[e] = __builtin_fmaf(qr, s[i][e], acc[e]);
         }
         __builtin_nontemporal_store(s[i], reinterpret_cast<f32x4*>(S + r * DV));
