@@ -116,6 +116,16 @@ __device__ __forceinline__ void split3(float x, float y, uint32_t& h, uint32_t& 
     l = __builtin_amdgcn_perm(__float_as_uint(y2), __float_as_uint(x2), 0x07060302u);
 }
 
+// x times f, with f as hi + lo: a state that goes from call to call would otherwise take the rounding of f
+// along each time, the same way (10000 pieces of a prompt that each decay by 1e-3: the state off by 3.0e-4 of
+// itself with f as one fp32 number, by 1.3e-6 so).
+__device__ __forceinline__ f32x4 times(f32x4 x, double f) {
+    const float hi = static_cast<float>(f), lo = static_cast<float>(f - static_cast<double>(hi));
+#pragma unroll
+    for (int r = 0; r < 4; ++r) x[r] = __builtin_fmaf(x[r], hi, x[r] * lo);
+    return x;
+}
+
 template <typename T>
 __device__ __forceinline__ T lds_get(const void* sm, uint32_t byte) {
     typedef T __attribute__((may_alias)) T_ma;
@@ -204,7 +214,7 @@ struct ChunkLds {
     // so ub lam^(i-j) of a lane's scores: tile on the diagonal (masked), tile next to it
     f32x4 on_diag[STATE_ONLY ? 1 : 64], next[STATE_ONLY ? 1 : 64];
     double lam[TOK + 1];
-    double lam_full_inv;
+    double lam_n_inv;                                // of the chunk's length
 };
 
 // The pass in chunks of TOK tokens; one workgroup per (segment, head), wave w with the output columns
@@ -293,7 +303,6 @@ __device__ __forceinline__ void chunk_pass(const Launch& L, const Pass& p, int32
     if (len > 0) {
         const double g = static_cast<double>(L.g[h]);
         if (t <= TOK) lds.lam[t] = t == 0 ? 1.0 : exp(t * g);
-        if (t == TOK + 1) lds.lam_full_inv = exp(-TOK * g);
     }
     lds_barrier();
     if constexpr (!STATE_ONLY) {
@@ -329,7 +338,8 @@ __device__ __forceinline__ void chunk_pass(const Launch& L, const Pass& p, int32
     };
 
     // The state is held as f times the registers, so that most chunks need not multiply it; f and 1 / f
-    // are fp64, and the registers take f over before it leaves [2^-12, 2^12].
+    // are fp64, and the registers take f over before it leaves [2^-12, 2^12] (rounded to fp32: not more often
+    // than every eight e-foldings).
     double f = 1.0, f_inv = 1.0;
     const bool exact = STATE_ONLY ? p.exact != 0 : p.m_out && w.s == (BACK ? 0 : w.n_seg - 1);
     int table_n = -1;
@@ -339,6 +349,7 @@ __device__ __forceinline__ void chunk_pass(const Launch& L, const Pass& p, int32
         const int n = static_cast<int>(len - off < TOK ? len - off : TOK);
         if (n != table_n) {
             table_n = n;
+            if (t == TOK) lds.lam_n_inv = 1.0 / lds.lam[n];
             if (t < TOK) {
                 const int from_end = n - 1 - t;
                 lds.rd[t] = p.so * static_cast<float>(lds.lam[BACK ? (from_end < 0 ? 0 : from_end) : t + 1]);
@@ -430,9 +441,9 @@ __device__ __forceinline__ void chunk_pass(const Launch& L, const Pass& p, int32
         }
         // ---- decay
         const double fn = f * lds.lam[n];
-        if (n == TOK && fn >= 0x1p-12 && fn <= 0x1p12) {
+        if (fn >= 0x1p-12 && fn <= 0x1p12) {
             f = fn;
-            f_inv *= lds.lam_full_inv;
+            f_inv *= lds.lam_n_inv;
         } else {
             const float x = static_cast<float>(fn);
             f = f_inv = 1.0;
@@ -565,11 +576,12 @@ __device__ __forceinline__ void chunk_pass(const Launch& L, const Pass& p, int32
     if constexpr (STATE_ONLY) dst = p.seg_states + (static_cast<int64_t>(slot) * L.H + h) * (DA * DC);
     else if (p.m_out && w.s == (BACK ? 0 : w.n_seg - 1)) dst = p.m_out + unit * (DA * DC);
     if (dst) {
-        const float ff = static_cast<float>(f);
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
+        for (int mt = 0; mt < MT; ++mt) {
+            const f32x4 x = times(M[mt], f);
 #pragma unroll
-            for (int r = 0; r < 4; ++r) dst[(row(mt) + r) * DC + col] = M[mt][r] * ff;
+            for (int r = 0; r < 4; ++r) dst[(row(mt) + r) * DC + col] = x[r];
+        }
     }
 }
 

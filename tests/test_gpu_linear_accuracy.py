@@ -53,3 +53,20 @@ def test_decode_decay_over_many_steps(dtype):
         K.kda_linear_decode_step(z, z, z, gd, S, o=o)
     torch.cuda.synchronize()
     check_decayed(S, h0, g, 1, 1, "decode")
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("T", [1, 17, 64, 65])
+def test_prefill_decay_over_many_calls(T, dtype):
+    """A prompt fed in short pieces, each from the state the one before left: a partial chunk's decay and
+    the one pending at the end round the state twice."""
+    g = decays(T)
+    z = torch.zeros((2, T, 3, 64), dtype=dtype, device=DEV)
+    gen = torch.Generator("cpu").manual_seed(2)
+    h0 = torch.randn((2, 3, 64, 64), generator=gen).to(DEV)
+    S, gd = h0.clone(), torch.tensor(g, dtype=F32, device=DEV)
+    o = torch.empty_like(z)
+    for _ in range(CALLS):
+        K.kda_linear_chunk_fwd(z, z, z, gd, initial_state=S, final_state=S, o=o)
+    torch.cuda.synchronize()
+    check_decayed(S, h0, g, T, 2, f"prefill of {T}")
