@@ -70,3 +70,43 @@ def test_prefill_decay_over_many_calls(T, dtype):
         K.kda_linear_chunk_fwd(z, z, z, gd, initial_state=S, final_state=S, o=o)
     torch.cuda.synchronize()
     check_decayed(S, h0, g, T, 2, f"prefill of {T}")
+
+
+def relative(got, ref):
+    return float((got.double() - ref).norm() / ref.norm())
+
+
+def exact_states(k, v, g, h0):
+    """Final states of [B, T, H, d] inputs, token by token in fp64 on the GPU."""
+    lam = torch.exp(g.double())[:, None, None]
+    S = h0.double()
+    for t in range(k.shape[1]):
+        S = lam * S + k[:, t].double()[..., None] * v[:, t].double()[..., None, :]
+    return S
+
+
+@pytest.mark.parametrize("B,H", [(64, 4), (1, 3)])      # whole sequences, and segments
+def test_states_hold_fp32_accuracy(B, H):
+    """bf16 inputs, slow decays: each of the 192 additions to a state (2048 tokens in steps of 32, three terms
+    each) rounds it by 2^-24 * 1.5 / sqrt(12) of itself (rms), on the way to a state that grows like the root
+    of the tokens: 2^-24 * 0.43 * sqrt(192 / 2) = 2.5e-7 in all; four times that.  Two terms instead of three
+    would leave out 2^-17 of each addend and more, 2.6e-6."""
+    T = 2048
+    gen = torch.Generator("cpu").manual_seed(7)
+    q, k, v, do = (torch.randn((B, T, H, 64), generator=gen).to(BF).to(DEV) for _ in range(4))
+    g = torch.tensor([-1e-4, -1e-3, -1e-2, -1e-4][:H], device=DEV)
+    h0, dhT = (torch.randn((B, H, 64, 64), generator=gen).to(DEV) for _ in range(2))
+    tol = 4 * 2.0 ** -24 * 0.43 * 96 ** 0.5
+    _, S = K.kda_linear_chunk_fwd(q, k, v, g, initial_state=h0)
+    err = relative(S, exact_states(k, v, g, h0))
+    say(f"  final state {err:.2e} of {tol:.2e}")
+    assert err <= tol
+    dh0 = K.kda_linear_chunk_bwd(q, k, v, g, do, initial_state=h0, d_final_state=dhT)[3]
+    # G_t adds q_t do_t^T before its decay: the recurrence run from the back, decayed once more at the end
+    lam = torch.exp(g.double())[:, None, None]
+    ref = dhT.double()
+    for t in range(T - 1, -1, -1):
+        ref = lam * (ref + q[:, t].double()[..., None] * do[:, t].double()[..., None, :])
+    err = relative(dh0, ref)
+    say(f"  d_initial_state {err:.2e} of {tol:.2e}")
+    assert err <= tol
