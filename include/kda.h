@@ -284,8 +284,9 @@ int kda_decode_commit(const void *q, const void *k, const void *v, const void *b
  *   - g is device memory and its sign the caller's contract, tested by KDA_DEBUG_VALIDATE;
  *     positive values grow the state instead of failing;
  *   - H <= 32768 (KDA_ERR_UNSUPPORTED).
- * Inputs are finite numbers: an infinity or a NaN in one token may also reach the outputs of other tokens
- * of its sequence within 64 tokens before it (never another sequence's).
+ * Inputs are finite numbers: besides what the formulas give it, an infinity or a NaN in one token may reach
+ * o and dq of its sequence's tokens up to 64 before it, and dk and dv of those up to 64 after it (never
+ * another sequence's).
  *
  * kda_linear_chunk_workspace_size -- workspace bytes of kda_linear_chunk_fwd (backward = 0) or
  * kda_linear_chunk_bwd (backward != 0) for n_seqs sequences of total_tokens tokens (B*T).  May be
