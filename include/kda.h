@@ -41,10 +41,10 @@
  *   - Debug check: with the environment variable KDA_DEBUG_VALIDATE set (to anything but "" or
  *     "0"), kda_chunk_fwd, kda_chunk_fwd_checkpointed and the three decode calls first test those
  *     preconditions on the device (kda_chunk_fwd_gated tests cu_seqlens only: its g is in range
- *     by construction), wait for the answer on `stream` and return KDA_ERR_INVALID_ARGUMENT,
- *     with nothing else enqueued, on a violation.  This synchronises the host, shares one word
- *     of library-owned device memory between all calls on a device (overlapping checked calls
- *     race on it) and must not be used under stream capture.
+ *     by construction; the linear-attention calls test g <= 0 and cu_seqlens), wait for the answer
+ *     on `stream` and return KDA_ERR_INVALID_ARGUMENT, with nothing else enqueued, on a violation.
+ *     This synchronises the host, shares one word of library-owned device memory between all calls
+ *     on a device (overlapping checked calls race on it) and must not be used under stream capture.
  *   - Calls are stateless and reentrant (the debug check aside).
  */
 #ifndef KDA_H
@@ -283,7 +283,8 @@ int kda_decode_commit(const void *q, const void *k, const void *v, const void *b
  *   - the stream must belong to the current device;
  *   - g is device memory and its sign the caller's contract, tested by KDA_DEBUG_VALIDATE;
  *     positive values grow the state instead of failing;
- *   - H <= 32768 (KDA_ERR_UNSUPPORTED).
+ *   - sizes (KDA_ERR_UNSUPPORTED past them): H <= 32768 and n_seqs * H <= 2^21 in the prefill and the
+ *     gradients; N * H < 2^24 in the decode step; N * H * d_k * d_v < 2^36 in the state cache.
  * Inputs are finite numbers: besides what the formulas give it, an infinity or a NaN in one token may reach
  * o and dq of its sequence's tokens up to 64 before it, and dk and dv of those up to 64 after it (never
  * another sequence's).
