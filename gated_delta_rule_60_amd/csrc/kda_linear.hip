@@ -231,10 +231,11 @@ struct ChunkLds {
 //   16-bit inputs: M and the scores are read as two bf16 terms (2^-16); the decayed c as three (exact)
 //   where M ends in a state that is handed out in fp32, as two where it only feeds 16-bit outputs.
 //   fp32 inputs: 16x16x4 fp32 MFMAs throughout.
-//   16-bit outputs leave through LDS as whole rows past the caches (4 x 4096 x 16 heads: 67 us for the
-//   pass, 73 us with each wave's 32-byte pieces stored as they are).
-// Sixteen waves fill a CU (two workgroups; 128 registers and 69 KB of LDS each), and one workgroup's
-// transfers run under the other's products.
+//   16-bit outputs leave through LDS as whole rows past the caches (4 x 4096 x 16 heads, the same inputs over
+//   and over: 67 us for the pass, 73 us with each wave's 32-byte pieces stored as they are).
+// One workgroup's transfers run under another's products.  16-bit inputs, on a CU: DA x DC = 128 x 128 two
+// workgroups of eight waves (128 registers, 69 KB of LDS each), 64 x 128 two (49 KB), 64 x 64 four of four
+// waves (39 KB), 128 x 64 two of four (59 KB, more than 128 registers).
 // STATE_ONLY: just M from zero, the segment's own contribution.
 template <int DT, int ODT, int DA, int DC, bool BACK, bool STATE_ONLY>
 __device__ __forceinline__ void chunk_pass(const Launch& L, const Pass& p, int32_t slot, int32_t h,
@@ -604,8 +605,8 @@ __global__ void __launch_bounds__(DC * 4, DA > DC ? 2 : 4) linear_chunk_kernel(L
 
 // Segment states: from each segment's own contribution to the state it starts from, in place.  Grid
 // (sequence * H + head, element blocks of 1024, pass); each lane carries four elements along, eight
-// segments' loads at a time: 10.4 us for 4 x 4096 x 16 heads (8 segments of 64 KB each), 11.3 us with one
-// load at a time.
+// segments' loads at a time: 10.4 us for 4 x 4096 x 16 heads (8 segments of 64 KB each; the same inputs over
+// and over), 11.3 us with one load at a time.
 __global__ void __launch_bounds__(256) linear_scan_kernel(Launch L, int32_t elems) {
     const Pass& p = L.pass[blockIdx.z];
     const int32_t n = blockIdx.x / L.H, h = blockIdx.x % L.H;
@@ -647,14 +648,21 @@ __global__ void __launch_bounds__(256) linear_scan_kernel(Launch L, int32_t elem
 
 // ---------------------------------------------------------------- host side
 
-// Tokens per segment, a multiple of 64.  Whole sequences where (sequence, head) units alone give every CU a
-// workgroup (16 x 4096 tokens x 16 heads, bf16, d = 128: 337 us whole, 388 us in two segments each; 4 x 4096
-// x 16 in eight segments: 105 us) or where none is long (below 1024 tokens two more launches cost what the
-// shorter chains save).  Else segments for two workgroups a CU, in one round: 512 in all, a few fewer for a
-// packed batch, whose sequences each end in a short one (65536 tokens x 33 heads: 796 us, in 528 segments
-// 1033 us).  No shorter than 256 tokens (fp32, whose chunks take longer: 128), so that a segment's state,
-// read and written about four times, stays small against its rows (16384 x 4 heads, d = 64: 46 us with 256,
-// 62 us with 128).
+// Tokens per segment, a multiple of 64 (figures: bf16, d = 128 unless said otherwise).
+//   Whole sequences from 256 (sequence, head) units on: every CU has a workgroup.  Right for sequences of about
+//   one length: 16 x 4096 tokens x 16 heads 348 us whole, 371 us in two segments each (gradients 763, 881);
+//   packed 8 x 8192 x 32 heads 664 us, 1033 us in segments of 8192 by all tokens (gradients 1573, 2225).  Wrong
+//   for a packed batch of that many units where one sequence holds most tokens -- the lengths are on the device:
+//   8 sequences x 32 heads, one of 55702 of the 65536 tokens, 4028 us whole, 1418 us in segments of 8192
+//   (gradients 8456, 2910); the same tokens as one sequence take 777 us.
+//   Whole, too, below 1024 tokens (of a packed batch: in all).  A call is one launch then, and needs no
+//   workspace, but from 500 tokens on (fp32: from fewer) it is slower than three launches: 500 x 8 heads 32.5 us
+//   whole, 32.7 in segments, 1000 x 8 59.8 and 33.7, fp32 89 and 45, 174 and 47.  Gradients of 4 x 1000 x 16
+//   gain (68.5 and 76.0, fp32 186 and 208).
+//   Else segments for two workgroups a CU, in one round: 512 in all, a few fewer for a packed batch, whose
+//   sequences each end in a short one (65536 tokens x 33 heads: 796 us, in 528 segments 1033 us).  No shorter
+//   than 256 tokens (fp32, whose chunks take longer: 128), so that a segment's state, read and written about
+//   four times, stays small against its rows (16384 x 4 heads, d = 64: 46 us with 256, 62 us with 128).
 int32_t segment_tokens(int32_t n_seqs, int64_t total, int32_t H, int32_t in_dtype, bool packed) {
     const int64_t units = int64_t(n_seqs) * H, longest = packed ? total : total / n_seqs;
     if (units >= 256 || longest < 1024) return WHOLE;
@@ -777,7 +785,7 @@ namespace {
 
 // One workgroup per (sequence, head): the state is read once, updated in registers and written once
 // (non-temporal both ways: a step touches it once).  Lane t owns four columns of DK / RG rows.  Bound by
-// HBM: 256 x 32 states of 128 x 128 in 173 us, 6.2 TB/s (a large copy reaches 4.95); one sequence of 32
+// HBM: 256 x 32 states of 128 x 128 in 176 us, 6.1 TB/s (a large copy reaches 4.92); one sequence of 32
 // heads in 3.8 us.
 template <int DT, int ODT, int DK, int DV>
 __global__ void __launch_bounds__(256) linear_decode_kernel(const void* __restrict__ q, const void* __restrict__ k,

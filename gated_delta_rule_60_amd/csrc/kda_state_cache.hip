@@ -79,8 +79,11 @@ __device__ __forceinline__ float4 decode4(uint32_t w) {
 }
 
 // One workgroup: ROUNDS blocks of 4096 elements of one sequence's states (or what is left of them).  Every
-// workgroup looks through the later sequences for its slot, so where there are many, one takes four blocks
-// (16384 sequences of 2 x 64 x 64: 155 us, 206 us with one; 1024 of 32 x 128 x 128: 551 us, 503 us with one).
+// workgroup looks through the later sequences for its slot, so where there are many, one takes four blocks;
+// where there are few, four blocks only leave the chip unevenly filled.  Four and one, in us, by sequences:
+//     2 x 64 x 64     512: 8.8, 8.1    1024: 11.9, 11.4   2048: 20.4, 22.0   16384: 159, 202
+//     8 x 128 x 128   512: 65, 64      1024: 123, 125     2048: 252, 269     16384: 2275, 3018
+//     32 x 128 x 128  512: 254, 251    1024: 547, 525     2048: 1095, 1070   4096: 2178, 2233
 template <int CODE, int GROUP, int ROUNDS>
 __global__ void __launch_bounds__(256, 8) store_kernel(const float* __restrict__ states, const int32_t* __restrict__ slots,
                                                        uint8_t* __restrict__ codes, float* __restrict__ scales,

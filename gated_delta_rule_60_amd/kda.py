@@ -546,7 +546,8 @@ def kda_linear_chunk_fwd(q, k, v, g, initial_state=None, final_state=None, cu_se
     """Chunked prefill of linear attention, S_t = e^g S_{t-1} + k_t v_t^T, o_t = scale S_t^T q_t:
     q, k [B, T, H, dk]; v [B, T, H, dv]; g [H] fp32 log-decay (<= 0); initial_state
     [N, H, dk, dv] fp32 or None; cu_seqlens device int32 [N+1] or None (B == 1).  Returns
-    (o, final_state); final_state is allocated when output_final_state and not given."""
+    (o, final_state); final_state is allocated when output_final_state and not given.  Not recorded by
+    autograd: gradients come from kda_linear_chunk_bwd."""
     fn = "kda_linear_chunk_fwd"
     B, T, N, H, dk, dv, dev = _check_linear(
         fn, q, k, v, g, cu_seqlens, workspace,
