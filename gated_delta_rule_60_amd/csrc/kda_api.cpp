@@ -5,34 +5,16 @@
 #include <cmath>
 #include <cstdint>
 #include <initializer_list>
-#include <limits>
 #include <mutex>
 
 #include "../../include/kda.h"
+#include "kda_api_util.hpp"
 #include "kda_internal.hpp"
 #include "kda_linear.hpp"
 
 namespace {
 
 constexpr int kVersion = 300;  // 0.3.0
-
-bool valid_dtype(int dt) { return dt == KDA_F32 || dt == KDA_BF16; }
-int64_t esize(int dt) { return dt == KDA_F32 ? 4 : 2; }
-bool supported_d(int32_t d) { return d == 64 || d == 128; }
-
-struct Range {
-    uintptr_t lo, hi;  // [lo, hi)
-};
-Range range(const void* p, int64_t bytes) {
-    const uintptr_t a = reinterpret_cast<uintptr_t>(p);
-    return Range{a, a + static_cast<uintptr_t>(bytes > 0 ? bytes : 0)};
-}
-bool overlap(Range a, Range b) {
-    if (a.lo == a.hi || b.lo == b.hi) return false;
-    return a.lo < b.hi && b.lo < a.hi;
-}
-
-kda_status from_hip(hipError_t e) { return e == hipSuccess ? KDA_OK : KDA_ERR_HIP; }
 
 // ---- the prefill workspace of kda_chunk_fwd_gated_noalloc: a static device array ------------
 // Each GPU the library runs on holds its own copy from the first use on that device until the
@@ -351,28 +333,6 @@ size_t kda_linear_chunk_workspace_size(int32_t n_seqs, int64_t total_tokens, int
 
 namespace {
 
-bool aligned16(std::initializer_list<const void*> ps) {
-    for (const void* p : ps)
-        if (reinterpret_cast<uintptr_t>(p) % 16 != 0) return false;
-    return true;
-}
-bool aligned4(std::initializer_list<const void*> ps) {
-    for (const void* p : ps)
-        if (reinterpret_cast<uintptr_t>(p) % 4 != 0) return false;
-    return true;
-}
-
-// No output overlaps an input or another output.
-bool disjoint(std::initializer_list<Range> outs, std::initializer_list<Range> ins) {
-    for (const Range* a = outs.begin(); a != outs.end(); ++a) {
-        for (const Range* b = a + 1; b != outs.end(); ++b)
-            if (overlap(*a, *b)) return false;
-        for (const Range& b : ins)
-            if (overlap(*a, b)) return false;
-    }
-    return true;
-}
-
 // Checks the forward and the backward share; KDA_OK, or the status to return.
 int linear_sizes(int in_dtype, const int32_t* cu, int32_t B, int64_t T, int32_t n_seqs, int32_t H,
                  int32_t dk, int32_t dv, float scale) {
@@ -387,16 +347,6 @@ int linear_sizes(int in_dtype, const int32_t* cu, int32_t B, int64_t T, int32_t 
     // a grid of 256-lane workgroups (up to six per (sequence, head)) must stay within 2^32 lanes
     if (int64_t(n_seqs) * H > (int64_t(1) << 21)) return KDA_ERR_UNSUPPORTED;
     return KDA_OK;
-}
-
-// The debug check of g and cu_seqlens; KDA_OK with the check off.
-int linear_debug(const float* g, const int32_t* cu, int32_t n_seqs, int64_t ntok, int32_t H, void* stream) {
-    if (!kda::debug_validation_enabled() || ntok == 0) return KDA_OK;
-    bool ok = true;
-    if (kda::debug_validate_from(-std::numeric_limits<float>::infinity(), g, KDA_F32, H, cu, n_seqs, ntok,
-                                 static_cast<hipStream_t>(stream), &ok) != hipSuccess)
-        return KDA_ERR_HIP;
-    return ok ? KDA_OK : KDA_ERR_INVALID_ARGUMENT;
 }
 
 int state_cache_check(const float* states, const int32_t* slots, const void* codes, int code,
