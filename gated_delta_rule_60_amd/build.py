@@ -8,7 +8,8 @@ import sys
 _HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(_HERE, "csrc")
 SOURCES = ["kda_api.cpp", "kda_gate.hip", "kda_decode.hip", "kda_chunk.hip", "kda_fused.hip",
-           "kda_validate.hip", "kda_linear.hip", "kda_state_cache.hip"]
+           "kda_validate.hip", "kda_linear.hip", "kda_state_cache.hip", "kda_api_ssm.cpp",
+           "kda_conv.hip", "kda_scan.hip", "kda_slots.hip"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
 # Packed-fp32 VALU forms are disabled for all device code; hipcc's host pass warns that it does

@@ -88,6 +88,31 @@ def load_library(path: Optional[str] = None):
     lib.kda_state_store.restype = ctypes.c_int
     lib.kda_state_load.argtypes = [vp, ctypes.c_int, vp, vp, vp, i32, i32, i32, i32, i32, i32, vp]
     lib.kda_state_load.restype = ctypes.c_int
+    ci = ctypes.c_int
+    signatures = {
+        "kda_conv_bwd_workspace_size": [i32, i64, i32, i32],
+        "kda_conv_fwd": [vp, i64, ci, vp, vp, vp, vp, vp, vp, i64, i32, i64, i32, i32, i32, ci, vp],
+        "kda_conv_bwd": [vp, i64, ci, vp, vp, vp, vp, vp, i64, vp, vp, i64, vp, vp, vp, i32, i64, i32, i32,
+                         i32, ci, vp, sz, vp],
+        "kda_conv_step": [vp, i64, ci, vp, vp, vp, vp, vp, i64, i32, i32, i32, i32, ci, vp],
+        "kda_ssm_chunk_workspace_size": [i32, i64, i32, i32, i32, i32, ci, ci],
+        "kda_ssm_chunk_fwd": [vp, i64, vp, i64, vp, i64, vp, i64, ci, vp, vp, vp, vp, vp, vp, vp, i64, ci,
+                              i32, i64, i32, i32, i32, i32, i32, vp, sz, vp],
+        "kda_ssm_chunk_bwd": [vp, i64, vp, i64, vp, i64, vp, i64, ci, vp, vp, vp, vp, vp, vp, i64, vp, vp,
+                              i64, vp, i64, vp, i64, vp, i64, vp, vp, vp, vp, i32, i64, i32, i32, i32, i32,
+                              i32, vp, sz, vp],
+        "kda_ssm_decode_step": [vp, i64, vp, i64, vp, i64, vp, i64, ci, vp, vp, vp, vp, vp, vp, i64, ci,
+                                i32, i32, i32, i32, i32, i32, vp],
+        "kda_slots_workspace_size": [i32, i32],
+        "kda_slots_copy": [vp, vp, vp, i32, vp, vp, i32, i32, i32, vp],
+        "kda_slots_retain": [vp, vp, i32, i32, vp],
+        "kda_slots_release": [vp, vp, i32, i32, vp],
+        "kda_slots_fork": [vp, vp, i32, vp, vp, vp, i32, i32, vp, sz, vp],
+        "kda_slots_compact": [vp, vp, i32, vp, vp, i64, vp, i32, vp, sz, vp],
+    }
+    for name, argtypes in signatures.items():
+        getattr(lib, name).argtypes = argtypes
+        getattr(lib, name).restype = sz if name.endswith("_workspace_size") else ci
     if path == lib_path():
         _lib = lib
     return lib
@@ -97,7 +122,11 @@ EXPORTED = ["kda_status_string", "kda_version", "kda_gate", "kda_chunk_fwd_works
             "kda_chunk_fwd", "kda_chunk_fwd_gated", "kda_chunk_fwd_gated_noalloc",
             "kda_chunk_fwd_checkpointed", "kda_decode_step", "kda_decode_verify",
             "kda_decode_commit", "kda_linear_chunk_workspace_size", "kda_linear_chunk_fwd",
-            "kda_linear_chunk_bwd", "kda_linear_decode_step", "kda_state_store", "kda_state_load"]
+            "kda_linear_chunk_bwd", "kda_linear_decode_step", "kda_state_store", "kda_state_load",
+            "kda_conv_bwd_workspace_size", "kda_conv_fwd", "kda_conv_bwd", "kda_conv_step",
+            "kda_ssm_chunk_workspace_size", "kda_ssm_chunk_fwd", "kda_ssm_chunk_bwd",
+            "kda_ssm_decode_step", "kda_slots_workspace_size", "kda_slots_copy", "kda_slots_retain",
+            "kda_slots_release", "kda_slots_fork", "kda_slots_compact"]
 
 # Size of the library's static prefill workspace used by kda_chunk_fwd_gated_noalloc.
 NOALLOC_SCRATCH_BYTES = 256 << 20
@@ -688,3 +717,414 @@ def kda_state_load(codes, scales, slots=None, states=None, stream=None):
     _launch(fn, dev, load_library().kda_state_load, _addr(codes), _CODES[codes.dtype],
             _addr(scales), _addr(slots), _addr(states), N, n_slots, H, dk, dv, group, sp)
     return states
+
+
+# ---- rows of tokens that may be parts of wider rows ---------------------------------------------
+
+def _rows(fn, name, t, shape, dtype, lead):
+    """Elements from one token's row of t to the next: t has the given shape, its first `lead`
+    dimensions count tokens, the others are contiguous."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{fn}: {name} must be a torch.Tensor")
+    if t.shape != shape:
+        raise ValueError(f"{fn}: {name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.dtype is not dtype:
+        raise ValueError(f"{fn}: {name} must be {dtype}, got {t.dtype}")
+    row = 1
+    for n in shape[lead:]:
+        row *= n
+    if t.is_contiguous():
+        return row
+    strides, want = t.stride(), 1
+    for d in range(len(shape) - 1, lead - 1, -1):
+        if shape[d] != 1 and strides[d] != want:
+            raise ValueError(f"{fn}: {name}'s rows must be contiguous")
+        want *= shape[d]
+    ld, tokens = None, 1
+    for d in range(lead - 1, -1, -1):
+        if shape[d] != 1:
+            if ld is None:
+                ld = strides[d]
+            elif strides[d] != ld * tokens:
+                raise ValueError(f"{fn}: {name}'s tokens must be evenly spaced")
+        tokens *= shape[d]
+    if ld is None or tokens == 0:
+        return row
+    if ld < row:
+        raise ValueError(f"{fn}: {name}'s rows must not overlap")
+    return ld
+
+
+def _float_dtype(fn, name, t):
+    if not isinstance(t, torch.Tensor) or t.dtype not in _FLOATS:
+        raise TypeError(f"{fn}: {name} must be a float32 or bfloat16 tensor")
+    return t.dtype
+
+
+def _sequences(fn, B, cu_seqlens):
+    """Sequences of a batch of B rows of tokens, or of a packed one."""
+    if cu_seqlens is None:
+        return B
+    if B != 1:
+        raise ValueError(f"{fn}: cu_seqlens needs B == 1 (a packed batch)")
+    _expect(fn, "cu_seqlens", cu_seqlens, (None,), (torch.int32,))
+    if cu_seqlens.numel() < 2:
+        raise ValueError(f"{fn}: cu_seqlens needs at least two offsets")
+    return cu_seqlens.numel() - 1
+
+
+def _bytes_of(fn, ts, workspace, need, dev):
+    """The workspace (allocated on `ts` where none is given and one is needed) and its bytes."""
+    if workspace is None:
+        if need == 0:
+            return None, 0
+        workspace = _alloc(ts, (need,), torch.uint8, dev)
+    elif not workspace.is_contiguous():
+        raise ValueError(f"{fn}: workspace must be contiguous")
+    return workspace, workspace.numel() * workspace.element_size()
+
+
+# ---- short convolution --------------------------------------------------------------------------
+
+def _check_conv(fn, x, weight, bias, cu_seqlens, like_x, windows):
+    """Sizes and strides of a convolution's prompt calls: (B, T, N, C, W, ldx, strides of like_x)."""
+    dt = _float_dtype(fn, "x", x)
+    if x.dim() != 3:
+        raise ValueError(f"{fn}: x must be a [B, T, C] tensor")
+    B, T, C = x.shape
+    ldx = _rows(fn, "x", x, (B, T, C), dt, 2)
+    _expect(fn, "weight", weight, (C, None), (torch.float32,))
+    _expect(fn, "bias", bias, (C,), (torch.float32,))
+    W = weight.shape[1]
+    N = _sequences(fn, B, cu_seqlens)
+    lds = [ldx if t is None else _rows(fn, name, t, (B, T, C), dt, 2) for name, t in like_x.items()]
+    for name, t in windows.items():
+        _expect(fn, name, t, (N, W - 1, C), (dt,))
+    return B, T, N, C, W, ldx, lds
+
+
+def kda_conv_fwd(x, weight, bias=None, initial_state=None, final_state=None, cu_seqlens=None, y=None,
+                 silu: bool = True, output_final_state: bool = False, stream=None):
+    """Short causal convolution of every channel, u_t = bias + sum_i weight[:, i] x_{t-W+1+i} and
+    y = silu(u) (or u): x [B, T, C], whose rows may be parts of wider ones; weight [C, W] fp32 with W
+    2, 3 or 4; bias [C] fp32 or None; initial_state [N, W-1, C] in x's dtype or None (zeros); cu_seqlens
+    device int32 [N+1] or None (B == 1).  Returns (y, final_state), the latter the last W - 1
+    inputs, allocated when output_final_state and not given.  Not recorded by autograd: gradients come
+    from kda_conv_bwd."""
+    fn = "kda_conv_fwd"
+    B, T, N, C, W, ldx, (ldy,) = _check_conv(
+        fn, x, weight, bias, cu_seqlens, dict(y=y),
+        dict(initial_state=initial_state, final_state=final_state))
+    dev = _one_device(fn, x=x, weight=weight, bias=bias, initial_state=initial_state,
+                      final_state=final_state, cu_seqlens=cu_seqlens, y=y)
+    ts, sp = _launch_stream(stream, dev)
+    if y is None:
+        y, ldy = _alloc(ts, (B, T, C), x.dtype, dev), C
+    if final_state is None and output_final_state:
+        final_state = _alloc(ts, (N, W - 1, C), x.dtype, dev)
+    _launch(fn, dev, load_library().kda_conv_fwd, _addr(x), ldx, _dt(x), _addr(weight), _addr(bias),
+            _addr(initial_state), _addr(final_state), _addr(cu_seqlens), _addr(y), ldy, B, T, N, C, W,
+            int(silu), sp)
+    return y, final_state
+
+
+def kda_conv_bwd_workspace_size(n_seqs: int, total_tokens: int, C: int, W: int) -> int:
+    return int(load_library().kda_conv_bwd_workspace_size(n_seqs, total_tokens, C, W))
+
+
+def kda_conv_bwd(x, weight, dy, bias=None, initial_state=None, d_final_state=None, cu_seqlens=None,
+                 silu: bool = True, dx=None, output_d_initial_state: Optional[bool] = None,
+                 workspace=None, stream=None):
+    """Gradients of kda_conv_fwd: dy [B, T, C] and d_final_state [N, W-1, C] (or None: zeros) in x's
+    dtype, the other inputs as there.  Returns (dx, d_weight, d_bias, d_initial_state); d_bias is
+    None without a bias, d_initial_state is formed when output_d_initial_state (default: when
+    initial_state is given)."""
+    fn = "kda_conv_bwd"
+    if not isinstance(dy, torch.Tensor):
+        raise TypeError(f"{fn}: dy must be a torch.Tensor")
+    B, T, N, C, W, ldx, (lddy, lddx) = _check_conv(
+        fn, x, weight, bias, cu_seqlens, dict(dy=dy, dx=dx),
+        dict(initial_state=initial_state, d_final_state=d_final_state))
+    dev = _one_device(fn, x=x, weight=weight, dy=dy, bias=bias, initial_state=initial_state,
+                      d_final_state=d_final_state, cu_seqlens=cu_seqlens, dx=dx, workspace=workspace)
+    ts, sp = _launch_stream(stream, dev)
+    if dx is None:
+        dx, lddx = _alloc(ts, (B, T, C), x.dtype, dev), C
+    d_weight = _alloc(ts, (C, W), torch.float32, dev)
+    d_bias = None if bias is None else _alloc(ts, (C,), torch.float32, dev)
+    if output_d_initial_state is None:
+        output_d_initial_state = initial_state is not None
+    dh0 = _alloc(ts, (N, W - 1, C), x.dtype, dev) if output_d_initial_state else None
+    workspace, ws_bytes = _bytes_of(fn, ts, workspace, kda_conv_bwd_workspace_size(N, B * T, C, W), dev)
+    _launch(fn, dev, load_library().kda_conv_bwd, _addr(x), ldx, _dt(x), _addr(weight), _addr(bias),
+            _addr(initial_state), _addr(cu_seqlens), _addr(dy), lddy, _addr(d_final_state), _addr(dx), lddx,
+            _addr(d_weight), _addr(d_bias), _addr(dh0), B, T, N, C, W, int(silu), _addr(workspace),
+            ws_bytes, sp)
+    return dx, d_weight, d_bias, dh0
+
+
+def kda_conv_step(x, weight, windows, bias=None, slots=None, y=None, silu: bool = True, stream=None):
+    """One token of kda_conv_fwd for N sequences: x [N, C]; windows [n_slots, W-1, C] in x's dtype, moved
+    on in place; slots device int32 [N] or None (sequence n in slot n).  Sequences whose slot lies
+    outside the pool, and all but the last with one slot, are skipped and get zeros.  Returns y [N, C]."""
+    fn = "kda_conv_step"
+    dt = _float_dtype(fn, "x", x)
+    if x.dim() != 2:
+        raise ValueError(f"{fn}: x must be a [N, C] tensor")
+    N, C = x.shape
+    ldx = _rows(fn, "x", x, (N, C), dt, 1)
+    _expect(fn, "weight", weight, (C, None), (torch.float32,))
+    W = weight.shape[1]
+    _expect(fn, "windows", windows, (None, W - 1, C), (dt,))
+    _expect(fn, "bias", bias, (C,), (torch.float32,))
+    _expect(fn, "slots", slots, (N,), (torch.int32,))
+    ldy = C if y is None else _rows(fn, "y", y, (N, C), dt, 1)
+    dev = _one_device(fn, x=x, weight=weight, windows=windows, bias=bias, slots=slots, y=y)
+    ts, sp = _launch_stream(stream, dev)
+    if y is None:
+        y = _alloc(ts, (N, C), dt, dev)
+    _launch(fn, dev, load_library().kda_conv_step, _addr(x), ldx, _DT[dt], _addr(weight), _addr(bias),
+            _addr(windows), _addr(slots), _addr(y), ldy, N, windows.shape[0], C, W, int(silu), sp)
+    return y
+
+
+# ---- selective state space scan -----------------------------------------------------------------
+
+def kda_ssm_chunk_workspace_size(n_seqs: int, total_tokens: int, H: int, G: int, dk: int, dv: int,
+                                 in_dtype: torch.dtype = torch.bfloat16, backward: bool = False) -> int:
+    return int(load_library().kda_ssm_chunk_workspace_size(n_seqs, total_tokens, H, G, dk, dv,
+                                                           _DT[in_dtype], int(backward)))
+
+
+def _check_ssm(fn, x, dt, A, B, C, D, dt_bias, lead):
+    """Sizes and strides of a scan's inputs, `lead` dimensions of tokens: (tokens' sizes, H, G, dk, dv,
+    strides of x, dt, B, C)."""
+    ty = _float_dtype(fn, "x", x)
+    if x.dim() != lead + 2:
+        raise ValueError(f"{fn}: x must be a {'[B, T, H, dv]' if lead == 2 else '[N, H, dv]'} tensor")
+    if not isinstance(B, torch.Tensor) or B.dim() != lead + 2:
+        raise ValueError(f"{fn}: B must be a {'[B, T, G, dk]' if lead == 2 else '[N, G, dk]'} tensor")
+    tok, (H, dv), (G, dk) = tuple(x.shape[:lead]), x.shape[lead:], B.shape[lead:]
+    if G < 1 or H % G != 0:
+        raise ValueError(f"{fn}: G = {G} must divide H = {H}")
+    lds = (_rows(fn, "x", x, tok + (H, dv), ty, lead), _rows(fn, "dt", dt, tok + (H,), ty, lead),
+           _rows(fn, "B", B, tok + (G, dk), ty, lead), _rows(fn, "C", C, tok + (G, dk), ty, lead))
+    _expect(fn, "A", A, (H,), (torch.float32,))
+    _expect(fn, "D", D, (H,), (torch.float32,))
+    _expect(fn, "dt_bias", dt_bias, (H,), (torch.float32,))
+    return tok, H, G, dk, dv, lds
+
+
+def kda_ssm_chunk_fwd(x, dt, A, B, C, D=None, dt_bias=None, initial_state=None, final_state=None,
+                      cu_seqlens=None, y=None, y_dtype=None, output_final_state: bool = True,
+                      workspace=None, stream=None):
+    """Chunked prefill of the selective state space scan: with delta = softplus(dt + dt_bias),
+    S_t = e^(delta_t A) S_{t-1} + delta_t B_t x_t^T and y_t = S_t^T C_t + D x_t.  x [B, T, H, dv];
+    dt [B, T, H]; B, C [B, T, G, dk] (head h uses group h // (H // G)), whose rows may be parts of wider
+    ones; A (<= 0), D, dt_bias [H] fp32, the latter two may be None; initial_state [N, H, dk, dv]
+    fp32 or None; cu_seqlens device int32 [N+1] or None (B == 1).  Returns (y, final_state);
+    final_state is allocated when output_final_state and not given.  Not recorded by autograd:
+    gradients come from kda_ssm_chunk_bwd."""
+    fn = "kda_ssm_chunk_fwd"
+    (nb, T), H, G, dk, dv, (ldx, lddt, ldb, ldc) = _check_ssm(fn, x, dt, A, B, C, D, dt_bias, 2)
+    N = _sequences(fn, nb, cu_seqlens)
+    for name, t in (("initial_state", initial_state), ("final_state", final_state)):
+        _expect(fn, name, t, (N, H, dk, dv), (torch.float32,))
+    ldy = H * dv if y is None else _rows(fn, "y", y, (nb, T, H, dv), _float_dtype(fn, "y", y), 2)
+    dev = _one_device(fn, x=x, dt=dt, A=A, B=B, C=C, D=D, dt_bias=dt_bias, initial_state=initial_state,
+                      final_state=final_state, cu_seqlens=cu_seqlens, y=y, workspace=workspace)
+    ts, sp = _launch_stream(stream, dev)
+    if y is None:
+        y = _alloc(ts, (nb, T, H, dv), y_dtype or x.dtype, dev)
+    if final_state is None and output_final_state:
+        final_state = _alloc(ts, (N, H, dk, dv), torch.float32, dev)
+    workspace, ws_bytes = _bytes_of(fn, ts, workspace, 0 if workspace is not None else
+                                    kda_ssm_chunk_workspace_size(N, nb * T, H, G, dk, dv, x.dtype), dev)
+    _launch(fn, dev, load_library().kda_ssm_chunk_fwd, _addr(x), ldx, _addr(dt), lddt, _addr(B), ldb,
+            _addr(C), ldc, _dt(x), _addr(A), _addr(dt_bias), _addr(D), _addr(initial_state),
+            _addr(final_state), _addr(cu_seqlens), _addr(y), ldy, _dt(y), nb, T, N, H, G, dk, dv,
+            _addr(workspace), ws_bytes, sp)
+    return y, final_state
+
+
+def kda_ssm_chunk_bwd(x, dt, A, B, C, dy, D=None, dt_bias=None, initial_state=None, d_final_state=None,
+                      cu_seqlens=None, dx=None, ddt=None, dB=None, dC=None, d_initial_state=None,
+                      output_d_initial_state: Optional[bool] = None, workspace=None, stream=None):
+    """Gradients of kda_ssm_chunk_fwd: dy [B, T, H, dv] in x's dtype, d_final_state [N, H, dk, dv] fp32
+    or None (zeros), the other inputs as there; dx, ddt, dB, dC may be given (parts of wider rows, say).
+    Returns (dx, ddt, dA, dB, dC, dD, d_dt_bias, d_initial_state); dD and d_dt_bias are None without
+    D and dt_bias, d_initial_state is formed when output_d_initial_state (default: when initial_state
+    is given) or given."""
+    fn = "kda_ssm_chunk_bwd"
+    (nb, T), H, G, dk, dv, (ldx, lddt, ldb, ldc) = _check_ssm(fn, x, dt, A, B, C, D, dt_bias, 2)
+    N, ty = _sequences(fn, nb, cu_seqlens), x.dtype
+    lddy = _rows(fn, "dy", dy, (nb, T, H, dv), ty, 2)
+    for name, t in (("initial_state", initial_state), ("d_final_state", d_final_state),
+                    ("d_initial_state", d_initial_state)):
+        _expect(fn, name, t, (N, H, dk, dv), (torch.float32,))
+    dev = _one_device(fn, x=x, dt=dt, A=A, B=B, C=C, dy=dy, D=D, dt_bias=dt_bias,
+                      initial_state=initial_state, d_final_state=d_final_state, cu_seqlens=cu_seqlens,
+                      dx=dx, ddt=ddt, dB=dB, dC=dC, d_initial_state=d_initial_state, workspace=workspace)
+    ts, sp = _launch_stream(stream, dev)
+    outs = []
+    for name, t, like in (("dx", dx, x), ("ddt", ddt, dt), ("dB", dB, B), ("dC", dC, C)):
+        if t is None:
+            t = _alloc(ts, like.shape, ty, dev)
+        outs.append((t, _rows(fn, name, t, like.shape, ty, 2)))
+    (dx, lddx), (ddt, ldddt), (dB, lddb), (dC, lddc) = outs
+    heads = _alloc(ts, (3, H), torch.float32, dev)
+    dA, dD, dbias = heads[0], None if D is None else heads[1], None if dt_bias is None else heads[2]
+    if output_d_initial_state is None:
+        output_d_initial_state = initial_state is not None
+    if d_initial_state is None and output_d_initial_state:
+        d_initial_state = _alloc(ts, (N, H, dk, dv), torch.float32, dev)
+    workspace, ws_bytes = _bytes_of(fn, ts, workspace, 0 if workspace is not None else
+                                    kda_ssm_chunk_workspace_size(N, nb * T, H, G, dk, dv, ty, True), dev)
+    _launch(fn, dev, load_library().kda_ssm_chunk_bwd, _addr(x), ldx, _addr(dt), lddt, _addr(B), ldb,
+            _addr(C), ldc, _dt(x), _addr(A), _addr(dt_bias), _addr(D), _addr(initial_state),
+            _addr(cu_seqlens), _addr(dy), lddy, _addr(d_final_state), _addr(dx), lddx, _addr(ddt), ldddt,
+            _addr(dB), lddb, _addr(dC), lddc, _addr(dA), _addr(dD), _addr(dbias), _addr(d_initial_state),
+            nb, T, N, H, G, dk, dv, _addr(workspace), ws_bytes, sp)
+    return dx, ddt, dA, dB, dC, dD, dbias, d_initial_state
+
+
+def kda_ssm_decode_step(x, dt, A, B, C, state, D=None, dt_bias=None, slots=None, y=None, y_dtype=None,
+                        stream=None):
+    """One token of the selective scan for N sequences: x [N, H, dv]; dt [N, H]; B, C [N, G, dk]; A, D,
+    dt_bias [H] fp32; state [n_slots, H, dk, dv] fp32 updated in place; slots device int32 [N] or None
+    (sequence n in slot n).  Sequences whose slot lies outside the pool, and all but the last with one
+    slot, are skipped and get zeros.  Returns y [N, H, dv]."""
+    fn = "kda_ssm_decode_step"
+    (N,), H, G, dk, dv, (ldx, lddt, ldb, ldc) = _check_ssm(fn, x, dt, A, B, C, D, dt_bias, 1)
+    _expect(fn, "state", state, (None, H, dk, dv), (torch.float32,))
+    _expect(fn, "slots", slots, (N,), (torch.int32,))
+    ldy = H * dv if y is None else _rows(fn, "y", y, (N, H, dv), _float_dtype(fn, "y", y), 1)
+    dev = _one_device(fn, x=x, dt=dt, A=A, B=B, C=C, state=state, D=D, dt_bias=dt_bias, slots=slots, y=y)
+    ts, sp = _launch_stream(stream, dev)
+    if y is None:
+        y = _alloc(ts, (N, H, dv), y_dtype or x.dtype, dev)
+    _launch(fn, dev, load_library().kda_ssm_decode_step, _addr(x), ldx, _addr(dt), lddt, _addr(B), ldb,
+            _addr(C), ldc, _dt(x), _addr(A), _addr(dt_bias), _addr(D), _addr(state), _addr(slots),
+            _addr(y), ldy, _dt(y), N, state.shape[0], H, G, dk, dv, sp)
+    return y
+
+
+# ---- slot pools ---------------------------------------------------------------------------------
+
+def _planes(fn, name, pool):
+    """(number of slots, addresses, bytes of a slot, number of planes) of a pool: a tensor or a list of
+    up to four, each with the slots as its first dimension."""
+    pool = [pool] if isinstance(pool, torch.Tensor) else list(pool)
+    if not 1 <= len(pool) <= 4:
+        raise ValueError(f"{fn}: {name} must be one to four tensors")
+    n_slots = None
+    for t in pool:
+        if not isinstance(t, torch.Tensor) or t.dim() < 1 or not t.is_contiguous():
+            raise ValueError(f"{fn}: {name} must hold contiguous tensors [n_slots, ...]")
+        if n_slots is None:
+            n_slots = t.shape[0]
+        elif t.shape[0] != n_slots:
+            raise ValueError(f"{fn}: the planes of {name} must have one number of slots")
+    if n_slots < 1 or any(t.numel() == 0 for t in pool):
+        raise ValueError(f"{fn}: the planes of {name} must not be empty")
+    addresses = (ctypes.c_void_p * len(pool))(*[t.data_ptr() for t in pool])
+    sizes = (ctypes.c_int64 * len(pool))(*[t.numel() // n_slots * t.element_size() for t in pool])
+    return pool, n_slots, addresses, sizes
+
+
+def _pool_device(fn, pool, **named):
+    return _one_device(fn, **{f"plane {i}": t for i, t in enumerate(pool)}, **named)
+
+
+def kda_slots_workspace_size(n_slots: int, N: int = 0) -> int:
+    return int(load_library().kda_slots_workspace_size(n_slots, N))
+
+
+def kda_slots_copy(src, dst, src_slots=None, dst_slots=None, stream=None):
+    """dst[dst_slots[n]] = src[src_slots[n]] for two pools that do not overlap (each a tensor or a list of
+    up to four, slots first; the same sizes per slot), device int32 lists or None (pair n has slot n).
+    A source outside its pool gives zeros, a destination outside is skipped, of several pairs with
+    one destination the last is taken.  Returns dst."""
+    fn = "kda_slots_copy"
+    src_, n_src, sa, sb = _planes(fn, "src", src)
+    dst_, n_dst, da, db = _planes(fn, "dst", dst)
+    if list(sb) != list(db):
+        raise ValueError(f"{fn}: src and dst must have the same planes per slot")
+    _expect(fn, "src_slots", src_slots, (None,), (torch.int32,))
+    _expect(fn, "dst_slots", dst_slots, (None,), (torch.int32,))
+    lists = [t.numel() for t in (src_slots, dst_slots) if t is not None]
+    if len(lists) == 2 and lists[0] != lists[1]:
+        raise ValueError(f"{fn}: src_slots and dst_slots must have one length")
+    N = lists[0] if lists else min(n_src, n_dst)
+    dev = _pool_device(fn, src_ + dst_, src_slots=src_slots, dst_slots=dst_slots)
+    _, sp = _launch_stream(stream, dev)
+    _launch(fn, dev, load_library().kda_slots_copy, sa, da, sb, len(src_), _addr(src_slots), _addr(dst_slots),
+            N, n_src, n_dst, sp)
+    return dst
+
+
+def _count(fn, refs, slots, stream):
+    _expect(fn, "refs", refs, (None,), (torch.int32,))
+    _expect(fn, "slots", slots, (None,), (torch.int32,))
+    dev = _one_device(fn, refs=refs, slots=slots)
+    _, sp = _launch_stream(stream, dev)
+    _launch(fn, dev, getattr(load_library(), fn), _addr(refs), _addr(slots), slots.numel(), refs.numel(), sp)
+    return refs
+
+
+def kda_slots_retain(refs, slots, stream=None):
+    """One more user of every listed slot (device int32) that is in use; refs int32 [n_slots], the users
+    of each slot, is updated in place.  Returns refs."""
+    return _count("kda_slots_retain", refs, slots, stream)
+
+
+def kda_slots_release(refs, slots, stream=None):
+    """One user less of every listed slot (device int32); a slot without users is free.  Returns refs."""
+    return _count("kda_slots_release", refs, slots, stream)
+
+
+def kda_slots_fork(pool, refs, parents, children=None, workspace=None, stream=None):
+    """For each of parents (device int32 [N], or a number: N new sequences) the lowest free slots of the
+    pool (a tensor or a list of up to four, slots first), in order, with the parent's contents --
+    zeros without a parent, or for one that is free -- and one user in refs (int32 [n_slots], updated
+    in place).  Returns children, int32 [N], -1 where no slot was left."""
+    fn = "kda_slots_fork"
+    pool, n_slots, pa, pb = _planes(fn, "pool", pool)
+    new = isinstance(parents, int)
+    N = parents if new else None
+    if not new:
+        if not isinstance(parents, torch.Tensor):
+            raise TypeError(f"{fn}: parents must be an int32 tensor or a number")
+        _expect(fn, "parents", parents, (None,), (torch.int32,))
+        N = parents.numel()
+    _expect(fn, "refs", refs, (n_slots,), (torch.int32,))
+    _expect(fn, "children", children, (N,), (torch.int32,))
+    dev = _pool_device(fn, pool, refs=refs, parents=None if new else parents, children=children,
+                       workspace=workspace)
+    ts, sp = _launch_stream(stream, dev)
+    if children is None:
+        children = _alloc(ts, (N,), torch.int32, dev)
+    workspace, ws_bytes = _bytes_of(fn, ts, workspace, kda_slots_workspace_size(n_slots, N), dev)
+    _launch(fn, dev, load_library().kda_slots_fork, pa, pb, len(pool), _addr(refs),
+            None if new else _addr(parents), _addr(children), N, n_slots, _addr(workspace), ws_bytes, sp)
+    return children
+
+
+def kda_slots_compact(pool, refs, table=None, used=None, workspace=None, stream=None):
+    """Moves the used slots of the pool together: with U of them, those from U on go to the free ones
+    before U, both in order; refs (int32 [n_slots]) goes along, table (int32, slot numbers, or None) is
+    rewritten in place, -1 where it named no used slot.  Returns U, an int32 tensor of one element."""
+    fn = "kda_slots_compact"
+    pool, n_slots, pa, pb = _planes(fn, "pool", pool)
+    _expect(fn, "refs", refs, (n_slots,), (torch.int32,))
+    if table is not None:
+        _expect(fn, "table", table, tuple(table.shape) if isinstance(table, torch.Tensor) else (), (torch.int32,))
+    _expect(fn, "used", used, (1,), (torch.int32,))
+    dev = _pool_device(fn, pool, refs=refs, table=table, used=used, workspace=workspace)
+    ts, sp = _launch_stream(stream, dev)
+    if used is None:
+        used = _alloc(ts, (1,), torch.int32, dev)
+    workspace, ws_bytes = _bytes_of(fn, ts, workspace, kda_slots_workspace_size(n_slots), dev)
+    _launch(fn, dev, load_library().kda_slots_compact, pa, pb, len(pool), _addr(refs), _addr(table),
+            0 if table is None else table.numel(), _addr(used), n_slots, _addr(workspace), ws_bytes, sp)
+    return used

@@ -1,8 +1,9 @@
 /*
  * kda.h -- C ABI of libkda.so, the MI355X (gfx950) implementation of the Kimi Delta Attention
  * (KDA) forward pass: the forget gate, chunked prefill and the single-token decode step; and of its
- * siblings: linear attention with one decay per head (prefill, gradients, decode step) and an 8-bit
- * cache of recurrent states.
+ * siblings: linear attention with one decay per head (prefill, gradients, decode step), the selective state
+ * space scan with its short convolution (the same three), an 8-bit cache of recurrent states and the
+ * management of their slots.
  *
  * Pages the operations come from (titles as published):
  *   [bagrov] "Архитектура Kimi K3: как открытая модель с миллионным контекстом конкурирует с
@@ -277,7 +278,7 @@ int kda_decode_commit(const void *q, const void *k, const void *v, const void *b
  *     S_t = e^g S_{t-1} + k_t v_t^T,   o_t = scale * S_t^T q_t,
  * with g = g[h] <= 0 one log-decay per head, a constant of the model (0 = plain linear attention,
  * -inf = each token sees itself alone).  Layouts, streams, workspaces and errors are those stated at
- * the top of this file; further, for the calls from here to the end of this file:
+ * the top of this file; further, for these calls and those of the state cache:
  *   - every tensor pointer must be aligned to 16 bytes except g, cu_seqlens, slots, scales (4)
  *     (KDA_ERR_UNSUPPORTED);
  *   - the stream must belong to the current device;
@@ -380,6 +381,168 @@ int kda_state_store(const float *states, const int32_t *slots, void *codes, int 
 int kda_state_load(const void *codes, int code, const float *scales, const int32_t *slots,
                    float *states, int32_t N, int32_t n_slots, int32_t H, int32_t dk, int32_t dv,
                    int32_t group, void *stream);
+
+/*
+ * ---- Selective state space scan, short convolution, slot pools ---------------------------------
+ * The recurrent sibling of linear attention whose decay and write strength come from the token, with the short
+ * causal convolution that such layers run before it, and the management of the slots their states live in.  For
+ * the calls from here to the end of this file:
+ *   - Rows of tokens may be parts of wider rows: ldx, ldb, .. are the elements from one token's row to the next
+ *     (at least a row's own; token t of sequence n of a fixed-length batch is row n * T + t), so that x, B and C can
+ *     be read where one convolution wrote them side by side, and their gradients written the same way.  A stride
+ *     may be up to 2^24 bytes (KDA_ERR_UNSUPPORTED past it).  States and windows are contiguous.
+ *   - Outputs must not overlap inputs or one another (rows of one stride side by side do not).
+ *   - The stream must belong to the current device.
+ *   - Pools: where a call takes `slots` (device int32 [N]), sequence n works on slot slots[n] of an array of
+ *     n_slots, or on slot n with slots NULL (then N <= n_slots is required).  A sequence whose slot lies outside
+ *     [0, n_slots) -- a padded row of a batch -- is skipped and gets zeros for its output; of several with one slot
+ *     only the last is carried out, and the others get zeros.
+ *   - Rows of a packed batch that belong to no sequence are left as they were.
+ *   - Inputs are finite numbers: an infinity or a NaN in one token may reach, besides what the formulas give it,
+ *     outputs of its sequence's tokens up to 64 before it, gradients of those up to 64 after it, and every token's ddt
+ *     up to 512 before it; never another sequence's (the sums over tokens, dA and the like, aside).
+ *
+ * kda_conv_fwd -- short causal convolution of every channel (W = 2, 3 or 4 taps):
+ *     u_t = bias + sum_i weight[c, i] x_{t - W + 1 + i},   y_t = u_t / (1 + e^-u_t) with silu, else u_t.
+ *   x, y          : [B, T, C] in dtype (KDA_F32 or KDA_BF16), strides ldx, ldy.  Any C; 16-byte accesses where C, the
+ *                   strides and the addresses allow them, else 8-byte (16-bit types) or single elements.
+ *   weight, bias  : [C, W] fp32; [C] fp32 or NULL (= zeros).
+ *   initial_state : [N, W - 1, C] in dtype, the inputs before a sequence's first token, or NULL (= zeros).
+ *   final_state   : [N, W - 1, C] in dtype or NULL: the last W - 1 inputs (initial ones where a sequence is
+ *                   shorter); must not overlap initial_state.
+ *   cu_seqlens, B, T, n_seqs : as in kda_chunk_fwd.
+ * Sums are fp32, y is rounded once.
+ */
+int kda_conv_fwd(const void *x, int64_t ldx, int dtype, const float *weight, const float *bias,
+                 const void *initial_state, void *final_state, const int32_t *cu_seqlens, void *y,
+                 int64_t ldy, int32_t B, int64_t T, int32_t n_seqs, int32_t C, int32_t W, int silu,
+                 void *stream);
+
+/*
+ * kda_conv_bwd -- gradients of kda_conv_fwd, u recomputed from x.
+ *   dy, d_final_state : gradients of y and of final_state (dtype; the latter NULL = zeros).
+ *   dx, d_initial_state : in dtype; the latter NULL where it is not wanted.
+ *   d_weight, d_bias  : [C, W], [C] fp32, written (not added to); d_bias NULL where it is not wanted.  Their sums over
+ *                       the tokens have a fixed order.
+ *   workspace     : at least kda_conv_bwd_workspace_size(...) bytes, aligned to 16 (KDA_ERR_WORKSPACE).
+ */
+size_t kda_conv_bwd_workspace_size(int32_t n_seqs, int64_t total_tokens, int32_t C, int32_t W);
+
+int kda_conv_bwd(const void *x, int64_t ldx, int dtype, const float *weight, const float *bias,
+                 const void *initial_state, const int32_t *cu_seqlens, const void *dy, int64_t lddy,
+                 const void *d_final_state, void *dx, int64_t lddx, float *d_weight, float *d_bias,
+                 void *d_initial_state, int32_t B, int64_t T, int32_t n_seqs, int32_t C, int32_t W,
+                 int silu, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * kda_conv_step -- one token of N sequences: x, y [N, C] (strides ldx, ldy), windows [n_slots, W - 1, C] in dtype,
+ * moved on by the token in place; slots as above.  N >= 0 (0 is a no-op).
+ */
+int kda_conv_step(const void *x, int64_t ldx, int dtype, const float *weight, const float *bias,
+                  void *windows, const int32_t *slots, void *y, int64_t ldy, int32_t N, int32_t n_slots,
+                  int32_t C, int32_t W, int silu, void *stream);
+
+/*
+ * kda_ssm_chunk_fwd -- chunked prefill of the selective scan.  Per head, with
+ *     delta_t = softplus(dt_t + dt_bias),   a_t = e^(delta_t A):
+ *     S_t = a_t S_{t-1} + delta_t B_t x_t^T,   y_t = S_t^T C_t + D x_t,
+ * the state S as everywhere [d_k, d_v] (row = channel of B and C); head h uses B and C of group h / (H / G).
+ *   x             : [B, T, H, d_v];  dt : [B, T, H];  Bm, Cm : [B, T, G, d_k], all in in_dtype, strides ldx, lddt,
+ *                   ldb, ldc.  x, Bm, Cm, y: addresses and strides in steps of 16 bytes (KDA_ERR_UNSUPPORTED).
+ *   A, dt_bias, D : [H] fp32; A <= 0 (caller contract, tested by KDA_DEBUG_VALIDATE); dt_bias, D may be NULL (= 0).
+ *   initial_state, final_state : [N, H, d_k, d_v] fp32 or NULL; may be the same buffer.
+ *   cu_seqlens, B, T, n_seqs   : as in kda_chunk_fwd.
+ *   y             : [B, T, H, d_v] in y_dtype, stride ldy.
+ *   H, G, dk, dv  : G divides H; dk, dv 64 or 128 each.  Sizes (KDA_ERR_UNSUPPORTED past them): H <= 32768,
+ *                   (B * T / 128 + n_seqs) * H <= 2^21, B * T * G * dk <= 2^33.
+ *   workspace     : at least kda_ssm_chunk_workspace_size(..., 0) bytes, aligned to 16 (may be 0).
+ * Sums and states are fp32, decays between tokens come from fp64 sums.  bf16 inputs enter the products exactly, states
+ * and weighted scores as two or more bf16 terms; y is rounded once to y_dtype.
+ */
+size_t kda_ssm_chunk_workspace_size(int32_t n_seqs, int64_t total_tokens, int32_t H, int32_t G, int32_t dk,
+                                    int32_t dv, int in_dtype, int backward);
+
+int kda_ssm_chunk_fwd(const void *x, int64_t ldx, const void *dt, int64_t lddt, const void *Bm, int64_t ldb,
+                      const void *Cm, int64_t ldc, int in_dtype, const float *A, const float *dt_bias,
+                      const float *D, const float *initial_state, float *final_state,
+                      const int32_t *cu_seqlens, void *y, int64_t ldy, int y_dtype, int32_t B, int64_t T,
+                      int32_t n_seqs, int32_t H, int32_t G, int32_t dk, int32_t dv, void *workspace,
+                      size_t workspace_bytes, void *stream);
+
+/*
+ * kda_ssm_chunk_bwd -- gradients of kda_ssm_chunk_fwd; the states are recomputed, nothing has to be kept from the
+ * forward call.  With G_t the gradient of S_t (G_t = a_{t+1} G_{t+1} + C_t dy_t^T, behind the last token
+ * d_final_state):
+ *     dC_t = sum over the group's heads of S_t dy_t,      dB_t = sum over them of delta_t G_t x_t,
+ *     dx_t = delta_t G_t^T B_t + D dy_t,                  dg_t = a_t <G_t, S_{t-1}>  (of the log-decay delta_t A),
+ *     ddt_t = (x_t . G_t^T B_t + A dg_t) / (1 + e^-(dt_t + dt_bias)),   d_dt_bias = sum ddt_t,
+ *     dA = sum delta_t dg_t,   dD = sum x_t . dy_t,       d_initial_state = a_1 G_1.
+ *   dy, dx, ddt, dBm, dCm : in in_dtype, shaped as y, x, dt, Bm, Cm, strides lddy, lddx, ldddt, lddb, lddc.
+ *   d_final_state : [N, H, d_k, d_v] fp32 or NULL (= zeros).
+ *   dA, dD, d_dt_bias : [H] fp32, written; dD, d_dt_bias NULL where they are not wanted.  Sums have a fixed order.
+ *   d_initial_state : [N, H, d_k, d_v] fp32 or NULL where it is not wanted.
+ *   workspace     : at least kda_ssm_chunk_workspace_size(..., 1) bytes, aligned to 16.
+ */
+int kda_ssm_chunk_bwd(const void *x, int64_t ldx, const void *dt, int64_t lddt, const void *Bm, int64_t ldb,
+                      const void *Cm, int64_t ldc, int in_dtype, const float *A, const float *dt_bias,
+                      const float *D, const float *initial_state, const int32_t *cu_seqlens, const void *dy,
+                      int64_t lddy, const float *d_final_state, void *dx, int64_t lddx, void *ddt,
+                      int64_t ldddt, void *dBm, int64_t lddb, void *dCm, int64_t lddc, float *dA, float *dD,
+                      float *d_dt_bias, float *d_initial_state, int32_t B, int64_t T, int32_t n_seqs,
+                      int32_t H, int32_t G, int32_t dk, int32_t dv, void *workspace, size_t workspace_bytes,
+                      void *stream);
+
+/*
+ * kda_ssm_decode_step -- one token of N sequences on a pool of states [n_slots, H, d_k, d_v] fp32, each read once and
+ * written once; slots as above.  x [N, H, d_v], dt [N, H], Bm, Cm [N, G, d_k] in in_dtype, y [N, H, d_v] in y_dtype,
+ * strides and alignments as in kda_ssm_chunk_fwd.  N >= 0 (0 is a no-op).
+ */
+int kda_ssm_decode_step(const void *x, int64_t ldx, const void *dt, int64_t lddt, const void *Bm, int64_t ldb,
+                        const void *Cm, int64_t ldc, int in_dtype, const float *A, const float *dt_bias,
+                        const float *D, float *state, const int32_t *slots, void *y, int64_t ldy, int y_dtype,
+                        int32_t N, int32_t n_slots, int32_t H, int32_t G, int32_t dk, int32_t dv,
+                        void *stream);
+
+/*
+ * Slot pools.  A pool is n_planes (1 to 4) device arrays of n_slots slots each -- states, 8-bit codes and scales,
+ * convolution windows -- given by host arrays of their addresses (aligned to 16 bytes) and of the bytes of a slot
+ * (any number; 16-byte accesses where 16 divides it).  refs (device int32 [n_slots], n_slots <= 2^20) counts the
+ * users of each slot, 0 or less: free.  The calls keep refs; the host never reads it.
+ *
+ * kda_slots_copy -- dst[dst_slots[n]] = src[src_slots[n]] for N pairs between two pools that do not overlap (a batch's
+ * states into a pool, or back).  NULL lists: pair n has slot n.  A source outside [0, n_src) gives zeros, a
+ * destination outside [0, n_dst) is skipped, and of several pairs with one destination the last is taken.
+ *
+ * kda_slots_retain, kda_slots_release -- one user more or less of each listed slot, a slot listed k times k users; free
+ * slots and numbers outside [0, n_slots) are left alone, and no count falls below 0.
+ *
+ * kda_slots_fork -- children[n] = a free slot (the lowest ones, in order; -1 where none is left) that from now on has
+ * one user and the contents of slot parents[n]; zeros where the parent is free, lies outside [0, n_slots) or
+ * parents is NULL (a new sequence's state).  Parents keep their users.
+ *
+ * kda_slots_compact -- moves the used slots together: with U of them, those from U on go to the free ones before U,
+ * both in order, with their users.  *used = U (device int32).  table: n_table slot numbers (device int32, or NULL with
+ * n_table 0) rewritten to where the slots are now, -1 for what named no used slot.
+ *
+ * workspace     : at least kda_slots_workspace_size(n_slots, N) bytes (compact: N = 0), aligned to 16.
+ */
+size_t kda_slots_workspace_size(int32_t n_slots, int32_t N);
+
+int kda_slots_copy(const void *const *src, void *const *dst, const int64_t *slot_bytes, int32_t n_planes,
+                   const int32_t *src_slots, const int32_t *dst_slots, int32_t N, int32_t n_src,
+                   int32_t n_dst, void *stream);
+
+int kda_slots_retain(int32_t *refs, const int32_t *slots, int32_t N, int32_t n_slots, void *stream);
+
+int kda_slots_release(int32_t *refs, const int32_t *slots, int32_t N, int32_t n_slots, void *stream);
+
+int kda_slots_fork(void *const *planes, const int64_t *slot_bytes, int32_t n_planes, int32_t *refs,
+                   const int32_t *parents, int32_t *children, int32_t N, int32_t n_slots, void *workspace,
+                   size_t workspace_bytes, void *stream);
+
+int kda_slots_compact(void *const *planes, const int64_t *slot_bytes, int32_t n_planes, int32_t *refs,
+                      int32_t *table, int64_t n_table, int32_t *used, int32_t n_slots, void *workspace,
+                      size_t workspace_bytes, void *stream);
 
 #ifdef __cplusplus
 }
