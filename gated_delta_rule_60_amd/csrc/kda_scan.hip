@@ -14,13 +14,15 @@
 // The gradient dg_t = e^g_t <G_t, S_{t-1}> of a token's log-decay adds up all ways from a token before it (or the
 // chunk's first state) to an output from it on (or the chunk's last state).  With
 //     z_ij = e^(c_i - c_j) delta_j (C_i . B_j) (x_j . dy_i), j < i,
-//     p_i  = e^c_i dy_i . S^T C_i,  r_j = delta_j e^(c_n - c_j) x_j . G^T B_j
-// it is <G, S_n> + sum_{s >= t} (sum_j z_sj - sum_i z_is + p_s - r_s), S_n the state after the chunk, and the chunk
-// before ends with <G, S_n> + sum (p - r).  The sums run over a segment from <G, S> at its end, formed directly.
-// What a token adds and an earlier one takes off has to agree to fp32's accuracy, or the difference would stay in every
-// token before (in dA, times their number): both sums of z are over the same numbers, and the states behind p and r
-// are updated with, and read as, three bf16 terms (exact).  With two terms, and the sums C . dC and B . dB in their
-// place, dA was off by 5e-4 of itself on 63 tokens.
+//     p_i  = e^c_i dy_i . S^T C_i,  r_j = delta_j e^(c_n - c_j) x_j . G^T B_j,  thr = e^c_n <G, S>
+// it is  thr + sum_{i >= t} (sum_j z_ij - sum_{j > i} z_ji + p_i) + sum_{j < t} r_j,  and with S_n the state after the chunk
+// <G, S_n> = thr + sum r, while the chunk before ends with thr + sum p.  So thr runs over a segment from <G, S> at its
+// end, formed directly.  What one token adds and another takes off has to agree to fp32's accuracy, or the difference
+// would stay in many tokens: both sums of z are over the same numbers, and the states behind p and r are updated with, and
+// read as, three bf16 terms (exact).  Sums sum_t w_t dg_t over the tokens (dA: w = delta; dbias: w = A slope) are
+// formed from the ways themselves, W the running sum of w in the chunk:
+//     sum z_ij (W_i - W_j) + sum p_i W_i + sum r_j (W_n - W_j) + thr W_n.
+// (Sums of dg as it comes out, from two terms: dA off by 5e-4 of itself on 63 tokens; from three: 1e-4 on 16384.)
 //
 // All decays between two tokens are 2^(difference of fp64 sums): a difference of fp32 sums would lose a weak decay
 // behind a strong one.
@@ -55,7 +57,9 @@ struct Scan {
     double* seg_log[2];      // [slots, H] log2 of a segment's decay
     float* S_last;           // [N, H, dk, dv] states behind the sequences, where E needs them
     float* part[2];          // [head blocks of a group, tokens, G, dk] dC, dB per block; nullptr: one block
-    float *zz, *pp, *xu, *rr;    // [H, tokens]: sum_j z_tj - sum_i z_it; p_t; x_t . u_t; r_t
+    // [H, tokens]: sum_j z_tj - sum_i z_it; p_t; x_t . u_t from this chunk's outputs, and from later ones (r_t / delta_t)
+    float *zz, *pp, *xz, *xr;
+    float *zA, *zb;          // [slots, H]: sums of z_ij (W_i - W_j) for W of delta and of the slopes
     float *E, *dDp;          // [slots, H]: <G, S> at the segment's end, sums of x . dy
     Out ddt;
     float *dAp, *dbp;        // [slots, H]
@@ -115,12 +119,18 @@ __device__ __forceinline__ double shuffle(double x, int lane) {
 // 2^x, x <= 0 where A <= 0.
 __device__ __forceinline__ float pow2(double x) { return __builtin_amdgcn_exp2f(static_cast<float>(x)); }
 
+// The states in registers change sign from chunk to chunk: chunk k works on (-1)^k S.  The MFMAs' sums lose what they
+// drop towards minus infinity, which over all of a state's elements, against inputs that are positive on average (behind
+// a SiLU), adds up: with the signs, dA of 4096 tokens was off by 6e-6 of itself, the same way in every head.
+__device__ __forceinline__ float chunk_sign(int k) { return k & 1 ? -1.f : 1.f; }
+
 // Per chunk and head: c (log2), delta, the update's weights and the chunk's decay as hi + lo (a state's decay goes
-// the same way chunk after chunk, and so would its rounding).  Two chunks' worth: one is made while the other is
-// used.
-template <int TOK, int HB>
+// the same way chunk after chunk, and so would its rounding), these two with the sign that takes the state to the next
+// chunk's.  Two chunks' worth: one is made while the other is used.
+// Forward also the running sums of delta and of its slope.
+template <int TOK, int HB, bool BACK>
 struct Decays {
-    double cum[2][HB][TOK];
+    double cum[2][HB][TOK], dsum[BACK ? 1 : 2][HB][BACK ? 1 : TOK], ssum[BACK ? 1 : 2][HB][BACK ? 1 : TOK];
     float del[2][HB][TOK], up[2][HB][TOK];
     f32x2 over[2][HB];
 };
@@ -129,29 +139,33 @@ __device__ __forceinline__ float load_dt(const Scan& L, int64_t tok0, int n, int
     if (lane >= n) return 0.f;
     return load_as_f32<DT>(L.dt.p + (tok0 + lane) * L.dt.ld, h);
 }
-// One wave makes head hb's table: dt its token's value (lane), n tokens.  Returns the sum of the chunk.
+// One wave makes head hb's table: dt its token's value (lane), n tokens.
 template <int TOK, int HB, bool BACK>
-__device__ __forceinline__ double make_decays(Decays<TOK, HB>& t, int buf, int hb, float dt, float bias, float A, int n, int lane) {
-    const float delta = lane < n ? strength(dt, bias).delta : 0.f;
-    const double c = prefix_sum(static_cast<double>(delta) * (static_cast<double>(A) * LOG2E));
-    const double all = lane_value(c, TOK - 1);
-    const double over = exp2(all);
-    const float hi = static_cast<float>(over);
+__device__ __forceinline__ void make_decays(Decays<TOK, HB, BACK>& t, int k, int hb, float dt, float bias, float A, int n, int lane) {
+    const int buf = k & 1;
+    const Strength s = lane < n ? strength(dt, bias) : Strength{0.f, 0.f};
+    const double d = prefix_sum(static_cast<double>(s.delta)), o = BACK ? 0.0 : prefix_sum(static_cast<double>(s.slope));
+    const double c = d * (static_cast<double>(A) * LOG2E), all = lane_value(c, TOK - 1), over = -exp2(all);
+    const float hi = static_cast<float>(over), sign = chunk_sign(k + 1);
     if (lane < TOK) {
         t.cum[buf][hb][lane] = c;
-        t.del[buf][hb][lane] = delta;
-        t.up[buf][hb][lane] = BACK ? pow2(c) : delta * pow2(all - c);
+        if constexpr (!BACK) {
+            t.dsum[buf][hb][lane] = d;
+            t.ssum[buf][hb][lane] = o;
+        }
+        t.del[buf][hb][lane] = s.delta;
+        t.up[buf][hb][lane] = sign * (BACK ? pow2(c) : s.delta * pow2(all - c));
         if (lane == 0) t.over[buf][hb] = f32x2{hi, static_cast<float>(over - static_cast<double>(hi))};
     }
-    return all;
 }
 
 // What a lane's four scores of a tile (tokens i = 16 it + l16, j = 16 jt + 4 q + r) are multiplied by: the decay from the
-// earlier of the two to the later, 0 where j lies on the wrong side; forward: times delta_j; WEIGH_I: times delta_i.
-template <bool BACK, bool WEIGH_I>
+// earlier of the two to the later, 0 where j lies on the wrong side; WEIGH_J: times delta_j; WEIGH_I: times delta_i.
+template <bool BACK, bool WEIGH_J, bool WEIGH_I>
 __device__ __forceinline__ f32x4 score_weights(const double* cum, const float* del, int it, int jt, int q, int l16) {
     const double ci = cum[16 * it + l16];
-    const f32x4 dj = lds_get<f32x4>(del, 4 * (16 * jt + 4 * q));
+    f32x4 dj;
+    if constexpr (WEIGH_J) dj = lds_get<f32x4>(del, 4 * (16 * jt + 4 * q));
     const float di = WEIGH_I ? del[16 * it + l16] : 1.f;
     f32x4 w;
 #pragma unroll
@@ -159,8 +173,10 @@ __device__ __forceinline__ f32x4 score_weights(const double* cum, const float* d
         const int i = 16 * it + l16, j = 16 * jt + 4 * q + r;
         const double cj = cum[j];
         const bool seen = BACK ? j >= i : j <= i;
-        const float e = pow2(seen ? (BACK ? cj - ci : ci - cj) : 0.0);
-        w[r] = seen ? (BACK ? (WEIGH_I ? e * di : e) : e * dj[r]) : 0.f;
+        float e = pow2(seen ? (BACK ? cj - ci : ci - cj) : 0.0);
+        if constexpr (WEIGH_J) e *= dj[r];
+        if constexpr (WEIGH_I) e *= di;
+        w[r] = seen ? e : 0.f;
     }
     return w;
 }
@@ -185,13 +201,12 @@ struct ValueLds {
     static constexpr int C_BYTES = TOK / TC::R * TC::PIECE, P_BYTES = (ES == 2 ? 12 : 3) * 1024;
     __align__(16) uint8_t b[TOK / TA::R * TA::PIECE];
     __align__(16) uint8_t c[HB * C_BYTES];
-    // MODE DX: also the sums of x . u by waves, once the scores and the state's part are done
     __align__(16) uint8_t a[STATE ? 16 : TOK / TA::R * TA::PIECE];
     __align__(16) uint8_t p[STATE ? 16 : HB * P_BYTES];              // scores per head
     __align__(16) double cum[2][HB][TOK];
     __align__(16) float del[2][HB][TOK], up[STATE ? 2 : 1][HB][TOK];
     f32x2 over[2][HB];
-    __align__(16) float red[MODE == DX ? WAVES * TOK : 1];   // r by waves
+    __align__(16) float red[MODE == DX ? WAVES * TOK : 1];   // r / delta by waves
 };
 
 // One workgroup per (segment, HB heads of a group): a and b rows are shared, wave w has 16 columns of head
@@ -257,13 +272,13 @@ __device__ __forceinline__ void value_pass(const Scan& L, int32_t slot, int32_t 
         const int buf = c & 1, n = chunk_n(chunk_at(c));
         const float delta = lane < n ? strength(dt, bias).delta : 0.f;
         const double cum = prefix_sum(static_cast<double>(delta) * (static_cast<double>(A) * LOG2E));
-        const double all = lane_value(cum, TOK - 1), over = exp2(all);
+        const double all = lane_value(cum, TOK - 1), over = -exp2(all);
         const float hi = static_cast<float>(over);
         log_sum += all;
         if (lane < TOK) {
             lds.cum[buf][table][lane] = cum;
             lds.del[buf][table][lane] = delta;
-            if (STATE) lds.up[STATE ? buf : 0][table][lane] = BACK ? pow2(cum) : delta * pow2(all - cum);
+            if (STATE) lds.up[STATE ? buf : 0][table][lane] = chunk_sign(c + 1) * (BACK ? pow2(cum) : delta * pow2(all - cum));
             if (lane == 0) lds.over[buf][table] = f32x2{hi, static_cast<float>(over - static_cast<double>(hi))};
         }
     };
@@ -383,7 +398,7 @@ __device__ __forceinline__ void value_pass(const Scan& L, int32_t slot, int32_t 
         if constexpr (!STATE) {
             if (table >= 0 && lane < TOK) {          // the update's weights, read behind the next barrier
                 const double ct = lds.cum[buf][table][lane], all = lds.cum[buf][table][TOK - 1];
-                lds.up[0][table][lane] = BACK ? pow2(ct) : lds.del[buf][table][lane] * pow2(all - ct);
+                lds.up[0][table][lane] = chunk_sign(c + 1) * (BACK ? pow2(ct) : lds.del[buf][table][lane] * pow2(all - ct));
             }
             // ---- scores, shared out over the waves, weighted for every head
             if constexpr (BF) {
@@ -402,7 +417,7 @@ __device__ __forceinline__ void value_pass(const Scan& L, int32_t slot, int32_t 
                         u32x4 hi, lo;
 #pragma unroll
                         for (int hh = 0; hh < 2; ++hh) {
-                            const f32x4 x = P[hh] * score_weights<BACK, false>(lds.cum[buf][i], lds.del[buf][i], it, 2 * tg + hh, q, l16);
+                            const f32x4 x = P[hh] * score_weights<BACK, !BACK, false>(lds.cum[buf][i], lds.del[buf][i], it, 2 * tg + hh, q, l16);
                             uint32_t h0_, o0, h1, o1;
                             split_pair(x[0], x[1], h0_, o0);
                             split_pair(x[2], x[3], h1, o1);
@@ -427,7 +442,7 @@ __device__ __forceinline__ void value_pass(const Scan& L, int32_t slot, int32_t 
 #pragma unroll
                 for (int i = 0; i < HB; ++i)
                     lds_put(lds.p + i * Lds::P_BYTES, wave * 1024 + lane * 16,
-                            P * score_weights<BACK, false>(lds.cum[buf][i], lds.del[buf][i], it, jt, q, l16));
+                            P * score_weights<BACK, !BACK, false>(lds.cum[buf][i], lds.del[buf][i], it, jt, q, l16));
             }
             // ---- the state's part
 #pragma unroll
@@ -470,15 +485,15 @@ __device__ __forceinline__ void value_pass(const Scan& L, int32_t slot, int32_t 
 #pragma unroll
             for (int it = 0; it < IT; ++it) {
                 const double ci = cum[16 * it + l16];
-                O[it] *= pow2(BACK ? all - ci : ci);
-                if constexpr (MODE == DX) {          // r, but for delta
+                O[it] *= chunk_sign(c) * pow2(BACK ? all - ci : ci);
+                if constexpr (MODE == DX) {          // r / delta
                     if constexpr (BF) xf[it] = f32x4{lo_f32(xr[it][0]), hi_f32(xr[it][0]), lo_f32(xr[it][1]), hi_f32(xr[it][1])};
                     float s = 0.f;
 #pragma unroll
                     for (int r = 0; r < 4; ++r) s = __builtin_fmaf(xf[it][r], O[it][r], s);
                     s += __shfl_xor(s, 16, 64);
                     s += __shfl_xor(s, 32, 64);
-                    if (q == 0) lds_put(lds.red, 4 * (wave * TOK + 16 * it + l16), s);
+                    if (q == 0) lds.red[wave * TOK + 16 * it + l16] = s;
                 }
             }
         }
@@ -527,15 +542,8 @@ __device__ __forceinline__ void value_pass(const Scan& L, int32_t slot, int32_t 
                     f32x4 x;
                     if constexpr (BF) x = f32x4{lo_f32(xr[it][0]), hi_f32(xr[it][0]), lo_f32(xr[it][1]), hi_f32(xr[it][1])};
                     else x = xf[it];
-                    float s = 0.f;
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        s = __builtin_fmaf(x[r], O[it][r], s);
-                        dD = __builtin_fmaf(x[r], own[r], dD);
-                    }
-                    s += __shfl_xor(s, 16, 64);
-                    s += __shfl_xor(s, 32, 64);
-                    if (q == 0) lds_put(lds.a, 4 * (wave * TOK + 16 * it + l16), s);
+                    for (int r = 0; r < 4; ++r) dD = __builtin_fmaf(x[r], own[r], dD);
                     const float di = del[16 * it + l16];
                     O[it] = O[it] * di + D * own;
                 }
@@ -611,21 +619,15 @@ __device__ __forceinline__ void value_pass(const Scan& L, int32_t slot, int32_t 
         }
         lds_barrier();                               // the tiles have been read, the output is there
         if (c + 1 < n_chunks) load_b(c + 1);
-        if constexpr (MODE == Y)
+        if constexpr (!STATE)
             if (c + 1 < n_chunks) load_a(c + 1);
         if constexpr (MODE == DX) {
             for (int e = t; e < HB * TOK; e += WAVES * 64) {
                 const int i = e / TOK, at = e % TOK;
-                float s = 0.f;
-#pragma unroll
-                for (int x = 0; x < WPH; ++x) s += lds_get<float>(lds.a, 4 * ((i * WPH + x) * TOK + at));
                 float r = 0.f;
 #pragma unroll
-                for (int x = 0; x < WPH; ++x) r += lds_get<float>(lds.red, 4 * ((i * WPH + x) * TOK + at));
-                if (at < n && h0 + i < h_end) {
-                    L.xu[(h0 + i) * L.total + tok0 + at] = s;
-                    L.rr[(h0 + i) * L.total + tok0 + at] = r * lds.del[buf][i][at];
-                }
+                for (int x = 0; x < WPH; ++x) r += lds.red[(i * WPH + x) * TOK + at];
+                if (at < n && h0 + i < h_end) L.xr[(h0 + i) * L.total + tok0 + at] = r;
             }
         }
         if constexpr (STAGED) {
@@ -644,9 +646,7 @@ __device__ __forceinline__ void value_pass(const Scan& L, int32_t slot, int32_t 
                 }
             }
         }
-        if constexpr (STAGED || MODE == DX) lds_barrier();     // the output and the sums have been read
-        if constexpr (MODE == DX)
-            if (c + 1 < n_chunks) load_a(c + 1);
+        if constexpr (STAGED) lds_barrier();         // the output has been read
         if (c + 1 < n_chunks) load_c(c + 1);
     }
 
@@ -657,7 +657,7 @@ __device__ __forceinline__ void value_pass(const Scan& L, int32_t slot, int32_t 
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-            for (int r = 0; r < 4; ++r) dst[(row(mt) + r) * DV + col] = M[mt][r];
+            for (int r = 0; r < 4; ++r) dst[(row(mt) + r) * DV + col] = chunk_sign(n_chunks) * M[mt][r];
     }
     if constexpr (STATE) {
         if (table >= 0 && h0 + table < h_end && lane == 0) L.seg_log[ST][static_cast<int64_t>(slot) * L.H + h0 + table] = log_sum;
@@ -753,7 +753,7 @@ __global__ void __launch_bounds__(256) scan_kernel(Scan L, int32_t elems, int32_
 
 // ---------------------------------------------------------------- dC and dB
 
-template <int DT, int DK, int DV, int HB>
+template <int DT, int DK, int DV, int HB, bool BACK>
 struct SharedLds {
     static constexpr int ES = DT == KDA_BF16 ? 2 : 4, TOK = DT == KDA_BF16 ? 64 : 32, WAVES = DK / 16;
     using TA = Tile<DV, ES>;
@@ -763,10 +763,10 @@ struct SharedLds {
     __align__(16) uint8_t a[2 * A_BYTES];
     __align__(16) uint8_t c[TOK / TC::R * TC::PIECE];
     __align__(16) uint8_t p[(ES == 2 ? 12 : 3) * 1024];    // scores, summed over the heads
-    Decays<TOK, HB> t;
-    // dC: p by waves, sums of z over j by 32 tokens j (fp32: 16), over i by 16 tokens i
-    static constexpr int RED = WAVES + 2 + TOK / 16;
-    float red[HB][RED][TOK];
+    Decays<TOK, HB, BACK> t;
+    // dC: p by waves, sums of z over j by 32 tokens j (fp32: 16), of z / delta over i by 16 tokens i, z_jj / delta_j
+    static constexpr int RED = BACK ? 1 : WAVES + 2 + TOK / 16 + 1;
+    float red[BACK ? 1 : HB][RED][BACK ? 1 : TOK];
 };
 
 // The sum over a row of 16 lanes, in its last one.
@@ -785,8 +785,8 @@ __device__ __forceinline__ float row_sum(float x) {
 // products.  The output's sum over the heads is formed in registers, and since c is the group's, its product with
 // the scores is formed once, with their sum.
 template <int DT, int DK, int DV, int HB, bool BACK>
-__device__ __forceinline__ void shared_pass(const Scan& L, int32_t slot, int32_t block, SharedLds<DT, DK, DV, HB>& lds) {
-    using Lds = SharedLds<DT, DK, DV, HB>;
+__device__ __forceinline__ void shared_pass(const Scan& L, int32_t slot, int32_t block, SharedLds<DT, DK, DV, HB, BACK>& lds) {
+    using Lds = SharedLds<DT, DK, DV, HB, BACK>;
     using TA = typename Lds::TA;
     using TC = typename Lds::TC;
     constexpr bool BF = DT == KDA_BF16;
@@ -822,7 +822,7 @@ __device__ __forceinline__ void shared_pass(const Scan& L, int32_t slot, int32_t
         return load_dt<DT>(L, w.lo + off, chunk_n(off), h0 + hb, lane);
     };
     auto decays = [&](int c, int hb, float dt) {
-        make_decays<TOK, HB, BACK>(lds.t, c & 1, hb, dt, L.bias ? L.bias[h0 + hb] : 0.f, L.A[h0 + hb], chunk_n(chunk_at(c)), lane);
+        make_decays<TOK, HB, BACK>(lds.t, c, hb, dt, L.bias ? L.bias[h0 + hb] : 0.f, L.A[h0 + hb], chunk_n(chunk_at(c)), lane);
     };
     load_ab(0, 0, 0);
     load_c(0);
@@ -876,6 +876,9 @@ __device__ __forceinline__ void shared_pass(const Scan& L, int32_t slot, int32_t
     };
 
     int step = 0;
+    float zA[BACK ? 1 : HB], zb[BACK ? 1 : HB];      // sums of z_ij (W_i - W_j)
+#pragma unroll
+    for (int hb = 0; hb < (BACK ? 1 : HB); ++hb) zA[hb] = zb[hb] = 0.f;
     for (int c = 0; c < n_chunks; ++c) {
         const int64_t off = chunk_at(c), tok0 = w.lo + off;
         const int n = chunk_n(off), buf = c & 1;
@@ -975,26 +978,38 @@ __device__ __forceinline__ void shared_pass(const Scan& L, int32_t slot, int32_t
                         for (int r = 0; r < 4; ++r) X[0] = mfma_f32(b[r], a[r], X[0]);
                     }
                 }
-                float z = 0.f;
+                if constexpr (BACK) {
 #pragma unroll
-                for (int hh = 0; hh < TILES; ++hh) {
-                    X[hh] *= score_weights<BACK, true>(cum, del, it, jt + hh, q, l16);
-                    P[i][hh] += X[hh];
-                    if constexpr (!BACK) {
-                        f32x4 zs;
+                    for (int hh = 0; hh < TILES; ++hh) P[i][hh] += X[hh] * score_weights<true, false, true>(cum, del, it, jt + hh, q, l16);
+                } else {
+                    float rows = 0.f, diag = 0.f;
+                    const int ti = 16 * it + l16;
+                    const double di = lds.t.dsum[buf][hb][ti], si = lds.t.ssum[buf][hb][ti];
+#pragma unroll
+                    for (int hh = 0; hh < TILES; ++hh) {
+                        const int tj = 16 * (jt + hh) + 4 * q;
+                        const f32x4 dj = lds_get<f32x4>(del, 4 * tj), x = X[hh] * score_weights<false, false, false>(cum, del, it, jt + hh, q, l16);
+                        P[i][hh] += x * dj;
+                        f32x4 cols;
 #pragma unroll
                         for (int r = 0; r < 4; ++r) {
-                            zs[r] = 16 * (jt + hh) + 4 * q + r < 16 * it + l16 ? X[hh][r] * CB[i][hh][r] : 0.f;
-                            z += zs[r];
-                            zs[r] = row_sum(zs[r]);
+                            const float y = x[r] * CB[i][hh][r], below = tj + r < ti ? y : 0.f, z = below * dj[r];
+                            if (tj + r == ti) diag += y;
+                            rows += z;
+                            zA[hb] = __builtin_fmaf(z, static_cast<float>(di - lds.t.dsum[buf][hb][tj + r]), zA[hb]);
+                            zb[hb] = __builtin_fmaf(z, static_cast<float>(si - lds.t.ssum[buf][hb][tj + r]), zb[hb]);
+                            cols[r] = row_sum(below);
                         }
-                        if (l16 == 15) *reinterpret_cast<f32x4*>(&lds.red[hb][WAVES + 2 + it][16 * (jt + hh) + 4 * q]) = zs;
+                        if (l16 == 15) *reinterpret_cast<f32x4*>(&lds.red[hb][WAVES + 2 + it][tj]) = cols;
                     }
-                }
-                if constexpr (!BACK) {
-                    z += __shfl_xor(z, 16, 64);
-                    z += __shfl_xor(z, 32, 64);
-                    if (q == 0) lds.red[hb][WAVES + (BF ? jt / 2 : jt)][16 * it + l16] = z;
+                    rows += __shfl_xor(rows, 16, 64);
+                    rows += __shfl_xor(rows, 32, 64);
+                    if (q == 0) lds.red[hb][WAVES + (BF ? jt / 2 : jt)][ti] = rows;
+                    if (BF ? it / 2 == jt / 2 : it == jt) {        // the group of the tile's own tokens
+                        diag += __shfl_xor(diag, 16, 64);
+                        diag += __shfl_xor(diag, 32, 64);
+                        if (q == 0) lds.red[hb][Lds::RED - 1][ti] = diag;
+                    }
                 }
             }
             // ---- the state's part
@@ -1039,7 +1054,7 @@ __device__ __forceinline__ void shared_pass(const Scan& L, int32_t slot, int32_t
 #pragma unroll
             for (int it = 0; it < IT; ++it) {
                 const double ci = cum[16 * it + l16];
-                own[it] *= BACK ? del[16 * it + l16] * pow2(all - ci) : pow2(ci);
+                own[it] *= chunk_sign(c) * (BACK ? del[16 * it + l16] * pow2(all - ci) : pow2(ci));
                 O[it] += own[it];
                 if constexpr (!BACK) {
                     f32x4 cc;
@@ -1144,15 +1159,16 @@ __device__ __forceinline__ void shared_pass(const Scan& L, int32_t slot, int32_t
             for (int e = t; e < heads * TOK; e += WAVES * 64) {
                 const int hb = e / TOK, at = e % TOK;
                 // 64 (32) tokens: the second half's z also reach to the first half, and are reached from it
-                float s = lds.red[hb][WAVES][at];
-                if (at >= TOK / 2) s += lds.red[hb][WAVES + 1][at];
-                for (int x = at / (TOK / 2) * (IT / 2); x < IT; ++x) s -= lds.red[hb][WAVES + 2 + x][at];
-                float p = 0.f;
+                float rows = lds.red[hb][WAVES][at], cols = 0.f, p = 0.f;
+                if (at >= TOK / 2) rows += lds.red[hb][WAVES + 1][at];
+                for (int x = at / (TOK / 2) * (IT / 2); x < IT; ++x) cols += lds.red[hb][WAVES + 2 + x][at];
 #pragma unroll
                 for (int x = 0; x < WAVES; ++x) p += lds.red[hb][x][at];
                 if (at < n) {
-                    L.zz[(h0 + hb) * L.total + tok0 + at] = s;
-                    L.pp[(h0 + hb) * L.total + tok0 + at] = p;
+                    const int64_t i = (h0 + hb) * L.total + tok0 + at;
+                    L.zz[i] = rows - lds.t.del[buf][hb][at] * cols;
+                    L.xz[i] = cols + lds.red[hb][Lds::RED - 1][at];
+                    L.pp[i] = p;
                 }
             }
         }
@@ -1177,24 +1193,46 @@ __device__ __forceinline__ void shared_pass(const Scan& L, int32_t slot, int32_t
             }
         }
     }
+    if constexpr (!BACK) {
+        lds_barrier();                               // the last chunk's sums have been read
+#pragma unroll
+        for (int hb = 0; hb < HB; ++hb) {
+#pragma unroll
+            for (int off = 1; off < 64; off <<= 1) {
+                zA[hb] += __shfl_xor(zA[hb], off, 64);
+                zb[hb] += __shfl_xor(zb[hb], off, 64);
+            }
+            if (lane == 0) {
+                lds.red[hb][0][wave] = zA[hb];
+                lds.red[hb][1][wave] = zb[hb];
+            }
+        }
+        lds_barrier();
+        if (t < 2 * heads) {
+            float sum = 0.f;
+            for (int x = 0; x < WAVES; ++x) sum += lds.red[t >> 1][t & 1][x];
+            (t & 1 ? L.zb : L.zA)[static_cast<int64_t>(slot) * L.H + h0 + (t >> 1)] = sum;
+        }
+    }
 }
 
 template <int DT, int DK, int DV, int HB>
 __global__ void __launch_bounds__(DK * 4, DK == 128 ? 2 : 1) shared_kernel(Scan L) {
-    __shared__ SharedLds<DT, DK, DV, HB> lds;
+    __shared__ union {
+        SharedLds<DT, DK, DV, HB, false> c;
+        SharedLds<DT, DK, DV, HB, true> b;
+    } lds;
     uint32_t unit;
     int32_t pass;
     const uint32_t blocks = static_cast<uint32_t>(L.blocks) * L.G;
     if (!unit_of(L.slots * blocks, 2, unit, pass)) return;
-    if (pass == 0) shared_pass<DT, DK, DV, HB, false>(L, unit / blocks, unit % blocks, lds);
-    else shared_pass<DT, DK, DV, HB, true>(L, unit / blocks, unit % blocks, lds);
+    if (pass == 0) shared_pass<DT, DK, DV, HB, false>(L, unit / blocks, unit % blocks, lds.c);
+    else shared_pass<DT, DK, DV, HB, true>(L, unit / blocks, unit % blocks, lds.b);
 }
 
 // ---------------------------------------------------------------- ddt, dA, dbias; sums over blocks and segments
 
-// One wave per (segment, head): from its last 64 tokens to its first (a chunk; two with fp32 inputs), lane l has the
-// token l before the last.  dg runs from <G, S> at the segment's end; sums of z stay in their chunk, over all of which
-// they are zero.
+// One wave per (segment, head): from its last chunk to its first, lane l has the token l before the chunk's last.
 template <int DT>
 __global__ void __launch_bounds__(256) decay_grad_kernel(Scan L) {
     const int64_t u = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6);
@@ -1202,41 +1240,56 @@ __global__ void __launch_bounds__(256) decay_grad_kernel(Scan L) {
     if (u >= static_cast<int64_t>(L.slots) * L.H) return;
     const int32_t slot = static_cast<int32_t>(u / L.H), h = static_cast<int32_t>(u % L.H);
     Where w;
-    if (!locate(L, slot, w)) {                       // no such segment: nothing to add up
+    if (!locate(L, slot, w) || w.hi == w.lo) {       // no such segment, or an empty one: nothing to add up
         if (lane == 0) L.dAp[u] = L.dbp[u] = L.dDp[u] = 0.f;
         return;
     }
     const double A = static_cast<double>(L.A[h]);
     const float bias = L.bias ? L.bias[h] : 0.f;
-    double end = static_cast<double>(L.E[u]), dA = 0.0, db = 0.0;      // <G, S> behind the tokens in hand
+    double end = static_cast<double>(L.E[u]);        // <G, S> behind the tokens in hand
+    double dA = 0.0, db = 0.0, own = 0.0;            // a lane's part of sum delta dg, sum slope dg, sum slope x . u
     const int64_t row = h * L.total;
-    for (int64_t lo = w.lo + (w.hi - w.lo - 1) / 64 * 64; w.hi > w.lo && lo >= w.lo; lo -= 64) {
-        const int64_t hi = lo + 64 < w.hi ? lo + 64 : w.hi, tok = hi - 1 - lane;
+    constexpr int TOK = DT == KDA_BF16 ? 64 : 32;
+    for (int64_t lo = w.lo + (w.hi - w.lo - 1) / TOK * TOK; lo >= w.lo; lo -= TOK) {
+        const int64_t hi = lo + TOK < w.hi ? lo + TOK : w.hi, tok = hi - 1 - lane;
         const bool in = tok >= lo;
-        double x = 0.0, z = 0.0, pr = 0.0;
+        double x = 0.0, z = 0.0, p = 0.0, r = 0.0;
         Strength s = {0.f, 0.f};
         if (in) {
-            z = static_cast<double>(L.zz[row + tok]);
-            pr = static_cast<double>(L.pp[row + tok]) - static_cast<double>(L.rr[row + tok]);
-            x = static_cast<double>(L.xu[row + tok]);
             s = strength(load_as_f32<DT>(L.dt.p + tok * L.dt.ld, h), bias);
+            const float later = L.xr[row + tok];
+            x = static_cast<double>(L.xz[row + tok]) + later;
+            z = static_cast<double>(L.zz[row + tok]);
+            p = static_cast<double>(L.pp[row + tok]);
+            r = static_cast<double>(s.delta) * later;
         }
-        // Nothing to speak of goes through a token that decays by more than 2^-30: its dg is zero, and the sums start
-        // anew before it (its large delta would otherwise multiply their rounding).
-        const double sum = prefix_sum(z + pr), over = prefix_sum(pr);
-        const uint64_t cuts = __ballot(in && static_cast<double>(s.delta) * A < -20.8);
-        const uint64_t seen = cuts & (~uint64_t(0) >> (63 - lane));
-        const int cut = seen ? 63 - __builtin_clzll(seen) : -1, last_cut = cuts ? 63 - __builtin_clzll(cuts) : -1;
-        const double until = shuffle(sum, cut < 0 ? 0 : cut);
-        const double g = cut == lane ? 0.0 : cut < 0 ? end + sum : sum - until;
-        end = last_cut < 0 ? end + lane_value(over, 63) : lane_value(sum, 63) - lane_value(sum, last_cut);
-        if (in) {
-            const double d = (x + A * g) * s.slope;
-            store_from_f32<DT>(L.ddt.p + tok * L.ddt.ld, h, static_cast<float>(d));
-            db += d;
-            dA += s.delta * g;
+        const double delta = static_cast<double>(s.delta), slope = static_cast<double>(s.slope);
+        // sums over the tokens from a lane's own to the last
+        const double zs = prefix_sum(z + p), ps = prefix_sum(p), rs = prefix_sum(r), ds = prefix_sum(delta), ss = prefix_sum(slope);
+        const double r_all = lane_value(rs, 63), d_all = lane_value(ds, 63), s_all = lane_value(ss, 63);
+        // Where a chunk or a token decays by more than e^-14, what goes through it is below the difference's rounding
+        // (about 2^-20 of <G, S>, which W would multiply): it is taken as zero, and the sums start anew before it.
+        const double through = d_all * A < -14.0 ? 0.0 : end - r_all;
+        const uint64_t cuts = __ballot(in && delta * A < -14.0), seen = cuts & (~uint64_t(0) >> (63 - lane));
+        const int cut = seen ? 63 - __builtin_clzll(seen) : -1;
+        const double from = shuffle(zs - rs, cut < 0 ? 0 : cut);
+        const double g = cut == lane ? 0.0 : (zs - rs) + (cut < 0 ? through + r_all : -from);
+        end = through + lane_value(ps, 63);
+        if (in) store_from_f32<DT>(L.ddt.p + tok * L.ddt.ld, h, static_cast<float>((x + A * g) * slope));
+        // W_i = all - (from i on) + w_i, W_n - W_j = (from j on) - w_j
+        dA += p * (d_all - ds + delta) + r * (ds - delta);
+        db += p * (s_all - ss + slope) + r * (ss - slope);
+        own += slope * x;
+        if (lane == 0) {
+            dA += through * d_all;
+            db += through * s_all;
         }
     }
+    if (lane == 0) {
+        dA += static_cast<double>(L.zA[u]);
+        db += static_cast<double>(L.zb[u]);
+    }
+    db = own + A * db;
 #pragma unroll
     for (int off = 1; off < 64; off <<= 1) {
         dA += __shfl_xor(dA, off, 64);
@@ -1341,11 +1394,8 @@ void carve_backward(Scan& L, Carver& ws, int64_t elems, int32_t dk, bool last) {
     L.S_last = last ? S_last : nullptr;
     if (L.blocks > 1)
         for (int st : {S_STATE, G_STATE}) L.part[st] = ws.take<float>(L.total * L.G * dk * L.blocks);
-    for (float** p : {&L.zz, &L.pp, &L.xu, &L.rr}) *p = ws.take<float>(L.H * L.total);
-    L.E = ws.take<float>(su);
-    L.dDp = ws.take<float>(su);
-    L.dAp = ws.take<float>(su);
-    L.dbp = ws.take<float>(su);
+    for (float** p : {&L.zz, &L.pp, &L.xz, &L.xr}) *p = ws.take<float>(L.H * L.total);
+    for (float** p : {&L.zA, &L.zb, &L.E, &L.dDp, &L.dAp, &L.dbp}) *p = ws.take<float>(su);
 }
 
 void set_segments(Scan& L, bool backward, int32_t dv, int32_t in_dtype, bool packed) {
