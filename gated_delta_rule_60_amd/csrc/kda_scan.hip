@@ -8,21 +8,19 @@
 //     u_i   = e^(c_n - c_i) G^T B_i + sum_{j >= i} e^(c_j - c_i) (C_j . B_i) dy_j,   dx_i = delta_i u_i + D dy_i
 //     dB_i  = delta_i (e^(c_n - c_i) G x_i + sum_{j >= i} e^(c_j - c_i) (dy_j . x_i) C_j)         (sum over heads)
 //     S    <- e^c_n S + sum_j e^(c_n - c_j) delta_j B_j x_j^T,   G <- e^c_n G + sum_j e^c_j C_j dy_j^T.
-// y and dx are one pass (value_pass: a state of d_k rows by a head's d_v columns), dC and dB another
-// (shared_pass: its transpose, for several heads of a group whose outputs are added up in registers).
+// y and dx are one pass along the tokens (value_pass: a state of d_k rows by a head's d_v columns in registers).  For the
+// gradients the same pass writes the states before, and the gradients behind, every chunk; dC, dB and the decays'
+// gradients then come from all chunks at once (grad_kernel), with the sums over the heads in registers.
 //
 // The gradient dg_t = e^g_t <G_t, S_{t-1}> of a token's log-decay adds up all ways from a token before it (or the
 // chunk's first state) to an output from it on (or the chunk's last state).  With
 //     z_ij = e^(c_i - c_j) delta_j (C_i . B_j) (x_j . dy_i), j < i,
 //     p_i  = e^c_i dy_i . S^T C_i,  r_j = delta_j e^(c_n - c_j) x_j . G^T B_j,  thr = e^c_n <G, S>
-// it is  thr + sum_{i >= t} (sum_j z_ij - sum_{j > i} z_ji + p_i) + sum_{j < t} r_j,  and with S_n the state after the chunk
-// <G, S_n> = thr + sum r, while the chunk before ends with thr + sum p.  So thr runs over a segment from <G, S> at its
-// end, formed directly.  What one token adds and another takes off has to agree to fp32's accuracy, or the difference
-// would stay in many tokens: both sums of z are over the same numbers, and the states behind p and r are updated with, and
-// read as, three bf16 terms (exact).  Sums sum_t w_t dg_t over the tokens (dA: w = delta; dbias: w = A slope) are
-// formed from the ways themselves, W the running sum of w in the chunk:
+// it is  thr + sum_{i >= t} (sum_j z_ij - sum_{j > i} z_ji + p_i) + sum_{j < t} r_j.  Sums sum_t w_t dg_t over the tokens (dA:
+// w = delta; dbias: w = A slope) are formed from the ways themselves, W the running sum of w in the chunk:
 //     sum z_ij (W_i - W_j) + sum p_i W_i + sum r_j (W_n - W_j) + thr W_n.
-// (Sums of dg as it comes out, from two terms: dA off by 5e-4 of itself on 63 tokens; from three: 1e-4 on 16384.)
+// (The sum of C . dC - B . dB over the tokens behind t is dg_t, too, and needs no chunk's states; but what it adds at one
+// token and takes off at another only cancels to rounding: dA was off by 1e-4 of itself on 16384 tokens.)
 //
 // All decays between two tokens are 2^(difference of fp64 sums): a difference of fp32 sums would lose a weak decay
 // behind a strong one.
@@ -55,20 +53,25 @@ struct Scan {
     float* m_out[2];         // S: final states; G: gradients of the initial states; or nullptr
     float* seg_states[2];    // [slots, H, dk, dv]: a segment's S before its first token, G behind its last one
     double* seg_log[2];      // [slots, H] log2 of a segment's decay
-    float* S_last;           // [N, H, dk, dv] states behind the sequences, where E needs them
+    float* chunk_states[2];  // [c_slots, H, dk, dv]: S before a chunk, G behind it
     float* part[2];          // [head blocks of a group, tokens, G, dk] dC, dB per block; nullptr: one block
+    double* t_dsum;          // [c_slots, H, ct] a chunk's running sums of delta, delta, running sums of its slope
+    float *t_del, *t_ssum;
     // [H, tokens]: sum_j z_tj - sum_i z_it; p_t; x_t . u_t from this chunk's outputs, and from later ones (r_t / delta_t)
     float *zz, *pp, *xz, *xr;
-    float *zA, *zb;          // [slots, H]: sums of z_ij (W_i - W_j) for W of delta and of the slopes
-    float *E, *dDp;          // [slots, H]: <G, S> at the segment's end, sums of x . dy
+    // [c_slots, H]: sums of z_ij (W_i - W_j) for W of delta and of the slopes, of x . dy, <G, S>
+    float *zA, *zb, *dDp, *thr;
+    float *dAp, *dbp;        // [c_slots, H]
     Out ddt;
-    float *dAp, *dbp;        // [slots, H]
     float *dA, *dD, *dbias;  // [H]
+    int32_t ct, c_slots, c_per_seq;      // tokens of a chunk, chunks in all, chunks of a fixed-length sequence
+    int32_t heads;           // of a block of the gradients
     int32_t exact[2];        // the segment states end in one that is handed out
     int32_t blocks;          // head blocks of a group
 };
 enum { S_STATE = 0, G_STATE = 1 };
-enum Mode { Y, DX, S_ONLY, G_ONLY };
+// Passes along the tokens: y, dx, a segment's own contribution to the states, and the states of every chunk.
+enum Mode { Y, DX, S_ONLY, G_ONLY, S_CHUNKS, G_CHUNKS };
 constexpr int32_t WHOLE = 0x7fffffff;
 constexpr double LOG2E = 1.4426950408889634074;
 
@@ -124,49 +127,18 @@ __device__ __forceinline__ float pow2(double x) { return __builtin_amdgcn_exp2f(
 // a SiLU), adds up: with the signs, dA of 4096 tokens was off by 6e-6 of itself, the same way in every head.
 __device__ __forceinline__ float chunk_sign(int k) { return k & 1 ? -1.f : 1.f; }
 
-// Per chunk and head: c (log2), delta, the update's weights and the chunk's decay as hi + lo (a state's decay goes
-// the same way chunk after chunk, and so would its rounding), these two with the sign that takes the state to the next
-// chunk's.  Two chunks' worth: one is made while the other is used.
-// Forward also the running sums of delta and of its slope.
-template <int TOK, int HB, bool BACK>
-struct Decays {
-    double cum[2][HB][TOK], dsum[BACK ? 1 : 2][HB][BACK ? 1 : TOK], ssum[BACK ? 1 : 2][HB][BACK ? 1 : TOK];
-    float del[2][HB][TOK], up[2][HB][TOK];
-    f32x2 over[2][HB];
-};
 template <int DT>
 __device__ __forceinline__ float load_dt(const Scan& L, int64_t tok0, int n, int32_t h, int lane) {
     if (lane >= n) return 0.f;
     return load_as_f32<DT>(L.dt.p + (tok0 + lane) * L.dt.ld, h);
 }
-// One wave makes head hb's table: dt its token's value (lane), n tokens.
-template <int TOK, int HB, bool BACK>
-__device__ __forceinline__ void make_decays(Decays<TOK, HB, BACK>& t, int k, int hb, float dt, float bias, float A, int n, int lane) {
-    const int buf = k & 1;
-    const Strength s = lane < n ? strength(dt, bias) : Strength{0.f, 0.f};
-    const double d = prefix_sum(static_cast<double>(s.delta)), o = BACK ? 0.0 : prefix_sum(static_cast<double>(s.slope));
-    const double c = d * (static_cast<double>(A) * LOG2E), all = lane_value(c, TOK - 1), over = -exp2(all);
-    const float hi = static_cast<float>(over), sign = chunk_sign(k + 1);
-    if (lane < TOK) {
-        t.cum[buf][hb][lane] = c;
-        if constexpr (!BACK) {
-            t.dsum[buf][hb][lane] = d;
-            t.ssum[buf][hb][lane] = o;
-        }
-        t.del[buf][hb][lane] = s.delta;
-        t.up[buf][hb][lane] = sign * (BACK ? pow2(c) : s.delta * pow2(all - c));
-        if (lane == 0) t.over[buf][hb] = f32x2{hi, static_cast<float>(over - static_cast<double>(hi))};
-    }
-}
-
 // What a lane's four scores of a tile (tokens i = 16 it + l16, j = 16 jt + 4 q + r) are multiplied by: the decay from the
-// earlier of the two to the later, 0 where j lies on the wrong side; WEIGH_J: times delta_j; WEIGH_I: times delta_i.
-template <bool BACK, bool WEIGH_J, bool WEIGH_I>
+// earlier of the two to the later, 0 where j lies on the wrong side; forward: times delta_j.
+template <bool BACK>
 __device__ __forceinline__ f32x4 score_weights(const double* cum, const float* del, int it, int jt, int q, int l16) {
     const double ci = cum[16 * it + l16];
     f32x4 dj;
-    if constexpr (WEIGH_J) dj = lds_get<f32x4>(del, 4 * (16 * jt + 4 * q));
-    const float di = WEIGH_I ? del[16 * it + l16] : 1.f;
+    if constexpr (!BACK) dj = lds_get<f32x4>(del, 4 * (16 * jt + 4 * q));
     f32x4 w;
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
@@ -174,8 +146,7 @@ __device__ __forceinline__ f32x4 score_weights(const double* cum, const float* d
         const double cj = cum[j];
         const bool seen = BACK ? j >= i : j <= i;
         float e = pow2(seen ? (BACK ? cj - ci : ci - cj) : 0.0);
-        if constexpr (WEIGH_J) e *= dj[r];
-        if constexpr (WEIGH_I) e *= di;
+        if constexpr (!BACK) e *= dj[r];
         w[r] = seen ? e : 0.f;
     }
     return w;
@@ -194,7 +165,7 @@ __device__ __forceinline__ void decay_state(f32x4 (&M)[MT], f32x2 over) {
 
 template <int DT, int DK, int DV, int HB, int MODE>
 struct ValueLds {
-    static constexpr bool STATE = MODE == S_ONLY || MODE == G_ONLY;
+    static constexpr bool STATE = MODE >= S_ONLY;
     static constexpr int ES = DT == KDA_BF16 ? 2 : 4, TOK = DT == KDA_BF16 ? 64 : 32, WAVES = HB * DV / 16;
     using TA = Tile<DK, ES>;
     using TC = Tile<DV, ES>;
@@ -206,7 +177,6 @@ struct ValueLds {
     __align__(16) double cum[2][HB][TOK];
     __align__(16) float del[2][HB][TOK], up[STATE ? 2 : 1][HB][TOK];
     f32x2 over[2][HB];
-    __align__(16) float red[MODE == DX ? WAVES * TOK : 1];   // r / delta by waves
 };
 
 // One workgroup per (segment, HB heads of a group): a and b rows are shared, wave w has 16 columns of head
@@ -219,8 +189,9 @@ __device__ __forceinline__ void value_pass(const Scan& L, int32_t slot, int32_t 
     using Lds = ValueLds<DT, DK, DV, HB, MODE>;
     using TA = typename Lds::TA;
     using TC = typename Lds::TC;
-    constexpr bool BF = DT == KDA_BF16, STATE = Lds::STATE, BACK = MODE == DX || MODE == G_ONLY;
-    constexpr int ES = Lds::ES, TOK = Lds::TOK, WAVES = Lds::WAVES, WPH = DV / 16;
+    constexpr bool BF = DT == KDA_BF16, STATE = Lds::STATE, BACK = MODE == DX || MODE == G_ONLY || MODE == G_CHUNKS;
+    constexpr bool OWN = MODE == S_ONLY || MODE == G_ONLY, CHUNKS = MODE == S_CHUNKS || MODE == G_CHUNKS;
+    constexpr int TOK = Lds::TOK, WAVES = Lds::WAVES, WPH = DV / 16;
     constexpr int IT = TOK / 16, MT = DK / 16, KK = DK / 32, JG = TOK / 32;
     constexpr int OS = ODT == KDA_BF16 ? 2 : 4;
     constexpr bool STAGED = BF && OS == 2 && !STATE;
@@ -228,8 +199,8 @@ __device__ __forceinline__ void value_pass(const Scan& L, int32_t slot, int32_t 
 
     Where w;
     if (!locate(L, slot, w)) return;
-    // nothing follows the last segment's own contribution, but the state behind the sequence
-    if (STATE && w.s == (BACK ? 0 : w.n_seg - 1) && !(MODE == S_ONLY && L.S_last)) return;
+    if (OWN && w.s == (BACK ? 0 : w.n_seg - 1)) return;            // nothing follows it
+    if (MODE == DX && w.hi == w.lo) return;
     const int t = threadIdx.x, lane = t & 63, q = lane >> 4, l16 = lane & 15;
     const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
     const int hb = wave / WPH, wc = wave % WPH;
@@ -302,40 +273,14 @@ __device__ __forceinline__ void value_pass(const Scan& L, int32_t slot, int32_t 
             for (int r = 0; r < 4; ++r)
                 M[mt][r] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rs, ((row(mt) + r) * DV + col) * 4, 0, 0));
     };
-    if constexpr (STATE) {
-        load_state(nullptr);
-    } else {
-        if constexpr (MODE == DX) {                  // <G, S> at the segment's end
-            const float* after = w.s < w.n_seg - 1 ? L.seg_states[S_STATE] + (seg_unit + L.H) * (DK * DV)
-                                 : L.S_last        ? L.S_last + unit * (DK * DV)
-                                                   : nullptr;
-            load_state(after);
-            const float* grad = w.n_seg > 1 ? L.seg_states[G_STATE] + seg_unit * (DK * DV)
-                                : L.m_in[G_STATE] ? L.m_in[G_STATE] + unit * (DK * DV)
-                                                  : nullptr;
-            const __amdgpu_buffer_rsrc_t rs = make_rsrc_u(grad, grad ? DK * DV * 4 : 0);
-            float sum = 0.f;
-#pragma unroll
-            for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const float x = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rs, ((row(mt) + r) * DV + col) * 4, 0, 0));
-                    sum = __builtin_fmaf(M[mt][r], x, sum);
-                    M[mt][r] = x;
-                }
-#pragma unroll
-            for (int off = 1; off < 64; off <<= 1) sum += __shfl_xor(sum, off, 64);
-            if (lane == 0) lds_put(lds.p, 4 * wave, sum);
-            lds_barrier();
-            if (wc == 0 && lane == 0 && live) {
-                float all = 0.f;
-                for (int i = 0; i < WPH; ++i) all += lds_get<float>(lds.p, 4 * (wave + i));
-                L.E[seg_unit] = all;
-            }
-        } else {
-            load_state(w.n_seg > 1 ? L.seg_states[ST] + seg_unit * (DK * DV) : L.m_in[ST] ? L.m_in[ST] + unit * (DK * DV) : nullptr);
-        }
-    }
+    // a chunk's place among the states of all chunks: of the one that token w.lo + off belongs to
+    auto chunk_unit = [&](int64_t off) {
+        const int64_t first = w.lo - static_cast<int64_t>(w.s) * L.seg;
+        return ((L.cu ? first / L.ct + w.n : static_cast<int64_t>(w.n) * L.c_per_seq) + (w.lo + off - first) / L.ct) * L.H + h;
+    };
+    if constexpr (OWN) load_state(nullptr);
+    else if constexpr (MODE == DX) load_state(L.chunk_states[ST] + chunk_unit(len - 1) * (DK * DV));
+    else load_state(w.n_seg > 1 ? L.seg_states[ST] + seg_unit * (DK * DV) : L.m_in[ST] ? L.m_in[ST] + unit * (DK * DV) : nullptr);
 
     // ---- operands' byte offsets, as in linear attention's pass.  16 bits, along the channels: channels
     // 32 kk + 8 q .. + 7 of token 16 it + l16; along the tokens: tokens 32 tg + 4 q .. + 3 and 32 tg + 16 + 4 q .. + 3,
@@ -369,9 +314,7 @@ __device__ __forceinline__ void value_pass(const Scan& L, int32_t slot, int32_t 
         }
     };
     const float D = (MODE == Y || MODE == DX) && L.D ? L.D[h] : 0.f;
-    float dD = 0.f;
-
-    const bool exact = MODE == DX || (STATE ? L.exact[ST] != 0 : L.m_out[ST] && w.s == (BACK ? 0 : w.n_seg - 1));
+    const bool exact = STATE ? L.exact[ST] != 0 : MODE == Y && L.m_out[ST] && w.s == w.n_seg - 1;
     for (int c = 0; c < n_chunks; ++c) {
         const int64_t off = chunk_at(c), tok0 = w.lo + off;
         const int n = chunk_n(off), buf = c & 1;
@@ -383,16 +326,14 @@ __device__ __forceinline__ void value_pass(const Scan& L, int32_t slot, int32_t 
         const float* del = lds.del[buf][hb];
 
         f32x4 O[IT];
-        u32x2 xr[MODE == DX && BF ? IT : 1];
-        f32x4 xf[MODE == DX ? IT : 1];
-        if constexpr (MODE == DX) {                  // x of the lane's tokens and columns
-            const uint32_t ld = static_cast<uint32_t>(L.x.ld);
-            const __amdgpu_buffer_rsrc_t rx = make_rsrc_u(L.x.p + tok0 * L.x.ld + h * TC::RB, (n - 1) * ld + TC::RB);
+        if constexpr (CHUNKS) {
+            if (MODE == S_CHUNKS ? off % L.ct == 0 : c == 0 || (off + TOK) % L.ct == 0) {
+                float* dst = L.chunk_states[ST] + chunk_unit(off) * (DK * DV);
+                if (live)
 #pragma unroll
-            for (int it = 0; it < IT; ++it) {
-                const uint32_t at = (16 * it + l16) * ld + (16 * wc + 4 * q) * ES;
-                if constexpr (BF) xr[it] = __builtin_amdgcn_raw_buffer_load_b64(rx, at, 0, 0);
-                else xf[it] = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(rx, at, 0, 0));
+                    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) dst[(row(mt) + r) * DV + col] = chunk_sign(c) * M[mt][r];
             }
         }
         if constexpr (!STATE) {
@@ -417,7 +358,7 @@ __device__ __forceinline__ void value_pass(const Scan& L, int32_t slot, int32_t 
                         u32x4 hi, lo;
 #pragma unroll
                         for (int hh = 0; hh < 2; ++hh) {
-                            const f32x4 x = P[hh] * score_weights<BACK, !BACK, false>(lds.cum[buf][i], lds.del[buf][i], it, 2 * tg + hh, q, l16);
+                            const f32x4 x = P[hh] * score_weights<BACK>(lds.cum[buf][i], lds.del[buf][i], it, 2 * tg + hh, q, l16);
                             uint32_t h0_, o0, h1, o1;
                             split_pair(x[0], x[1], h0_, o0);
                             split_pair(x[2], x[3], h1, o1);
@@ -442,7 +383,7 @@ __device__ __forceinline__ void value_pass(const Scan& L, int32_t slot, int32_t 
 #pragma unroll
                 for (int i = 0; i < HB; ++i)
                     lds_put(lds.p + i * Lds::P_BYTES, wave * 1024 + lane * 16,
-                            P * score_weights<BACK, !BACK, false>(lds.cum[buf][i], lds.del[buf][i], it, jt, q, l16));
+                            P * score_weights<BACK>(lds.cum[buf][i], lds.del[buf][i], it, jt, q, l16));
             }
             // ---- the state's part
 #pragma unroll
@@ -450,26 +391,21 @@ __device__ __forceinline__ void value_pass(const Scan& L, int32_t slot, int32_t 
             if constexpr (BF) {
 #pragma unroll
                 for (int kk = 0; kk < KK; ++kk) {
-                    u32x4 hi, mid, lo, a[IT];
+                    u32x4 hi, lo, a[IT];
 #pragma unroll
                     for (int it = 0; it < IT; ++it) a[it] = channels(lds.a, it, kk);
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         const f32x4& m = M[2 * kk + (e >> 1)];
-                        uint32_t x, y, z = 0;
-                        if constexpr (MODE == DX) split3(m[2 * (e & 1)], m[2 * (e & 1) + 1], x, y, z);
-                        else split_pair(m[2 * (e & 1)], m[2 * (e & 1) + 1], x, y);
+                        uint32_t x, y;
+                        split_pair(m[2 * (e & 1)], m[2 * (e & 1) + 1], x, y);
                         hi[e] = x;
-                        mid[e] = y;
-                        lo[e] = z;
+                        lo[e] = y;
                     }
 #pragma unroll
                     for (int it = 0; it < IT; ++it) O[it] = mfma_bf16(hi, a[it], O[it]);
 #pragma unroll
-                    for (int it = 0; it < IT; ++it) O[it] = mfma_bf16(mid, a[it], O[it]);
-                    if constexpr (MODE == DX)
-#pragma unroll
-                        for (int it = 0; it < IT; ++it) O[it] = mfma_bf16(lo, a[it], O[it]);
+                    for (int it = 0; it < IT; ++it) O[it] = mfma_bf16(lo, a[it], O[it]);
                 }
             } else {
 #pragma unroll
@@ -486,15 +422,6 @@ __device__ __forceinline__ void value_pass(const Scan& L, int32_t slot, int32_t 
             for (int it = 0; it < IT; ++it) {
                 const double ci = cum[16 * it + l16];
                 O[it] *= chunk_sign(c) * pow2(BACK ? all - ci : ci);
-                if constexpr (MODE == DX) {          // r / delta
-                    if constexpr (BF) xf[it] = f32x4{lo_f32(xr[it][0]), hi_f32(xr[it][0]), lo_f32(xr[it][1]), hi_f32(xr[it][1])};
-                    float s = 0.f;
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) s = __builtin_fmaf(xf[it][r], O[it][r], s);
-                    s += __shfl_xor(s, 16, 64);
-                    s += __shfl_xor(s, 32, 64);
-                    if (q == 0) lds.red[wave * TOK + 16 * it + l16] = s;
-                }
             }
         }
         if (table >= 0 && c + 1 < n_chunks) decays(c + 1, dt_next);
@@ -532,21 +459,11 @@ __device__ __forceinline__ void value_pass(const Scan& L, int32_t slot, int32_t 
                     for (int r = 0; r < 4; ++r) O[it] = mfma_f32(__uint_as_float(vf[jt][r]), P[r], O[it]);
                 }
             }
-            // ---- lane l16 holds token 16 it + l16, four neighbouring columns: D's part, and x . u
+            // ---- lane l16 holds token 16 it + l16, four neighbouring columns
 #pragma unroll
             for (int it = 0; it < IT; ++it) {
-                const f32x4 own = widen(lds_c, own_at(it));
-                if constexpr (MODE == Y) {
-                    if (L.D) O[it] += D * own;
-                } else {
-                    f32x4 x;
-                    if constexpr (BF) x = f32x4{lo_f32(xr[it][0]), hi_f32(xr[it][0]), lo_f32(xr[it][1]), hi_f32(xr[it][1])};
-                    else x = xf[it];
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) dD = __builtin_fmaf(x[r], own[r], dD);
-                    const float di = del[16 * it + l16];
-                    O[it] = O[it] * di + D * own;
-                }
+                if constexpr (MODE == DX) O[it] *= del[16 * it + l16];
+                if (L.D) O[it] += D * widen(lds_c, own_at(it));
             }
             // ---- out, through c's tile (which all waves have read by now)
             if constexpr (STAGED) {
@@ -621,15 +538,6 @@ __device__ __forceinline__ void value_pass(const Scan& L, int32_t slot, int32_t 
         if (c + 1 < n_chunks) load_b(c + 1);
         if constexpr (!STATE)
             if (c + 1 < n_chunks) load_a(c + 1);
-        if constexpr (MODE == DX) {
-            for (int e = t; e < HB * TOK; e += WAVES * 64) {
-                const int i = e / TOK, at = e % TOK;
-                float r = 0.f;
-#pragma unroll
-                for (int x = 0; x < WPH; ++x) r += lds.red[(i * WPH + x) * TOK + at];
-                if (at < n && h0 + i < h_end) L.xr[(h0 + i) * L.total + tok0 + at] = r;
-            }
-        }
         if constexpr (STAGED) {
             const uint32_t orow = static_cast<uint32_t>(L.out[0].ld);
             int tt = t;                              // formed anew in each chunk: no registers over the loop
@@ -651,28 +559,16 @@ __device__ __forceinline__ void value_pass(const Scan& L, int32_t slot, int32_t 
     }
 
     float* dst = nullptr;
-    if constexpr (STATE) dst = L.seg_states[ST] + seg_unit * (DK * DV);
-    else if (L.m_out[ST] && w.s == (BACK ? 0 : w.n_seg - 1)) dst = L.m_out[ST] + unit * (DK * DV);
+    if constexpr (OWN) dst = L.seg_states[ST] + seg_unit * (DK * DV);
+    else if (MODE != DX && L.m_out[ST] && w.s == (BACK ? 0 : w.n_seg - 1)) dst = L.m_out[ST] + unit * (DK * DV);
     if (dst && live) {
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
             for (int r = 0; r < 4; ++r) dst[(row(mt) + r) * DV + col] = chunk_sign(n_chunks) * M[mt][r];
     }
-    if constexpr (STATE) {
+    if constexpr (OWN) {
         if (table >= 0 && h0 + table < h_end && lane == 0) L.seg_log[ST][static_cast<int64_t>(slot) * L.H + h0 + table] = log_sum;
-    }
-    if constexpr (MODE == DX) {
-#pragma unroll
-        for (int off = 1; off < 64; off <<= 1) dD += __shfl_xor(dD, off, 64);
-        lds_barrier();                               // (the first chunk's E may still be read)
-        if (lane == 0) lds_put(lds.p, 4 * wave, dD);
-        lds_barrier();
-        if (wc == 0 && lane == 0 && live) {
-            float all = 0.f;
-            for (int i = 0; i < WPH; ++i) all += lds_get<float>(lds.p, 4 * (wave + i));
-            L.dDp[seg_unit] = all;
-        }
     }
 }
 
@@ -685,7 +581,7 @@ __device__ __forceinline__ bool unit_of(uint32_t units, int32_t passes, uint32_t
 }
 
 template <int DT, int ODT, int DK, int DV, int HB, int MODE>
-__global__ void __launch_bounds__(HB * DV * 4, HB * DV == 128 && MODE != DX ? 4 : 2) value_kernel(Scan L) {
+__global__ void __launch_bounds__(HB * DV * 4, HB * DV == 128 ? 4 : 2) value_kernel(Scan L) {
     __shared__ ValueLds<DT, DK, DV, HB, MODE> lds;
     uint32_t unit;
     int32_t pass;
@@ -693,431 +589,439 @@ __global__ void __launch_bounds__(HB * DV * 4, HB * DV == 128 && MODE != DX ? 4 
     const uint32_t blocks = static_cast<uint32_t>(L.blocks) * L.G;
     value_pass<DT, ODT, DK, DV, HB, MODE>(L, unit / blocks, unit % blocks, lds);
 }
-// The segments' states: S, or G, or both.
-template <int DT, int DK, int DV, int HB>
-__global__ void __launch_bounds__(HB * DV * 4, HB * DV == 128 ? 4 : 2) state_kernel(Scan L, int32_t first, int32_t passes) {
+// The segments' own contributions to S, or G, or both; or the states of all chunks.
+template <int DT, int DK, int DV, int HB, bool CHUNKS>
+__global__ void __launch_bounds__(HB * DV * 4, HB * DV == 128 ? 4 : 2) state_kernel(Scan L, int32_t passes) {
+    constexpr int SM = CHUNKS ? S_CHUNKS : S_ONLY, GM = CHUNKS ? G_CHUNKS : G_ONLY;
     __shared__ union {
-        ValueLds<DT, DK, DV, HB, S_ONLY> s;
-        ValueLds<DT, DK, DV, HB, G_ONLY> g;
+        ValueLds<DT, DK, DV, HB, SM> s;
+        ValueLds<DT, DK, DV, HB, GM> g;
     } lds;
     uint32_t unit;
     int32_t pass;
     if (!unit_of(static_cast<uint32_t>(L.slots) * L.blocks * L.G, passes, unit, pass)) return;
     const uint32_t blocks = static_cast<uint32_t>(L.blocks) * L.G;
-    if (first + pass == S_STATE) value_pass<DT, DT, DK, DV, HB, S_ONLY>(L, unit / blocks, unit % blocks, lds.s);
-    else value_pass<DT, DT, DK, DV, HB, G_ONLY>(L, unit / blocks, unit % blocks, lds.g);
+    if (pass == S_STATE) value_pass<DT, DT, DK, DV, HB, SM>(L, unit / blocks, unit % blocks, lds.s);
+    else value_pass<DT, DT, DK, DV, HB, GM>(L, unit / blocks, unit % blocks, lds.g);
 }
 
 // Segment states: from each segment's own contribution to the state it starts from (S) or that follows it (G), in
 // place.  Grid (sequence * H + head, element blocks of 1024, pass); eight segments' loads at a time.
-__global__ void __launch_bounds__(256) scan_kernel(Scan L, int32_t elems, int32_t first) {
-    const int ST = first + blockIdx.z;
+__global__ void __launch_bounds__(256) scan_kernel(Scan L, int32_t elems) {
+    const int ST = blockIdx.z;
     const bool back = ST == G_STATE;
     const int32_t n = blockIdx.x / L.H, h = blockIdx.x % L.H;
     const int32_t e = blockIdx.y * 1024 + threadIdx.x * 4;
     int64_t lo, hi;
     seq_range(L, n, lo, hi);
     const int32_t n_seg = segments(L, hi - lo);
-    float* last = back ? nullptr : L.S_last;
-    if (n_seg == 1 && !last) return;
+    if (n_seg == 1) return;
     const int64_t slot0 = L.cu ? first_slot(L, n) : static_cast<int64_t>(n) * n_seg;
-    const int64_t unit = static_cast<int64_t>(n) * L.H + h;
     f32x4 x = zero4();
-    if (L.m_in[ST]) x = *reinterpret_cast<const f32x4*>(L.m_in[ST] + unit * elems + e);
+    if (L.m_in[ST]) x = *reinterpret_cast<const f32x4*>(L.m_in[ST] + (static_cast<int64_t>(n) * L.H + h) * elems + e);
     auto index = [&](int32_t i) { return (slot0 + (back ? n_seg - 1 - i : i)) * L.H + h; };
     auto slot = [&](int32_t i) { return reinterpret_cast<f32x4*>(L.seg_states[ST] + index(i) * elems + e); };
-    const int32_t steps = last ? n_seg : n_seg - 1;  // segments whose own contribution is taken in
     f32x4 ahead = *slot(0);                          // read before the batch before it writes its place
     *slot(0) = x;
-    for (int32_t i0 = 0; i0 < steps; i0 += 8) {
+    for (int32_t i0 = 0; i0 < n_seg - 1; i0 += 8) {
         f32x4 own[9];
         double lg[8];
         own[0] = ahead;
 #pragma unroll
-        for (int32_t j = 1; j < 9; ++j) own[j] = i0 + j < steps ? *slot(i0 + j) : zero4();
+        for (int32_t j = 1; j < 9; ++j) own[j] = i0 + j < n_seg - 1 ? *slot(i0 + j) : zero4();
 #pragma unroll
-        for (int32_t j = 0; j < 8; ++j) lg[j] = i0 + j < steps ? L.seg_log[ST][index(i0 + j)] : 0.0;
+        for (int32_t j = 0; j < 8; ++j) lg[j] = i0 + j < n_seg - 1 ? L.seg_log[ST][index(i0 + j)] : 0.0;
         ahead = own[8];
 #pragma unroll
         for (int32_t j = 0; j < 8; ++j) {
-            if (i0 + j >= steps) break;
+            if (i0 + j >= n_seg - 1) break;
             const double l = exp2(lg[j]);
             const float l_hi = static_cast<float>(l), l_lo = static_cast<float>(l - static_cast<double>(l_hi));
 #pragma unroll
             for (int r = 0; r < 4; ++r) x[r] = __builtin_fmaf(x[r], l_hi, __builtin_fmaf(x[r], l_lo, own[j][r]));
-            if (i0 + j + 1 < n_seg) *slot(i0 + j + 1) = x;
+            *slot(i0 + j + 1) = x;                   // segment i's end is what segment i + 1 starts from
         }
     }
-    if (last) *reinterpret_cast<f32x4*>(last + unit * elems + e) = x;
 }
 
-// ---------------------------------------------------------------- dC and dB
+// ---------------------------------------------------------------- dC, dB and the ways between tokens
 
-template <int DT, int DK, int DV, int HB, bool BACK>
-struct SharedLds {
-    static constexpr int ES = DT == KDA_BF16 ? 2 : 4, TOK = DT == KDA_BF16 ? 64 : 32, WAVES = DK / 16;
+// Tokens of a chunk of the gradients: as many as their rows, of one group and of two heads in turn, leave room for in
+// LDS (160 KB), so that the chunks' states, 8 d_k d_v bytes a head written and read, are few.
+template <int DT, int DK, int DV>
+constexpr int grad_tokens() {
+    return (DT == KDA_BF16 ? (DK == 128 ? 128 : 64) : (DV == 64 ? 64 : 32)) / (DT == KDA_BF16 && DK == 128 && DV == 128 ? 2 : 1);
+}
+
+// A chunk's decays, one wave per (chunk, head).
+template <int DT, int CT>
+__global__ void __launch_bounds__(256) table_kernel(Scan L) {
+    const int64_t u = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6);
+    const int lane = threadIdx.x & 63;
+    if (u >= static_cast<int64_t>(L.c_slots) * L.H) return;
+    const int32_t slot = static_cast<int32_t>(u / L.H), h = static_cast<int32_t>(u % L.H);
+    Where w;
+    if (!locate(L, slot, w)) return;
+    const float bias = L.bias ? L.bias[h] : 0.f;
+    const int n = static_cast<int>(w.hi - w.lo);
+    double d0 = 0.0, s0 = 0.0;
+#pragma unroll
+    for (int b = 0; b < (CT + 63) / 64; ++b) {
+        const int i = 64 * b + lane;
+        Strength s = {0.f, 0.f};
+        if (i < n) s = strength(load_as_f32<DT>(L.dt.p + (w.lo + i) * L.dt.ld, h), bias);
+        const double d = d0 + prefix_sum(static_cast<double>(s.delta)), o = s0 + prefix_sum(static_cast<double>(s.slope));
+        d0 = lane_value(d, 63);
+        s0 = lane_value(o, 63);
+        if (i < CT) {
+            L.t_dsum[u * CT + i] = d;
+            L.t_del[u * CT + i] = s.delta;
+            L.t_ssum[u * CT + i] = static_cast<float>(o);
+        }
+    }
+}
+
+template <int DT, int DK, int DV>
+struct GradLds {
+    static constexpr int ES = DT == KDA_BF16 ? 2 : 4, CT = grad_tokens<DT, DK, DV>(), WAVES = DK / 16;
     using TA = Tile<DV, ES>;
     using TC = Tile<DK, ES>;
-    static constexpr int A_BYTES = TOK / TA::R * TA::PIECE;
-    __align__(16) uint8_t b[2 * A_BYTES];            // this head's and the next one's
-    __align__(16) uint8_t a[2 * A_BYTES];
-    __align__(16) uint8_t c[TOK / TC::R * TC::PIECE];
-    __align__(16) uint8_t p[(ES == 2 ? 12 : 3) * 1024];    // scores, summed over the heads
-    Decays<TOK, HB, BACK> t;
-    // dC: p by waves, sums of z over j by 32 tokens j (fp32: 16), of z / delta over i by 16 tokens i, z_jj / delta_j
-    static constexpr int RED = BACK ? 1 : WAVES + 2 + TOK / 16 + 1;
-    float red[BACK ? 1 : HB][RED][BACK ? 1 : TOK];
+    static constexpr int A_BYTES = CT / TA::R * TA::PIECE, C_BYTES = CT / TC::R * TC::PIECE;
+    // scores are made in groups: a tile of 16 tokens by 32 (fp32: 16) others on its near side
+    static constexpr int IT = CT / 16, TG = DT == KDA_BF16 ? CT / 32 : IT;
+    static constexpr int GROUPS = DT == KDA_BF16 ? TG * (TG + 1) : IT * (IT + 1) / 2, G_BYTES = DT == KDA_BF16 ? 2048 : 1024;
+    static constexpr int TILES = DT == KDA_BF16 ? 2 : 1;           // of a group
+    __align__(16) uint8_t B[C_BYTES];
+    __align__(16) uint8_t C[C_BYTES];
+    // x and dy of a head and of the next one; in the end the scores, summed over the heads, one direction at a time
+    __align__(16) uint8_t xy[4 * A_BYTES];
+    static_assert(GROUPS * G_BYTES <= 4 * A_BYTES, "the scores take the place of the rows");
+    __align__(16) double dsum[2][CT];
+    __align__(16) float del[2][CT], ssum[2][CT];
+    // p and r / delta by waves, sums of z over j and of z / delta over i by groups, z_jj / delta_j
+    static constexpr int P = 0, R = WAVES, ROWS = 2 * WAVES, COLS = ROWS + TG, DIAG = COLS + TG;
+    float red[DIAG + 1][CT];
+    float sums[4][WAVES];
+    // direction 0: outputs i by groups of j <= i; direction 1: outputs j by groups of i >= j, mirrored.  Group number of
+    // (output tile, group of others), and back.
+    static __host__ __device__ constexpr int number(int dir, int out, int tg) {
+        const int o = dir ? IT - 1 - out : out, g = dir ? TG - 1 - tg : tg;
+        return g * IT - (TILES == 2 ? g * (g - 1) : g * (g - 1) / 2) + o - TILES * g;
+    }
+    static __device__ __forceinline__ void group(int dir, int k, int& out, int& tg) {
+        int g = 0;
+        for (int n = IT; k >= n; n -= TILES) {
+            k -= n;
+            ++g;
+        }
+        out = dir ? IT - 1 - (TILES * g + k) : TILES * g + k;
+        tg = dir ? TG - 1 - g : g;
+    }
+    static __host__ __device__ constexpr bool near(int dir, int out, int tg) {
+        return dir ? TILES * tg + TILES - 1 >= out : TILES * tg <= out;
+    }
 };
 
-// The sum over a row of 16 lanes, in its last one.
-__device__ __forceinline__ float row_sum(float x) {
-    auto add = [](float y, auto ctrl) {
-        return y + __uint_as_float(__builtin_amdgcn_update_dpp(0, __float_as_uint(y), decltype(ctrl)::value, 0xf, 0xf, false));
-    };
-    x = add(x, std::integral_constant<int, 0x111>{});              // row_shr:1, :2, :4, :8
-    x = add(x, std::integral_constant<int, 0x112>{});
-    x = add(x, std::integral_constant<int, 0x114>{});
-    return add(x, std::integral_constant<int, 0x118>{});
+// The sum of a value over the four lanes of one l16, in all of them: rows of 16 lanes and halves of the wave swapped.
+__device__ __forceinline__ float sum_q(float x) {
+    const uint32_t u = __float_as_uint(x);
+    const auto a = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+    const float y = __uint_as_float(a[0]) + __uint_as_float(a[1]);
+    const uint32_t v = __float_as_uint(y);
+    const auto b = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+    return __uint_as_float(b[0]) + __uint_as_float(b[1]);
+}
+__device__ __forceinline__ float sum_wave(float x) {
+#pragma unroll
+    for (int off = 1; off < 16; off <<= 1) x += __shfl_xor(x, off, 64);
+    return sum_q(x);
 }
 
-// One workgroup per (segment, up to HB heads of a group); wave w has the output columns 16 w .. 16 w + 15 and their
-// states (rows d_v) of all its heads.  The heads' rows come one head after the other, the next one's under this one's
-// products.  The output's sum over the heads is formed in registers, and since c is the group's, its product with
-// the scores is formed once, with their sum.
-template <int DT, int DK, int DV, int HB, bool BACK>
-__device__ __forceinline__ void shared_pass(const Scan& L, int32_t slot, int32_t block, SharedLds<DT, DK, DV, HB, BACK>& lds) {
-    using Lds = SharedLds<DT, DK, DV, HB, BACK>;
+// One workgroup per (chunk, block of a group's heads); wave w has the output channels 16 w .. 16 w + 15 of dC and dB, and
+// groups of scores of either direction.  B and C are read once, the heads' rows and states come one head after the
+// other, the next one's under this one's products.  The scores' products with B and C are formed once, from their sums
+// over the heads (two bf16 terms: they only feed 16-bit outputs).  The states are read as three (exact), for p, r and
+// what comes of them is handed out in fp32.
+template <int DT, int DK, int DV>
+__device__ __forceinline__ void grad_pass(const Scan& L, int32_t slot, int32_t block, GradLds<DT, DK, DV>& lds) {
+    using Lds = GradLds<DT, DK, DV>;
     using TA = typename Lds::TA;
     using TC = typename Lds::TC;
     constexpr bool BF = DT == KDA_BF16;
-    constexpr int ES = Lds::ES, TOK = Lds::TOK, WAVES = Lds::WAVES;
-    constexpr int IT = TOK / 16, MT = DV / 16, KK = DV / 32, JG = TOK / 32;
-    constexpr int ST = BACK ? G_STATE : S_STATE;
+    constexpr int ES = Lds::ES, CT = Lds::CT, WAVES = Lds::WAVES, IT = Lds::IT, TG = Lds::TG, TILES = Lds::TILES;
+    constexpr int KV = DV / 32, KC = DK / 32, NS = DV / 16;
+    constexpr int ROUNDS = (2 * Lds::GROUPS + WAVES - 1) / WAVES;
 
     Where w;
-    if (!locate(L, slot, w)) return;
+    if (!locate(L, slot, w) || w.hi == w.lo) return;
     const int t = threadIdx.x, lane = t & 63, q = lane >> 4, l16 = lane & 15;
     const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
     const int32_t rep = L.H / L.G, g = block / L.blocks, blk = block % L.blocks;
-    const int32_t h0 = g * rep + blk * HB, left = (g + 1) * rep - h0, heads = left < HB ? left : HB;
-    const int64_t len = w.hi - w.lo;
-    const int n_chunks = static_cast<int>((len + TOK - 1) / TOK);
-    if (n_chunks == 0) return;
+    const int32_t h0 = g * rep + blk * L.heads, left = (g + 1) * rep - h0, heads = left < L.heads ? left : L.heads;
+    const int n = static_cast<int>(w.hi - w.lo);
+    const int64_t units = static_cast<int64_t>(slot) * L.H + h0;   // of the block's first head
 
-    const In &ra = BACK ? L.x : L.dy, &rb = BACK ? L.dy : L.x, &rc = BACK ? L.C : L.B;
-    auto chunk_at = [&](int c) { return static_cast<int64_t>(BACK ? n_chunks - 1 - c : c) * TOK; };
-    auto chunk_n = [&](int64_t off) { return static_cast<int>(len - off < TOK ? len - off : TOK); };
-    auto load_ab = [&](int c, int hb, int buf) {
-        const int64_t off = chunk_at(c);
-        const int n = chunk_n(off);
-        fetch_rows<TA, TOK, WAVES>(lds.a + buf * Lds::A_BYTES, ra.p + (w.lo + off) * ra.ld + (h0 + hb) * TA::RB, static_cast<uint32_t>(ra.ld), n, wave, lane);
-        fetch_rows<TA, TOK, WAVES>(lds.b + buf * Lds::A_BYTES, rb.p + (w.lo + off) * rb.ld + (h0 + hb) * TA::RB, static_cast<uint32_t>(rb.ld), n, wave, lane);
+    auto load_head = [&](int k, int buf) {
+        fetch_rows<TA, CT, WAVES>(lds.xy + buf * 2 * Lds::A_BYTES, L.x.p + w.lo * L.x.ld + (h0 + k) * TA::RB, static_cast<uint32_t>(L.x.ld), n, wave, lane);
+        fetch_rows<TA, CT, WAVES>(lds.xy + (buf * 2 + 1) * Lds::A_BYTES, L.dy.p + w.lo * L.dy.ld + (h0 + k) * TA::RB, static_cast<uint32_t>(L.dy.ld), n, wave, lane);
     };
-    auto load_c = [&](int c) {
-        const int64_t off = chunk_at(c);
-        fetch_rows<TC, TOK, WAVES>(lds.c, rc.p + (w.lo + off) * rc.ld + g * TC::RB, static_cast<uint32_t>(rc.ld), chunk_n(off), wave, lane);
-    };
-    auto dt_of = [&](int c, int hb) {
-        const int64_t off = chunk_at(c);
-        return load_dt<DT>(L, w.lo + off, chunk_n(off), h0 + hb, lane);
-    };
-    auto decays = [&](int c, int hb, float dt) {
-        make_decays<TOK, HB, BACK>(lds.t, c, hb, dt, L.bias ? L.bias[h0 + hb] : 0.f, L.A[h0 + hb], chunk_n(chunk_at(c)), lane);
-    };
-    load_ab(0, 0, 0);
-    load_c(0);
-    for (int hb = wave; hb < heads; hb += WAVES) decays(0, hb, dt_of(0, hb));
-
-    // ---- the states, transposed: row row(mt) + r of d_v, column 16 wave + l16 of d_k
-    auto row = [&](int mt) { return BF ? 32 * (mt >> 1) + 8 * q + 4 * (mt & 1) : 16 * mt + 4 * q; };
-    const int col = 16 * wave + l16;
-    f32x4 M[HB][MT];
+    f32x4 S[NS], G[NS];                              // row 16 wave + l16 of the states, d_v along the contraction
+    auto load_state = [&](f32x4 (&X)[NS], const float* all, int k) {
+        const float* p = all + (units + k) * (DK * DV) + (16 * wave + l16) * DV;
 #pragma unroll
-    for (int hb = 0; hb < HB; ++hb) {
-        const float* src = nullptr;
-        if (hb < heads) {
-            if (w.n_seg > 1) src = L.seg_states[ST] + (static_cast<int64_t>(slot) * L.H + h0 + hb) * (DK * DV);
-            else if (L.m_in[ST]) src = L.m_in[ST] + (static_cast<int64_t>(w.n) * L.H + h0 + hb) * (DK * DV);
-        }
-        const __amdgpu_buffer_rsrc_t rs = make_rsrc_u(src, src ? DK * DV * 4 : 0);
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
-            M[hb][mt] = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(rs, (col * DV + row(mt)) * 4, 0, 0));
-    }
+        for (int i = 0; i < NS; ++i) X[i] = *reinterpret_cast<const f32x4*>(p + (BF ? 32 * (i >> 1) + 8 * q + 4 * (i & 1) : 16 * i + 4 * q));
+    };
+    struct Row {
+        double dsum;
+        float del, ssum;
+    };
+    auto load_row = [&](int k) {
+        const int64_t at = (units + k) * CT + t;
+        return Row{L.t_dsum[at], L.t_del[at], L.t_ssum[at]};
+    };
+    auto put_row = [&](int buf, const Row& r) {
+        lds.dsum[buf][t] = r.dsum;
+        lds.del[buf][t] = r.del;
+        lds.ssum[buf][t] = r.ssum;
+    };
+    static_assert(WAVES * 64 >= CT, "a lane per token");
+    fetch_rows<TC, CT, WAVES>(lds.B, L.B.p + w.lo * L.B.ld + g * TC::RB, static_cast<uint32_t>(L.B.ld), n, wave, lane);
+    fetch_rows<TC, CT, WAVES>(lds.C, L.C.p + w.lo * L.C.ld + g * TC::RB, static_cast<uint32_t>(L.C.ld), n, wave, lane);
+    load_head(0, 0);
+    load_state(S, L.chunk_states[S_STATE], 0);
+    load_state(G, L.chunk_states[G_STATE], 0);
+    if (t < CT) put_row(0, load_row(0));
 
-    uint32_t chan[2], tok[2];
+    uint32_t chan[2], chan_c[2];
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
         chan[x] = TA::at(l16, 4 * x + q);
-        tok[x] = TA::at(4 * q + (l16 >> 2), 4 * x + (l16 & 3));
+        chan_c[x] = TC::at(l16, 4 * x + q);
     }
     const uint32_t tok_c = TC::at(4 * q + (l16 >> 2), 2 * wave + ((l16 & 3) >> 1)) + 8 * (l16 & 1);
-    auto channels = [&](const uint8_t* sm, int it, int kk) {
-        return lds_get<u32x4>(sm, chan[kk & 1] + it * TA::ROWS16 + (kk >> 1) * 128);
-    };
-    auto channels_c = [&](int it, int kk) {          // of c's tile
-        return lds_get<u32x4>(lds.c, TC::at(l16, (4 * kk + q) & 7) + it * TC::ROWS16 + (kk >> 1) * 128);
-    };
-    auto tokens = [&](uint32_t at, const uint8_t* sm, int rows16) {
-        const u32x2 x = lds_transpose(sm + at), y = lds_transpose(sm + at + rows16);
+    auto tokens = [&](const uint8_t* sm, int tg) {   // the wave's channels of B or C, 32 tokens along the contraction
+        const u32x2 x = lds_transpose(sm + tok_c + 2 * tg * TC::ROWS16), y = lds_transpose(sm + tok_c + (2 * tg + 1) * TC::ROWS16);
         return u32x4{x[0], x[1], y[0], y[1]};
     };
-    // the scores this wave makes: 16 bits: group wave, of tiles (it, 2 tg) and (it, 2 tg + 1); fp32: tile (it, jt)
-    constexpr int GROUPS = BF ? 6 : 3, ROUNDS = (GROUPS + WAVES - 1) / WAVES, TILES = BF ? 2 : 1;
-    auto tile_of = [&](int grp, int hh, int& it, int& jt) {
+    // 16 rows' dot products with 16 others, channels along the contraction
+    auto dots = [&](const uint8_t* rows, const uint8_t* cols, int rt, int ct, auto wide, f32x4 acc) {
+        constexpr bool WIDE = decltype(wide)::value;               // B and C, or x and dy
+        using TT = std::conditional_t<WIDE, TC, TA>;
         if constexpr (BF) {
-            const int tg = BACK ? (grp < 4) : (grp >= 4);
-            it = BACK ? (grp & 3) : (grp < 4 ? grp : grp - 2);
-            jt = 2 * tg + hh;
+#pragma unroll
+            for (int kk = 0; kk < (WIDE ? KC : KV); ++kk) {
+                const uint32_t at = (WIDE ? chan_c : chan)[kk & 1] + (kk >> 1) * 128;
+                acc = mfma_bf16(lds_get<u32x4>(rows, at + rt * TT::ROWS16), lds_get<u32x4>(cols, at + ct * TT::ROWS16), acc);
+            }
         } else {
-            it = BACK ? (grp == 1) : (grp > 0);
-            jt = BACK ? (grp > 0) : (grp == 1);
+#pragma unroll
+            for (int mt = 0; mt < (WIDE ? DK : DV) / 16; ++mt) {
+                const f32x4 a = lds_get<f32x4>(rows, TT::at(16 * rt + l16, 4 * mt + q)), b = lds_get<f32x4>(cols, TT::at(16 * ct + l16, 4 * mt + q));
+#pragma unroll
+                for (int r = 0; r < 4; ++r) acc = mfma_f32(a[r], b[r], acc);
+            }
+        }
+        return acc;
+    };
+    auto own = [&](const uint8_t* sm, int it) {      // token 16 it + l16's channels 16 wave + 4 q .. + 3
+        if constexpr (BF) {
+            const u32x2 x = lds_get<u32x2>(sm, TC::at(16 * it + l16, 2 * wave + (q >> 1)) + 8 * (q & 1));
+            return f32x4{lo_f32(x[0]), hi_f32(x[0]), lo_f32(x[1]), hi_f32(x[1])};
+        } else {
+            return lds_get<f32x4>(sm, TC::at(16 * it + l16, 4 * wave + q));
         }
     };
 
-    int step = 0;
-    float zA[BACK ? 1 : HB], zb[BACK ? 1 : HB];      // sums of z_ij (W_i - W_j)
+    f32x4 dC[IT], dB[IT], P[ROUNDS][TILES], CB[ROUNDS][TILES];
 #pragma unroll
-    for (int hb = 0; hb < (BACK ? 1 : HB); ++hb) zA[hb] = zb[hb] = 0.f;
-    for (int c = 0; c < n_chunks; ++c) {
-        const int64_t off = chunk_at(c), tok0 = w.lo + off;
-        const int n = chunk_n(off), buf = c & 1;
-        f32x4 O[IT], P[ROUNDS][TILES], CB[BACK ? 1 : ROUNDS][TILES];
-        u32x2 cr[!BACK && BF ? IT : 1];
-        f32x4 cf[!BACK && !BF ? IT : 1];
-#pragma unroll
-        for (int it = 0; it < IT; ++it) O[it] = zero4();
-#pragma unroll
-        for (int i = 0; i < ROUNDS; ++i)
-#pragma unroll
-            for (int hh = 0; hh < TILES; ++hh) P[i][hh] = zero4();
-        constexpr int CJ = BF ? JG : IT;
-        u32x4 vf[CJ];
-#pragma unroll
-        for (int hb = 0; hb < HB; ++hb) {
-            if (hb >= heads) break;
-            __builtin_amdgcn_s_waitcnt(vmcnt_imm(0));
-            lds_barrier();                           // this head's rows are there
-            const uint8_t *sa = lds.a + (step & 1) * Lds::A_BYTES, *sb = lds.b + (step & 1) * Lds::A_BYTES;
-            ++step;
-            const bool more = c + 1 < n_chunks;
-            if (hb + 1 < heads) load_ab(c, hb + 1, step & 1);
-            else if (more) load_ab(c + 1, 0, step & 1);
-            float dt_next = 0.f;
-            if (wave == WAVES - 1 && more) dt_next = dt_of(c + 1, hb);
-            if (hb == 0) {                           // what the chunk's heads share
-#pragma unroll
-                for (int j = 0; j < CJ; ++j) {
-                    if constexpr (BF) vf[j] = tokens(tok_c + 2 * j * TC::ROWS16, lds.c, TC::ROWS16);
-                    else
-#pragma unroll
-                        for (int r = 0; r < 4; ++r)
-                            vf[j][r] = lds_get<uint32_t>(lds.c, TC::at(16 * j + 4 * q + r, 4 * wave + (l16 >> 2)) + 4 * (l16 & 3));
-                }
-                if constexpr (!BACK) {               // C . B of the wave's scores, C of its tokens and columns
-                    const uint32_t ld = static_cast<uint32_t>(L.C.ld);
-                    const __amdgpu_buffer_rsrc_t rC = make_rsrc_u(L.C.p + tok0 * L.C.ld + g * TC::RB, (n - 1) * ld + TC::RB);
-#pragma unroll
-                    for (int it = 0; it < IT; ++it) {
-                        const uint32_t at = (16 * it + l16) * ld + (16 * wave + 4 * q) * ES;
-                        if constexpr (BF) cr[it] = __builtin_amdgcn_raw_buffer_load_b64(rC, at, 0, 0);
-                        else cf[it] = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(rC, at, 0, 0));
-                    }
-#pragma unroll
-                    for (int i = 0; i < ROUNDS; ++i) {
-                        const int grp = wave + i * WAVES;
-#pragma unroll
-                        for (int hh = 0; hh < TILES; ++hh) CB[i][hh] = zero4();
-                        if (grp >= GROUPS) continue;
-                        int it, jt;
-                        tile_of(grp, 0, it, jt);
-                        if constexpr (BF) {
-#pragma unroll
-                            for (int kk = 0; kk < DK / 32; ++kk) {
-                                const u32x4 a = __builtin_amdgcn_raw_buffer_load_b128(rC, (16 * it + l16) * ld + (32 * kk + 8 * q) * 2, 0, 0);
-#pragma unroll
-                                for (int hh = 0; hh < 2; ++hh) CB[i][hh] = mfma_bf16(channels_c(jt + hh, kk), a, CB[i][hh]);
-                            }
-                        } else {
-#pragma unroll
-                            for (int mt = 0; mt < DK / 16; ++mt) {
-                                const f32x4 a = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(rC, (16 * it + l16) * ld + (16 * mt + 4 * q) * 4, 0, 0));
-                                const f32x4 b = lds_get<f32x4>(lds.c, TC::at(16 * jt + l16, 4 * mt + q));
-#pragma unroll
-                                for (int r = 0; r < 4; ++r) CB[i][0] = mfma_f32(b[r], a[r], CB[i][0]);
-                            }
-                        }
-                    }
-                }
-            }
-            const double* cum = lds.t.cum[buf][hb];
-            const float* del = lds.t.del[buf][hb];
-            // ---- scores
+    for (int it = 0; it < IT; ++it) dC[it] = dB[it] = zero4();
+    for (int k = 0; k < heads; ++k) {
+        const int buf = k & 1;
+        __builtin_amdgcn_s_waitcnt(vmcnt_imm(0));
+        lds_barrier();                               // the head's rows and decays are there
+        const uint8_t *x = lds.xy + buf * 2 * Lds::A_BYTES, *dy = x + Lds::A_BYTES;
+        const double* dsum = lds.dsum[buf];
+        const float* del = lds.del[buf];
+        const bool more = k + 1 < heads;
+        // decays by the sum of delta between two tokens
+        const double A2 = static_cast<double>(L.A[h0 + k]) * LOG2E;
+        const float A_hi = static_cast<float>(A2), A_lo = static_cast<float>(A2 - static_cast<double>(A_hi));
+        auto decay = [&](float d) { return __builtin_amdgcn_exp2f(__builtin_fmaf(d, A_hi, d * A_lo)); };
+        Row next{};
+        if (more) {
+            load_head(k + 1, buf ^ 1);
+            if (t < CT) next = load_row(k + 1);
+        }
+        if (k == 0) {                                // what the heads share
 #pragma unroll
             for (int i = 0; i < ROUNDS; ++i) {
-                const int grp = wave + i * WAVES;
-                if (grp >= GROUPS) continue;
-                f32x4 X[TILES];
-                int it, jt;
-                tile_of(grp, 0, it, jt);
+                const int grp = wave + i * WAVES, dir = grp >= Lds::GROUPS;
 #pragma unroll
-                for (int hh = 0; hh < TILES; ++hh) X[hh] = zero4();
-                if constexpr (BF) {
+                for (int hh = 0; hh < TILES; ++hh) P[i][hh] = CB[i][hh] = zero4();
+                if (grp >= 2 * Lds::GROUPS) continue;
+                int out, tg;
+                Lds::group(dir, grp - dir * Lds::GROUPS, out, tg);
 #pragma unroll
-                    for (int kk = 0; kk < KK; ++kk) {
-                        const u32x4 a = channels(sa, it, kk);
-#pragma unroll
-                        for (int hh = 0; hh < 2; ++hh) X[hh] = mfma_bf16(channels(sb, jt + hh, kk), a, X[hh]);
-                    }
-                } else {
-#pragma unroll
-                    for (int mt = 0; mt < MT; ++mt) {
-                        const f32x4 a = lds_get<f32x4>(sa, TA::at(16 * it + l16, 4 * mt + q));
-                        const f32x4 b = lds_get<f32x4>(sb, TA::at(16 * jt + l16, 4 * mt + q));
-#pragma unroll
-                        for (int r = 0; r < 4; ++r) X[0] = mfma_f32(b[r], a[r], X[0]);
-                    }
-                }
-                if constexpr (BACK) {
-#pragma unroll
-                    for (int hh = 0; hh < TILES; ++hh) P[i][hh] += X[hh] * score_weights<true, false, true>(cum, del, it, jt + hh, q, l16);
-                } else {
-                    float rows = 0.f, diag = 0.f;
-                    const int ti = 16 * it + l16;
-                    const double di = lds.t.dsum[buf][hb][ti], si = lds.t.ssum[buf][hb][ti];
-#pragma unroll
-                    for (int hh = 0; hh < TILES; ++hh) {
-                        const int tj = 16 * (jt + hh) + 4 * q;
-                        const f32x4 dj = lds_get<f32x4>(del, 4 * tj), x = X[hh] * score_weights<false, false, false>(cum, del, it, jt + hh, q, l16);
-                        P[i][hh] += x * dj;
-                        f32x4 cols;
-#pragma unroll
-                        for (int r = 0; r < 4; ++r) {
-                            const float y = x[r] * CB[i][hh][r], below = tj + r < ti ? y : 0.f, z = below * dj[r];
-                            if (tj + r == ti) diag += y;
-                            rows += z;
-                            zA[hb] = __builtin_fmaf(z, static_cast<float>(di - lds.t.dsum[buf][hb][tj + r]), zA[hb]);
-                            zb[hb] = __builtin_fmaf(z, static_cast<float>(si - lds.t.ssum[buf][hb][tj + r]), zb[hb]);
-                            cols[r] = row_sum(below);
-                        }
-                        if (l16 == 15) *reinterpret_cast<f32x4*>(&lds.red[hb][WAVES + 2 + it][tj]) = cols;
-                    }
-                    rows += __shfl_xor(rows, 16, 64);
-                    rows += __shfl_xor(rows, 32, 64);
-                    if (q == 0) lds.red[hb][WAVES + (BF ? jt / 2 : jt)][ti] = rows;
-                    if (BF ? it / 2 == jt / 2 : it == jt) {        // the group of the tile's own tokens
-                        diag += __shfl_xor(diag, 16, 64);
-                        diag += __shfl_xor(diag, 32, 64);
-                        if (q == 0) lds.red[hb][Lds::RED - 1][ti] = diag;
-                    }
-                }
+                for (int hh = 0; hh < TILES; ++hh)
+                    CB[i][hh] = dots(dir ? lds.C : lds.B, dir ? lds.B : lds.C, TILES * tg + hh, out, std::true_type{}, CB[i][hh]);
             }
-            // ---- the state's part
-            f32x4 own[IT];
-#pragma unroll
-            for (int it = 0; it < IT; ++it) own[it] = zero4();
-            if constexpr (BF) {
-#pragma unroll
-                for (int kk = 0; kk < KK; ++kk) {
-                    u32x4 hi, mid, lo, a[IT];
-#pragma unroll
-                    for (int it = 0; it < IT; ++it) a[it] = channels(sa, it, kk);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const f32x4& m = M[hb][2 * kk + (e >> 1)];
-                        uint32_t x, y, z = 0;
-                        if constexpr (!BACK) split3(m[2 * (e & 1)], m[2 * (e & 1) + 1], x, y, z);
-                        else split_pair(m[2 * (e & 1)], m[2 * (e & 1) + 1], x, y);
-                        hi[e] = x;
-                        mid[e] = y;
-                        lo[e] = z;
-                    }
-#pragma unroll
-                    for (int it = 0; it < IT; ++it) own[it] = mfma_bf16(hi, a[it], own[it]);
-#pragma unroll
-                    for (int it = 0; it < IT; ++it) own[it] = mfma_bf16(mid, a[it], own[it]);
-                    if constexpr (!BACK)
-#pragma unroll
-                        for (int it = 0; it < IT; ++it) own[it] = mfma_bf16(lo, a[it], own[it]);
-                }
-            } else {
-#pragma unroll
-                for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-                    for (int it = 0; it < IT; ++it) {
-                        const f32x4 a = lds_get<f32x4>(sa, TA::at(16 * it + l16, 4 * mt + q));
-#pragma unroll
-                        for (int r = 0; r < 4; ++r) own[it] = mfma_f32(M[hb][mt][r], a[r], own[it]);
-                    }
-            }
-            const double all = cum[TOK - 1];
-#pragma unroll
-            for (int it = 0; it < IT; ++it) {
-                const double ci = cum[16 * it + l16];
-                own[it] *= chunk_sign(c) * (BACK ? del[16 * it + l16] * pow2(all - ci) : pow2(ci));
-                O[it] += own[it];
-                if constexpr (!BACK) {
-                    f32x4 cc;
-                    if constexpr (BF) cc = f32x4{lo_f32(cr[it][0]), hi_f32(cr[it][0]), lo_f32(cr[it][1]), hi_f32(cr[it][1])};
-                    else cc = cf[it];
-                    float s = 0.f;
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) s = __builtin_fmaf(cc[r], own[it][r], s);
-                    s += __shfl_xor(s, 16, 64);
-                    s += __shfl_xor(s, 32, 64);
-                    if (q == 0) lds.red[hb][wave][16 * it + l16] = s;
-                }
-            }
-            // ---- update
-            decay_state(M[hb], lds.t.over[buf][hb]);
-            const float* up = lds.t.up[buf][hb];
-            if constexpr (BF) {
-#pragma unroll
-                for (int tg = 0; tg < JG; ++tg) {
-                    const f32x4 w0 = lds_get<f32x4>(up, 4 * (32 * tg + 4 * q));
-                    const f32x4 w1 = lds_get<f32x4>(up, 4 * (32 * tg + 16 + 4 * q));
-                    u32x4 ch, cm, cl;
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const f32x4& ww = e < 2 ? w0 : w1;
-                        const float c0 = lo_f32(vf[tg][e]) * ww[2 * (e & 1)], c1 = hi_f32(vf[tg][e]) * ww[2 * (e & 1) + 1];
-                        uint32_t x, y, z = 0;
-                        if constexpr (!BACK) split3(c0, c1, x, y, z);
-                        else split_pair(c0, c1, x, y);
-                        ch[e] = x;
-                        cm[e] = y;
-                        cl[e] = z;
-                    }
-#pragma unroll
-                    for (int mt = 0; mt < MT; ++mt) {
-                        const u32x4 kt = tokens(tok[(mt >> 1) & 1] + 2 * tg * TA::ROWS16 + (mt >> 2) * 128 + 8 * (mt & 1), sb,
-                                                TA::ROWS16);
-                        if constexpr (!BACK) M[hb][mt] = mfma_bf16(kt, cl, M[hb][mt]);
-                        M[hb][mt] = mfma_bf16(kt, cm, M[hb][mt]);
-                        M[hb][mt] = mfma_bf16(kt, ch, M[hb][mt]);
-                    }
-                }
-            } else {
-#pragma unroll
-                for (int jt = 0; jt < IT; ++jt) {
-                    const f32x4 ww = lds_get<f32x4>(up, 4 * (16 * jt + 4 * q));
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        const float cw = __uint_as_float(vf[jt][r]) * ww[r];
-#pragma unroll
-                        for (int mt = 0; mt < MT; ++mt)
-                            M[hb][mt] = mfma_f32(lds_get<float>(sb, TA::at(16 * jt + 4 * q + r, 4 * mt + (l16 >> 2)) + 4 * (l16 & 3)),
-                                                 cw, M[hb][mt]);
-                    }
-                }
-            }
-            if (wave == WAVES - 1 && more) decays(c + 1, hb, dt_next);
         }
-        // ---- the scores, summed over the heads
+        // ---- scores: rows 16 rt + 4 q + r, column 16 out + l16; direction 0: rows j, column i, direction 1: rows i, column j
+        float zA = 0.f, zb = 0.f, dD = 0.f;
 #pragma unroll
         for (int i = 0; i < ROUNDS; ++i) {
-            const int grp = wave + i * WAVES;
-            if (grp >= GROUPS) continue;
+            const int grp = wave + i * WAVES, dir = grp >= Lds::GROUPS;
+            if (grp >= 2 * Lds::GROUPS) continue;
+            int out, tg;
+            Lds::group(dir, grp - dir * Lds::GROUPS, out, tg);
+            const int col = 16 * out + l16;
+            const double dcol = dsum[col];
+            const float dc = del[col];
+            float sum = 0.f, diag = 0.f;
+#pragma unroll
+            for (int hh = 0; hh < TILES; ++hh) {
+                const int rt = TILES * tg + hh, row = 16 * rt + 4 * q;
+                const f32x4 X = dots(dir ? dy : x, dir ? x : dy, rt, out, std::false_type{}, zero4());
+                if (dir == 0) {
+                    const f32x4 dr = lds_get<f32x4>(del, 4 * row), ss = lds_get<f32x4>(lds.ssum[buf], 4 * row);
+                    const float scol = lds.ssum[buf][col];
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        const int j = row + r;
+                        const float d = static_cast<float>(dcol - dsum[j]), e = j <= col ? decay(d) * X[r] : 0.f, y = e * CB[i][hh][r];
+                        const float z = j < col ? y * dr[r] : 0.f;
+                        P[i][hh][r] = __builtin_fmaf(e, dr[r], P[i][hh][r]);
+                        sum += z;
+                        zA = __builtin_fmaf(z, d, zA);
+                        zb = __builtin_fmaf(z, scol - ss[r], zb);
+                        if (j == col) {
+                            diag += y;
+                            dD += X[r];
+                        }
+                    }
+                } else {
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        const int j = row + r;
+                        const float e = j >= col ? decay(static_cast<float>(dsum[j] - dcol)) * X[r] : 0.f;
+                        P[i][hh][r] = __builtin_fmaf(e, dc, P[i][hh][r]);
+                        sum += j > col ? e * CB[i][hh][r] : 0.f;
+                    }
+                }
+            }
+            sum = sum_q(sum);
+            if (q == 0) lds.red[(dir ? Lds::COLS : Lds::ROWS) + tg][col] = sum;
+            if (dir == 0 && out / TILES == tg) {     // the group that holds the tile's own tokens
+                diag = sum_q(diag);
+                if (q == 0) lds.red[Lds::DIAG][col] = diag;
+            }
+        }
+        // ---- the states' parts
+        float thr = 0.f;
+#pragma unroll
+        for (int i = 0; i < NS; ++i)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) thr = __builtin_fmaf(S[i][r], G[i][r], thr);
+        const double all = dsum[CT - 1];
+        auto state_part = [&](f32x4 (&X)[NS], const float* states, const uint8_t* rows, auto back) {
+            constexpr bool BACK = decltype(back)::value;
+            u32x4 hi[BF ? KV : 1], mid[BF ? KV : 1], lo[BF ? KV : 1];
+            f32x4 F[BF ? 1 : NS];
+            if constexpr (BF) {
+#pragma unroll
+                for (int kk = 0; kk < KV; ++kk)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const f32x4& m = X[2 * kk + (e >> 1)];
+                        uint32_t a, b, c;
+                        split3(m[2 * (e & 1)], m[2 * (e & 1) + 1], a, b, c);
+                        hi[kk][e] = a;
+                        mid[kk][e] = b;
+                        lo[kk][e] = c;
+                    }
+            } else {
+#pragma unroll
+                for (int i = 0; i < NS; ++i) F[i] = X[i];
+            }
+            if (more) load_state(X, states, k + 1);
+#pragma unroll
+            for (int it = 0; it < IT; ++it) {
+                f32x4 O = zero4();
+                if constexpr (BF) {
+#pragma unroll
+                    for (int kk = 0; kk < KV; ++kk) {
+                        const u32x4 a = lds_get<u32x4>(rows, chan[kk & 1] + it * TA::ROWS16 + (kk >> 1) * 128);
+                        O = mfma_bf16(lo[kk], a, O);
+                        O = mfma_bf16(mid[kk], a, O);
+                        O = mfma_bf16(hi[kk], a, O);
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < NS; ++i) {
+                        const f32x4 a = lds_get<f32x4>(rows, TA::at(16 * it + l16, 4 * i + q));
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) O = mfma_f32(F[i][r], a[r], O);
+                    }
+                }
+                const double di = dsum[16 * it + l16];
+                O *= decay(static_cast<float>(BACK ? all - di : di));
+                const f32x4 o = own(BACK ? lds.B : lds.C, it);
+                if constexpr (BACK) dB[it] += O * del[16 * it + l16];
+                else dC[it] += O;
+                const float s = sum_q(__builtin_fmaf(o[3], O[3], __builtin_fmaf(o[2], O[2], __builtin_fmaf(o[1], O[1], o[0] * O[0]))));
+                if (q == 0) lds.red[(BACK ? Lds::R : Lds::P) + wave][16 * it + l16] = s;
+            }
+        };
+        state_part(S, L.chunk_states[S_STATE], dy, std::false_type{});
+        state_part(G, L.chunk_states[G_STATE], x, std::true_type{});
+        zA = sum_wave(zA);
+        zb = sum_wave(zb);
+        dD = sum_wave(dD);
+        thr = sum_wave(thr);
+        if (lane == 0) {
+            lds.sums[0][wave] = zA;
+            lds.sums[1][wave] = zb;
+            lds.sums[2][wave] = dD;
+            lds.sums[3][wave] = thr;
+        }
+        if (more && t < CT) put_row(buf ^ 1, next);  // (all have left the last head's)
+        lds_barrier();                               // the sums are there, the rows have been read
+        if (t < n) {
+            float p = 0.f, r = 0.f, rows = 0.f, cols = 0.f;
+#pragma unroll
+            for (int i = 0; i < WAVES; ++i) {
+                p += lds.red[Lds::P + i][t];
+                r += lds.red[Lds::R + i][t];
+            }
+            const int tile = t / 16;
+#pragma unroll
+            for (int tg = 0; tg < TG; ++tg) {
+                if (Lds::near(0, tile, tg)) rows += lds.red[Lds::ROWS + tg][t];
+                if (Lds::near(1, tile, tg)) cols += lds.red[Lds::COLS + tg][t];
+            }
+            const int64_t at = (h0 + k) * L.total + w.lo + t;
+            L.zz[at] = rows - del[t] * cols;
+            L.xz[at] = cols + lds.red[Lds::DIAG][t];
+            L.pp[at] = p;
+            L.xr[at] = r;
+        }
+        if (t >= WAVES * 64 - 4) {
+            const int i = t - (WAVES * 64 - 4);
+            float sum = 0.f;
+#pragma unroll
+            for (int x = 0; x < WAVES; ++x) sum += lds.sums[i][x];
+            if (i == 3) sum = static_cast<float>(sum * exp2(all * A2));
+            (i == 0 ? L.zA : i == 1 ? L.zb : i == 2 ? L.dDp : L.thr)[units + k] = sum;
+        }
+    }
+    // ---- the scores' parts
+#pragma unroll
+    for (int dir = 0; dir < 2; ++dir) {
+        if (dir == 1) lds_barrier();                 // direction 0's scores have been read
+#pragma unroll
+        for (int i = 0; i < ROUNDS; ++i) {
+            const int grp = wave + i * WAVES - dir * Lds::GROUPS;
+            if (grp < 0 || grp >= Lds::GROUPS) continue;
             if constexpr (BF) {
                 u32x4 hi, lo;
 #pragma unroll
@@ -1128,62 +1032,48 @@ __device__ __forceinline__ void shared_pass(const Scan& L, int32_t slot, int32_t
                     hi[2 * hh] = x0; hi[2 * hh + 1] = x1;
                     lo[2 * hh] = y0; lo[2 * hh + 1] = y1;
                 }
-                lds_put(lds.p, grp * 2048 + lane * 16, hi);
-                lds_put(lds.p, grp * 2048 + 1024 + lane * 16, lo);
+                lds_put(lds.xy, grp * 2048 + lane * 16, hi);
+                lds_put(lds.xy, grp * 2048 + 1024 + lane * 16, lo);
             } else {
-                lds_put(lds.p, grp * 1024 + lane * 16, P[i][0]);
+                lds_put(lds.xy, grp * 1024 + lane * 16, P[i][0]);
             }
         }
-        lds_barrier();                               // the scores and the sums are there, c has been read
-        if (c + 1 < n_chunks) load_c(c + 1);
-        if constexpr (BF) {
+        lds_barrier();
+        f32x4(&O)[IT] = dir ? dB : dC;
+        const uint8_t* sm = dir ? lds.C : lds.B;
 #pragma unroll
-            for (int it = 0; it < IT; ++it)
+        for (int tg = 0; tg < TG; ++tg) {
+            u32x4 v;
+            if constexpr (BF) v = tokens(sm, tg);
+            else
 #pragma unroll
-                for (int tg = 0; tg < JG; ++tg) {
-                    if (BACK ? 2 * tg + 1 < it : 2 * tg > it) continue;
-                    const uint32_t at = score_group<BACK>(it, tg) * 2048 + lane * 16;
-                    O[it] = mfma_bf16(vf[tg], lds_get<u32x4>(lds.p, at), O[it]);
-                    O[it] = mfma_bf16(vf[tg], lds_get<u32x4>(lds.p, at + 1024), O[it]);
-                }
-        } else {
+                for (int r = 0; r < 4; ++r) v[r] = lds_get<uint32_t>(sm, TC::at(16 * tg + 4 * q + r, 4 * wave + (l16 >> 2)) + 4 * (l16 & 3));
 #pragma unroll
-            for (int tile = 0; tile < 3; ++tile) {
-                const int it = BACK ? (tile == 1) : (tile > 0), jt = BACK ? (tile > 0) : (tile == 1);
-                const f32x4 X = lds_get<f32x4>(lds.p, tile * 1024 + lane * 16);
+            for (int it = 0; it < IT; ++it) {
+                if (!Lds::near(dir, it, tg)) continue;
+                const uint32_t at = Lds::number(dir, it, tg) * Lds::G_BYTES + lane * 16;
+                if constexpr (BF) {
+                    O[it] = mfma_bf16(v, lds_get<u32x4>(lds.xy, at), O[it]);
+                    O[it] = mfma_bf16(v, lds_get<u32x4>(lds.xy, at + 1024), O[it]);
+                } else {
+                    const f32x4 X = lds_get<f32x4>(lds.xy, at);
 #pragma unroll
-                for (int r = 0; r < 4; ++r) O[it] = mfma_f32(__uint_as_float(vf[jt][r]), X[r], O[it]);
-            }
-        }
-        if constexpr (!BACK) {
-            for (int e = t; e < heads * TOK; e += WAVES * 64) {
-                const int hb = e / TOK, at = e % TOK;
-                // 64 (32) tokens: the second half's z also reach to the first half, and are reached from it
-                float rows = lds.red[hb][WAVES][at], cols = 0.f, p = 0.f;
-                if (at >= TOK / 2) rows += lds.red[hb][WAVES + 1][at];
-                for (int x = at / (TOK / 2) * (IT / 2); x < IT; ++x) cols += lds.red[hb][WAVES + 2 + x][at];
-#pragma unroll
-                for (int x = 0; x < WAVES; ++x) p += lds.red[hb][x][at];
-                if (at < n) {
-                    const int64_t i = (h0 + hb) * L.total + tok0 + at;
-                    L.zz[i] = rows - lds.t.del[buf][hb][at] * cols;
-                    L.xz[i] = cols + lds.red[hb][Lds::RED - 1][at];
-                    L.pp[i] = p;
+                    for (int r = 0; r < 4; ++r) O[it] = mfma_f32(__uint_as_float(v[r]), X[r], O[it]);
                 }
             }
         }
-        // ---- out: lane l16 holds token 16 it + l16, four neighbouring columns
-        if (L.part[ST]) {
+        // ---- out: lane l16 holds token 16 it + l16, four neighbouring channels
+        if (L.part[dir]) {
             const uint32_t orow = static_cast<uint32_t>(L.G) * DK * 4;
-            const __amdgpu_buffer_rsrc_t ro = make_rsrc_u(L.part[ST] + ((blk * L.total + tok0) * L.G + g) * DK, (n - 1) * orow + DK * 4);
+            const __amdgpu_buffer_rsrc_t ro = make_rsrc_u(L.part[dir] + ((blk * L.total + w.lo) * L.G + g) * DK, (n - 1) * orow + DK * 4);
 #pragma unroll
             for (int it = 0; it < IT; ++it)
                 __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, O[it]), ro,
                                                        (16 * it + l16) * orow + (16 * wave + 4 * q) * 4, 0, 0);
         } else {
-            const Out& out = L.out[ST];
+            const Out& out = L.out[dir];
             const uint32_t orow = static_cast<uint32_t>(out.ld);
-            const __amdgpu_buffer_rsrc_t ro = make_rsrc_u(out.p + tok0 * out.ld + g * TC::RB, (n - 1) * orow + TC::RB);
+            const __amdgpu_buffer_rsrc_t ro = make_rsrc_u(out.p + w.lo * out.ld + g * TC::RB, (n - 1) * orow + TC::RB);
 #pragma unroll
             for (int it = 0; it < IT; ++it) {
                 const uint32_t at = (16 * it + l16) * orow + (16 * wave + 4 * q) * ES;
@@ -1193,101 +1083,75 @@ __device__ __forceinline__ void shared_pass(const Scan& L, int32_t slot, int32_t
             }
         }
     }
-    if constexpr (!BACK) {
-        lds_barrier();                               // the last chunk's sums have been read
-#pragma unroll
-        for (int hb = 0; hb < HB; ++hb) {
-#pragma unroll
-            for (int off = 1; off < 64; off <<= 1) {
-                zA[hb] += __shfl_xor(zA[hb], off, 64);
-                zb[hb] += __shfl_xor(zb[hb], off, 64);
-            }
-            if (lane == 0) {
-                lds.red[hb][0][wave] = zA[hb];
-                lds.red[hb][1][wave] = zb[hb];
-            }
-        }
-        lds_barrier();
-        if (t < 2 * heads) {
-            float sum = 0.f;
-            for (int x = 0; x < WAVES; ++x) sum += lds.red[t >> 1][t & 1][x];
-            (t & 1 ? L.zb : L.zA)[static_cast<int64_t>(slot) * L.H + h0 + (t >> 1)] = sum;
-        }
-    }
 }
 
-template <int DT, int DK, int DV, int HB>
-__global__ void __launch_bounds__(DK * 4, DK == 128 ? 2 : 1) shared_kernel(Scan L) {
-    __shared__ union {
-        SharedLds<DT, DK, DV, HB, false> c;
-        SharedLds<DT, DK, DV, HB, true> b;
-    } lds;
+template <int DT, int DK, int DV>
+__global__ void __launch_bounds__(DK * 4, DK / 64) grad_kernel(Scan L) {
+    __shared__ GradLds<DT, DK, DV> lds;
     uint32_t unit;
     int32_t pass;
     const uint32_t blocks = static_cast<uint32_t>(L.blocks) * L.G;
-    if (!unit_of(L.slots * blocks, 2, unit, pass)) return;
-    if (pass == 0) shared_pass<DT, DK, DV, HB, false>(L, unit / blocks, unit % blocks, lds.c);
-    else shared_pass<DT, DK, DV, HB, true>(L, unit / blocks, unit % blocks, lds.b);
+    if (!unit_of(L.slots * blocks, 1, unit, pass)) return;
+    grad_pass<DT, DK, DV>(L, unit / blocks, unit % blocks, lds);
 }
 
-// ---------------------------------------------------------------- ddt, dA, dbias; sums over blocks and segments
+// ---------------------------------------------------------------- ddt, dA, dbias; sums over blocks and chunks
 
-// One wave per (segment, head): from its last chunk to its first, lane l has the token l before the chunk's last.
-template <int DT>
+// One wave per (chunk, head), lane l with the tokens l and 64 + l.
+template <int DT, int CT>
 __global__ void __launch_bounds__(256) decay_grad_kernel(Scan L) {
+    constexpr int NB = (CT + 63) / 64;
     const int64_t u = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6);
     const int lane = threadIdx.x & 63;
-    if (u >= static_cast<int64_t>(L.slots) * L.H) return;
+    if (u >= static_cast<int64_t>(L.c_slots) * L.H) return;
     const int32_t slot = static_cast<int32_t>(u / L.H), h = static_cast<int32_t>(u % L.H);
     Where w;
-    if (!locate(L, slot, w) || w.hi == w.lo) {       // no such segment, or an empty one: nothing to add up
+    if (!locate(L, slot, w) || w.hi == w.lo) {       // no such chunk, or an empty one: nothing to add up
         if (lane == 0) L.dAp[u] = L.dbp[u] = L.dDp[u] = 0.f;
         return;
     }
-    const double A = static_cast<double>(L.A[h]);
+    const double A = static_cast<double>(L.A[h]), thr = static_cast<double>(L.thr[u]);
     const float bias = L.bias ? L.bias[h] : 0.f;
-    double end = static_cast<double>(L.E[u]);        // <G, S> behind the tokens in hand
-    double dA = 0.0, db = 0.0, own = 0.0;            // a lane's part of sum delta dg, sum slope dg, sum slope x . u
-    const int64_t row = h * L.total;
-    constexpr int TOK = DT == KDA_BF16 ? 64 : 32;
-    for (int64_t lo = w.lo + (w.hi - w.lo - 1) / TOK * TOK; lo >= w.lo; lo -= TOK) {
-        const int64_t hi = lo + TOK < w.hi ? lo + TOK : w.hi, tok = hi - 1 - lane;
-        const bool in = tok >= lo;
-        double x = 0.0, z = 0.0, p = 0.0, r = 0.0;
-        Strength s = {0.f, 0.f};
-        if (in) {
-            s = strength(load_as_f32<DT>(L.dt.p + tok * L.dt.ld, h), bias);
-            const float later = L.xr[row + tok];
-            x = static_cast<double>(L.xz[row + tok]) + later;
-            z = static_cast<double>(L.zz[row + tok]);
-            p = static_cast<double>(L.pp[row + tok]);
-            r = static_cast<double>(s.delta) * later;
+    const int n = static_cast<int>(w.hi - w.lo);
+    const int64_t row = h * L.total + w.lo;
+    double x[NB], zp[NB], p[NB], r[NB], slope[NB], zs[NB], rs[NB], ds[NB], ss[NB];
+    double z_all = 0.0, r_all = 0.0;
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+        const int i = 64 * b + lane;
+        x[b] = zp[b] = p[b] = r[b] = slope[b] = ds[b] = ss[b] = 0.0;
+        if (i < n) {
+            const Strength s = strength(load_as_f32<DT>(L.dt.p + (w.lo + i) * L.dt.ld, h), bias);
+            const float later = L.xr[row + i];
+            x[b] = static_cast<double>(L.xz[row + i]) + later;
+            p[b] = static_cast<double>(L.pp[row + i]);
+            zp[b] = static_cast<double>(L.zz[row + i]) + p[b];
+            r[b] = static_cast<double>(s.delta) * later;
+            slope[b] = static_cast<double>(s.slope);
+            ds[b] = L.t_dsum[u * CT + i];
+            ss[b] = static_cast<double>(L.t_ssum[u * CT + i]);
         }
-        const double delta = static_cast<double>(s.delta), slope = static_cast<double>(s.slope);
-        // sums over the tokens from a lane's own to the last
-        const double zs = prefix_sum(z + p), ps = prefix_sum(p), rs = prefix_sum(r), ds = prefix_sum(delta), ss = prefix_sum(slope);
-        const double r_all = lane_value(rs, 63), d_all = lane_value(ds, 63), s_all = lane_value(ss, 63);
-        // Where a chunk or a token decays by more than e^-14, what goes through it is below the difference's rounding
-        // (about 2^-20 of <G, S>, which W would multiply): it is taken as zero, and the sums start anew before it.
-        const double through = d_all * A < -14.0 ? 0.0 : end - r_all;
-        const uint64_t cuts = __ballot(in && delta * A < -14.0), seen = cuts & (~uint64_t(0) >> (63 - lane));
-        const int cut = seen ? 63 - __builtin_clzll(seen) : -1;
-        const double from = shuffle(zs - rs, cut < 0 ? 0 : cut);
-        const double g = cut == lane ? 0.0 : (zs - rs) + (cut < 0 ? through + r_all : -from);
-        end = through + lane_value(ps, 63);
-        if (in) store_from_f32<DT>(L.ddt.p + tok * L.ddt.ld, h, static_cast<float>((x + A * g) * slope));
-        // W_i = all - (from i on) + w_i, W_n - W_j = (from j on) - w_j
-        dA += p * (d_all - ds + delta) + r * (ds - delta);
-        db += p * (s_all - ss + slope) + r * (ss - slope);
-        own += slope * x;
-        if (lane == 0) {
-            dA += through * d_all;
-            db += through * s_all;
+        zs[b] = z_all + prefix_sum(zp[b]);
+        rs[b] = r_all + prefix_sum(r[b]);
+        z_all = lane_value(zs[b], 63);
+        r_all = lane_value(rs[b], 63);
+    }
+    const double d_all = L.t_dsum[u * CT + CT - 1], s_all = static_cast<double>(L.t_ssum[u * CT + CT - 1]);
+    double dA = 0.0, db = 0.0, own = 0.0;            // a lane's part of sum delta dg, sum slope dg, sum slope x . u
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+        const int i = 64 * b + lane;
+        const double dg = thr + (z_all - zs[b] + zp[b]) + (rs[b] - r[b]);
+        if (i < n) {
+            store_from_f32<DT>(L.ddt.p + (w.lo + i) * L.ddt.ld, h, static_cast<float>((x[b] + A * dg) * slope[b]));
+            dA += p[b] * ds[b] + r[b] * (d_all - ds[b]);
+            db += p[b] * ss[b] + r[b] * (s_all - ss[b]);
+            own += slope[b] * x[b];
         }
     }
     if (lane == 0) {
-        dA += static_cast<double>(L.zA[u]);
-        db += static_cast<double>(L.zb[u]);
+        dA += static_cast<double>(L.zA[u]) + thr * d_all;
+        db += static_cast<double>(L.zb[u]) + thr * s_all;
     }
     db = own + A * db;
 #pragma unroll
@@ -1318,12 +1182,12 @@ __global__ void __launch_bounds__(256) part_sum_kernel(Scan L, int32_t row, int6
     store4_from_f32<DT>(out.p + tok * out.ld, e % row, make_float4(s[0], s[1], s[2], s[3]));
 }
 
-// dA, dbias and dD of head blockIdx.x: sums over the segments.
+// dA, dbias and dD of head blockIdx.x: sums over the chunks.
 __global__ void __launch_bounds__(256) head_sum_kernel(Scan L) {
     __shared__ double red[3][4];
     const int32_t h = blockIdx.x;
     double s[3] = {};
-    for (int32_t i = threadIdx.x; i < L.slots; i += 256) {
+    for (int32_t i = threadIdx.x; i < L.c_slots; i += 256) {
         const int64_t u = static_cast<int64_t>(i) * L.H + h;
         s[0] += L.dAp[u];
         s[1] += L.dbp[u];
@@ -1347,20 +1211,43 @@ __global__ void __launch_bounds__(256) head_sum_kernel(Scan L) {
 
 int32_t head_blocks(int32_t H, int32_t G, int HB) { return (H / G + HB - 1) / HB; }
 int value_heads(int32_t H, int32_t G, int32_t dv) { return dv == 64 && H / G > 1 ? 2 : 1; }
-int shared_heads(int32_t H, int32_t G, int32_t dv) {
-    const int32_t rep = H / G;
-    return rep == 1 ? 1 : (rep == 2 || dv == 128 ? 2 : 4);
+
+template <int V>
+using Int = std::integral_constant<int, V>;
+template <typename F>
+auto by_sizes(int32_t dk, int32_t dv, F go) {
+    if (dk == 128) return dv == 128 ? go(Int<128>{}, Int<128>{}) : go(Int<128>{}, Int<64>{});
+    return dv == 128 ? go(Int<64>{}, Int<128>{}) : go(Int<64>{}, Int<64>{});
+}
+int32_t chunk_tokens(int32_t in_dtype, int32_t dk, int32_t dv) {
+    return by_sizes(dk, dv, [&](auto k, auto v) {
+        constexpr int DK = decltype(k)::value, DV = decltype(v)::value;
+        return in_dtype == KDA_BF16 ? grad_tokens<KDA_BF16, DK, DV>() : grad_tokens<KDA_F32, DK, DV>();
+    });
 }
 
-// Tokens per segment, a multiple of 64.
-int32_t forward_segment(int32_t n_seqs, int64_t total, int32_t blocks, int32_t in_dtype, bool packed) {
-    const int64_t units = int64_t(n_seqs) * blocks, longest = packed ? total : total / n_seqs;
+// Tokens per segment, a multiple of 128, for `units` (sequence, head block) pairs.
+int32_t forward_segment(int64_t units, int32_t n_seqs, int64_t total, int32_t in_dtype, bool packed) {
+    const int64_t longest = packed ? total : total / n_seqs, blocks = units / n_seqs;
     if (units >= 256 || longest < 1024) return WHOLE;
     const int64_t shares = packed ? std::max<int64_t>(1, 512 / blocks - n_seqs / 2) : 512 / units;
-    const int64_t seg = std::max<int64_t>(((longest + shares - 1) / shares + 63) / 64 * 64, in_dtype == KDA_BF16 ? 256 : 128);
+    const int64_t seg = std::max<int64_t>(((longest + shares - 1) / shares + 127) / 128 * 128, in_dtype == KDA_BF16 ? 256 : 128);
     return seg >= longest || seg >= WHOLE ? WHOLE : static_cast<int32_t>(seg);
 }
-int32_t backward_segment(int32_t, int64_t, int32_t, int32_t, bool) { return 512; }
+int32_t state_segment(int64_t units, int32_t n_seqs, int64_t total, int32_t in_dtype, bool packed) {
+    const int64_t longest = packed ? total : total / n_seqs, blocks = units / n_seqs;
+    if (units >= 64 || longest < 1024) return WHOLE;
+    const int64_t shares = packed ? std::max<int64_t>(1, 256 / blocks - n_seqs / 2) : 256 / units;
+    const int64_t seg = std::max<int64_t>(((longest + shares - 1) / shares + 127) / 128 * 128, 512);
+    return seg >= longest || seg >= WHOLE ? WHOLE : static_cast<int32_t>(seg);
+}
+// dx starts from the states of a chunk, so its segments cost a state's read only.
+int32_t dx_segment(int64_t units, int32_t n_seqs, int64_t total, int32_t in_dtype, bool packed) {
+    const int64_t longest = packed ? total : total / n_seqs, blocks = units / n_seqs;
+    const int64_t shares = packed ? std::max<int64_t>(1, 1024 / blocks) : std::max<int64_t>(1, 1024 / units);
+    const int64_t seg = std::max<int64_t>(((longest + shares - 1) / shares + 127) / 128 * 128, 256);
+    return seg >= longest || seg >= WHOLE ? WHOLE : static_cast<int32_t>(seg);
+}
 
 int64_t segment_slots(int32_t n_seqs, int64_t total, int32_t seg, bool packed) {
     if (packed) return total / seg + n_seqs;
@@ -1379,30 +1266,40 @@ struct Carver {
     }
 };
 
-void carve_forward(Scan& L, Carver& ws, int64_t elems) {
-    if (L.seg == WHOLE) return;
-    L.seg_states[S_STATE] = ws.take<float>(int64_t(L.slots) * L.H * elems);
-    L.seg_log[S_STATE] = ws.take<double>(int64_t(L.slots) * L.H);
-}
-void carve_backward(Scan& L, Carver& ws, int64_t elems, int32_t dk, bool last) {
-    const int64_t su = int64_t(L.slots) * L.H;
-    for (int st : {S_STATE, G_STATE}) {
-        L.seg_states[st] = ws.take<float>(su * elems);
-        L.seg_log[st] = ws.take<double>(su);
-    }
-    float* S_last = ws.take<float>(int64_t(L.n_seqs) * L.H * elems);
-    L.S_last = last ? S_last : nullptr;
-    if (L.blocks > 1)
-        for (int st : {S_STATE, G_STATE}) L.part[st] = ws.take<float>(L.total * L.G * dk * L.blocks);
-    for (float** p : {&L.zz, &L.pp, &L.xz, &L.xr}) *p = ws.take<float>(L.H * L.total);
-    for (float** p : {&L.zA, &L.zb, &L.E, &L.dDp, &L.dAp, &L.dbp}) *p = ws.take<float>(su);
-}
-
-void set_segments(Scan& L, bool backward, int32_t dv, int32_t in_dtype, bool packed) {
-    const int32_t vb = head_blocks(L.H, L.G, value_heads(L.H, L.G, dv)) * L.G;
-    L.seg = (backward ? backward_segment : forward_segment)(L.n_seqs, L.total, vb, in_dtype, packed);
+void set_segments(Scan& L, int32_t (*rule)(int64_t, int32_t, int64_t, int32_t, bool), int32_t dv, int32_t in_dtype, bool packed) {
+    const int64_t units = int64_t(L.n_seqs) * head_blocks(L.H, L.G, value_heads(L.H, L.G, dv)) * L.G;
+    L.seg = rule(units, L.n_seqs, L.total, in_dtype, packed);
     L.slots = static_cast<int32_t>(segment_slots(L.n_seqs, L.total, L.seg, packed));
     L.n_seg = L.slots / L.n_seqs;
+}
+// Chunks of the gradients and blocks of heads: as few as leave every CU a workgroup.
+void set_chunks(Scan& L, int32_t dk, int32_t dv, int32_t in_dtype, bool packed) {
+    L.ct = chunk_tokens(in_dtype, dk, dv);
+    L.c_slots = static_cast<int32_t>(segment_slots(L.n_seqs, L.total, L.ct, packed));
+    L.c_per_seq = L.c_slots / L.n_seqs;
+    L.heads = L.H / L.G;
+    while (L.heads > 1 && int64_t(L.c_slots) * L.G * head_blocks(L.H, L.G, L.heads) < 256) L.heads = (L.heads + 1) / 2;
+    L.blocks = head_blocks(L.H, L.G, L.heads);
+}
+
+void carve_segments(Scan& L, Carver& ws, int64_t elems, int passes) {
+    if (L.seg == WHOLE) return;
+    for (int st = 0; st < passes; ++st) {
+        L.seg_states[st] = ws.take<float>(int64_t(L.slots) * L.H * elems);
+        L.seg_log[st] = ws.take<double>(int64_t(L.slots) * L.H);
+    }
+}
+void carve_forward(Scan& L, Carver& ws, int64_t elems) { carve_segments(L, ws, elems, 1); }
+void carve_backward(Scan& L, Carver& ws, int32_t dk, int32_t dv) {
+    const int64_t cu = int64_t(L.c_slots) * L.H;
+    carve_segments(L, ws, int64_t(dk) * dv, 2);
+    for (float*& p : L.chunk_states) p = ws.take<float>(cu * dk * dv);
+    if (L.blocks > 1)
+        for (float*& p : L.part) p = ws.take<float>(L.total * L.G * dk * L.blocks);
+    L.t_dsum = ws.take<double>(cu * L.ct);
+    for (float** p : {&L.t_del, &L.t_ssum}) *p = ws.take<float>(cu * L.ct);
+    for (float** p : {&L.zz, &L.pp, &L.xz, &L.xr}) *p = ws.take<float>(L.H * L.total);
+    for (float** p : {&L.zA, &L.zb, &L.dDp, &L.thr, &L.dAp, &L.dbp}) *p = ws.take<float>(cu);
 }
 
 Scan base(const ScanArgs& a) {
@@ -1416,13 +1313,6 @@ Scan base(const ScanArgs& a) {
     return L;
 }
 
-template <int V>
-using Int = std::integral_constant<int, V>;
-template <typename F>
-hipError_t by_sizes(int32_t dk, int32_t dv, F go) {
-    if (dk == 128) return dv == 128 ? go(Int<128>{}, Int<128>{}) : go(Int<128>{}, Int<64>{});
-    return dv == 128 ? go(Int<64>{}, Int<128>{}) : go(Int<64>{}, Int<64>{});
-}
 unsigned xcd_grid(int64_t units, int32_t passes) { return static_cast<unsigned>((units + 7) / 8 * 8 * passes); }
 
 template <int DT, int ODT, int MODE>
@@ -1441,38 +1331,43 @@ hipError_t launch_value(Scan L, int32_t dk, int32_t dv, hipStream_t stream) {
         return go(Int<1>{});
     });
 }
-template <int DT>
-hipError_t launch_states(Scan L, int32_t dk, int32_t dv, int32_t first, int32_t passes, hipStream_t stream) {
-    const hipError_t e = by_sizes(dk, dv, [&](auto k, auto v) {
+template <int DT, bool CHUNKS>
+hipError_t launch_states(Scan L, int32_t dk, int32_t dv, int32_t passes, hipStream_t stream) {
+    return by_sizes(dk, dv, [&](auto k, auto v) {
         constexpr int DK = decltype(k)::value, DV = decltype(v)::value;
         auto go = [&](auto heads) {
             constexpr int HB = decltype(heads)::value;
             L.blocks = head_blocks(L.H, L.G, HB);
-            hipLaunchKernelGGL((state_kernel<DT, DK, DV, HB>), dim3(xcd_grid(int64_t(L.slots) * L.blocks * L.G, passes)),
-                               dim3(HB * DV * 4), 0, stream, L, first, passes);
+            hipLaunchKernelGGL((state_kernel<DT, DK, DV, HB, CHUNKS>), dim3(xcd_grid(int64_t(L.slots) * L.blocks * L.G, passes)),
+                               dim3(HB * DV * 4), 0, stream, L, passes);
             return hipGetLastError();
         };
         if constexpr (DV == 64)
             if (value_heads(L.H, L.G, dv) == 2) return go(Int<2>{});
         return go(Int<1>{});
     });
+}
+// The states that the segments start from (S), or that follow them (G).
+template <int DT>
+hipError_t launch_segments(const Scan& L, int32_t dk, int32_t dv, int32_t passes, hipStream_t stream) {
+    const hipError_t e = launch_states<DT, false>(L, dk, dv, passes, stream);
     if (e != hipSuccess) return e;
     hipLaunchKernelGGL(scan_kernel, dim3(static_cast<unsigned>(L.n_seqs * L.H), static_cast<unsigned>(dk * dv / 1024), passes),
-                       dim3(256), 0, stream, L, dk * dv, first);
+                       dim3(256), 0, stream, L, dk * dv);
     return hipGetLastError();
 }
 
 template <int DT, int ODT>
 hipError_t forward(const ScanArgs& a, hipStream_t stream) {
     Scan L = base(a);
-    set_segments(L, false, a.dv, a.in_dtype, a.cu != nullptr);
+    set_segments(L, forward_segment, a.dv, a.in_dtype, a.cu != nullptr);
     Carver ws{static_cast<uint8_t*>(a.workspace)};
     carve_forward(L, ws, int64_t(a.dk) * a.dv);
     L.m_out[S_STATE] = a.hT;
     L.exact[S_STATE] = a.hT != nullptr;
     L.out[0] = Out{static_cast<uint8_t*>(a.y.p), a.y.ld * (ODT == KDA_BF16 ? 2 : 4)};
     if (L.seg < WHOLE) {
-        const hipError_t e = launch_states<DT>(L, a.dk, a.dv, S_STATE, 1, stream);
+        const hipError_t e = launch_segments<DT>(L, a.dk, a.dv, 1, stream);
         if (e != hipSuccess) return e;
     }
     return launch_value<DT, ODT, Y>(L, a.dk, a.dv, stream);
@@ -1482,33 +1377,44 @@ template <int DT>
 hipError_t backward(const ScanArgs& a, hipStream_t stream) {
     const int64_t es = DT == KDA_BF16 ? 2 : 4;
     auto out = [&](const RowsOut& r) { return Out{static_cast<uint8_t*>(r.p), r.ld * es}; };
+    const bool packed = a.cu != nullptr;
     Scan L = base(a);
-    set_segments(L, true, a.dv, a.in_dtype, a.cu != nullptr);
-    const int HB = shared_heads(a.H, a.G, a.dv);
-    L.blocks = head_blocks(a.H, a.G, HB);
+    set_chunks(L, a.dk, a.dv, a.in_dtype, packed);
+    set_segments(L, state_segment, a.dv, a.in_dtype, packed);
     Carver ws{static_cast<uint8_t*>(a.workspace)};
-    carve_backward(L, ws, int64_t(a.dk) * a.dv, a.dk, a.dhT != nullptr);
+    carve_backward(L, ws, a.dk, a.dv);
     L.m_out[G_STATE] = a.dh0;
     L.exact[S_STATE] = L.exact[G_STATE] = 1;
     L.ddt = out(a.ddt);
     L.dA = a.dA; L.dD = a.dD; L.dbias = a.dbias;
+    // the states of every chunk
     hipError_t e = hipSuccess;
-    // one segment a sequence and no gradient behind it: all states are known
-    if (L.cu || L.n_seg > 1 || L.S_last) e = launch_states<DT>(L, a.dk, a.dv, S_STATE, 2, stream);
+    if (L.seg < WHOLE) e = launch_segments<DT>(L, a.dk, a.dv, 2, stream);
+    if (e == hipSuccess) e = launch_states<DT, true>(L, a.dk, a.dv, 2, stream);
     if (e != hipSuccess) return e;
+    // dx from them, in segments of its own
+    Scan X = L;
+    set_segments(X, dx_segment, a.dv, a.in_dtype, packed);
+    X.out[0] = out(a.dx);
+    e = launch_value<DT, DT, DX>(X, a.dk, a.dv, stream);
+    if (e != hipSuccess) return e;
+    // the other gradients, chunk by chunk
+    L.seg = L.ct;
+    L.slots = L.c_slots;
+    L.n_seg = L.c_per_seq;
     L.out[S_STATE] = out(a.dC);
     L.out[G_STATE] = out(a.dB);
+    const unsigned waves = static_cast<unsigned>((int64_t(L.c_slots) * L.H + 3) / 4);
     e = by_sizes(a.dk, a.dv, [&](auto k, auto v) {
-        constexpr int DK = decltype(k)::value, DV = decltype(v)::value;
-        auto go = [&](auto heads) {
-            hipLaunchKernelGGL((shared_kernel<DT, DK, DV, decltype(heads)::value>),
-                               dim3(xcd_grid(int64_t(L.slots) * L.blocks * L.G, 2)), dim3(DK * 4), 0, stream, L);
-            return hipGetLastError();
-        };
-        if (HB == 1) return go(Int<1>{});
-        if constexpr (DV == 64)
-            if (HB == 4) return go(Int<4>{});
-        return go(Int<2>{});
+        constexpr int DK = decltype(k)::value, DV = decltype(v)::value, CT = grad_tokens<DT, DK, DV>();
+        hipLaunchKernelGGL((table_kernel<DT, CT>), dim3(waves), dim3(256), 0, stream, L);
+        hipError_t r = hipGetLastError();
+        if (r != hipSuccess) return r;
+        hipLaunchKernelGGL((grad_kernel<DT, DK, DV>), dim3(xcd_grid(int64_t(L.slots) * L.blocks * L.G, 1)), dim3(DK * 4), 0, stream, L);
+        r = hipGetLastError();
+        if (r != hipSuccess) return r;
+        hipLaunchKernelGGL((decay_grad_kernel<DT, CT>), dim3(waves), dim3(256), 0, stream, L);
+        return hipGetLastError();
     });
     if (e != hipSuccess) return e;
     if (L.blocks > 1 && L.total > 0) {
@@ -1518,12 +1424,6 @@ hipError_t backward(const ScanArgs& a, hipStream_t stream) {
         e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
-    L.out[0] = out(a.dx);
-    e = launch_value<DT, DT, DX>(L, a.dk, a.dv, stream);
-    if (e != hipSuccess) return e;
-    hipLaunchKernelGGL(decay_grad_kernel<DT>, dim3(static_cast<unsigned>((int64_t(L.slots) * L.H + 3) / 4)), dim3(256), 0, stream, L);
-    e = hipGetLastError();
-    if (e != hipSuccess) return e;
     hipLaunchKernelGGL(head_sum_kernel, dim3(L.H), dim3(256), 0, stream, L);
     return hipGetLastError();
 }
@@ -1537,12 +1437,13 @@ size_t scan_workspace_bytes(int32_t n_seqs, int64_t total, int32_t H, int32_t G,
     for (const bool packed : {false, true}) {
         Scan L{};
         L.n_seqs = n_seqs; L.total = total; L.H = H; L.G = G;
-        set_segments(L, backward, dv, in_dtype, packed);
         Carver ws{nullptr};
         if (backward) {
-            L.blocks = head_blocks(H, G, shared_heads(H, G, dv));
-            carve_backward(L, ws, int64_t(dk) * dv, dk, true);
+            set_chunks(L, dk, dv, in_dtype, packed);
+            set_segments(L, state_segment, dv, in_dtype, packed);
+            carve_backward(L, ws, dk, dv);
         } else {
+            set_segments(L, forward_segment, dv, in_dtype, packed);
             carve_forward(L, ws, int64_t(dk) * dv);
         }
         most = std::max(most, ws.used);
