@@ -127,11 +127,18 @@ __device__ __forceinline__ float pow2(double x) { return __builtin_amdgcn_exp2f(
 // a SiLU), adds up: with the signs, dA of 4096 tokens was off by 6e-6 of itself, the same way in every head.
 __device__ __forceinline__ float chunk_sign(int k) { return k & 1 ? -1.f : 1.f; }
 
+// A chunk's dt of one head, one token a lane, as it comes: to be opened where it is used, a chunk later.
 template <int DT>
-__device__ __forceinline__ float load_dt(const Scan& L, int64_t tok0, int n, int32_t h, int lane) {
-    if (lane >= n) return 0.f;
-    return load_as_f32<DT>(L.dt.p + (tok0 + lane) * L.dt.ld, h);
+__device__ __forceinline__ uint32_t load_dt(const Scan& L, int64_t tok0, int n, int32_t h, int lane) {
+    constexpr uint32_t ES = DT == KDA_BF16 ? 2 : 4;
+    const uint32_t ld = static_cast<uint32_t>(L.dt.ld);
+    const __amdgpu_buffer_rsrc_t r = make_rsrc_u(L.dt.p + tok0 * L.dt.ld + h * ES, (n - 1) * ld + ES);
+    if constexpr (DT == KDA_BF16) return __builtin_amdgcn_raw_buffer_load_b16(r, lane * ld, 0, 0);
+    else return __builtin_amdgcn_raw_buffer_load_b32(r, lane * ld, 0, 0);
 }
+template <int DT>
+__device__ __forceinline__ float open_dt(uint32_t x) { return __uint_as_float(DT == KDA_BF16 ? x << 16 : x); }
+
 // What a lane's four scores of a tile (tokens i = 16 it + l16, j = 16 jt + 4 q + r) are multiplied by: the decay from the
 // earlier of the two to the later, 0 where j lies on the wrong side; forward: times delta_j.
 template <bool BACK>
@@ -170,8 +177,10 @@ struct ValueLds {
     using TA = Tile<DK, ES>;
     using TC = Tile<DV, ES>;
     static constexpr int C_BYTES = TOK / TC::R * TC::PIECE, P_BYTES = (ES == 2 ? 12 : 3) * 1024;
-    __align__(16) uint8_t b[TOK / TA::R * TA::PIECE];
-    __align__(16) uint8_t c[HB * C_BYTES];
+    // STATE: this chunk's rows and the next one's
+    static constexpr int B_BYTES = TOK / TA::R * TA::PIECE, BUFS = STATE ? 2 : 1;
+    __align__(16) uint8_t b[BUFS * B_BYTES];
+    __align__(16) uint8_t c[BUFS * HB * C_BYTES];
     __align__(16) uint8_t a[STATE ? 16 : TOK / TA::R * TA::PIECE];
     __align__(16) uint8_t p[STATE ? 16 : HB * P_BYTES];              // scores per head
     __align__(16) double cum[2][HB][TOK];
@@ -221,13 +230,13 @@ __device__ __forceinline__ void value_pass(const Scan& L, int32_t slot, int32_t 
     };
     auto load_b = [&](int c) {
         const int64_t off = chunk_at(c);
-        fetch_rows<TA, TOK, WAVES>(lds.b, rb.p + (w.lo + off) * rb.ld + g * TA::RB, static_cast<uint32_t>(rb.ld), chunk_n(off), wave, lane);
+        fetch_rows<TA, TOK, WAVES>(lds.b + (STATE ? c & 1 : 0) * Lds::B_BYTES, rb.p + (w.lo + off) * rb.ld + g * TA::RB, static_cast<uint32_t>(rb.ld), chunk_n(off), wave, lane);
     };
     auto load_c = [&](int c) {
         const int64_t off = chunk_at(c);
 #pragma unroll
         for (int i = 0; i < HB; ++i)
-            fetch_rows<TC, TOK, WAVES>(lds.c + i * Lds::C_BYTES, rc.p + (w.lo + off) * rc.ld + (h0 + i) * TC::RB,
+            fetch_rows<TC, TOK, WAVES>(lds.c + ((STATE ? c & 1 : 0) * HB + i) * Lds::C_BYTES, rc.p + (w.lo + off) * rc.ld + (h0 + i) * TC::RB,
                                        static_cast<uint32_t>(rc.ld), h0 + i < h_end ? chunk_n(off) : 0, wave, lane);
     };
     // the wave that makes a head's decays
@@ -239,9 +248,9 @@ __device__ __forceinline__ void value_pass(const Scan& L, int32_t slot, int32_t 
         return load_dt<DT>(L, w.lo + off, chunk_n(off), th, lane);
     };
     double log_sum = 0.0;
-    auto decays = [&](int c, float dt) {
+    auto decays = [&](int c, uint32_t dt) {
         const int buf = c & 1, n = chunk_n(chunk_at(c));
-        const float delta = lane < n ? strength(dt, bias).delta : 0.f;
+        const float delta = lane < n ? strength(open_dt<DT>(dt), bias).delta : 0.f;
         const double cum = prefix_sum(static_cast<double>(delta) * (static_cast<double>(A) * LOG2E));
         const double all = lane_value(cum, TOK - 1), over = -exp2(all);
         const float hi = static_cast<float>(over);
@@ -260,38 +269,73 @@ __device__ __forceinline__ void value_pass(const Scan& L, int32_t slot, int32_t 
         load_c(0);
         if (table >= 0) decays(0, dt_of(0));
     }
+    uint32_t dt_ahead = table >= 0 && n_chunks > 1 ? dt_of(1) : 0u;    // a chunk ahead of its use: it is there by then
 
-    // ---- the state: tile mt, register r of lane (l16, q) holds row row(mt) + r, column 16 wc + l16
+    // ---- the state, tile mt of 16 rows.  Y and DX: register r of lane (l16, q) holds row row(mt) + r, column 16 wc + l16;
+    // STATE: row 16 mt + l16, column 16 wc + 4 q + r, so that a lane's four lie side by side.  The states of the chunks
+    // are kept as those tiles, 1 KB each.
     auto row = [&](int mt) { return BF ? 32 * (mt >> 1) + 8 * q + 4 * (mt & 1) : 16 * mt + 4 * q; };
     const int col = 16 * wc + l16;
     f32x4 M[MT];
-    auto load_state = [&](const float* src) {        // nullptr: an empty range, which reads as zeros
+    auto state_at = [&](bool tiles) {                // of tile 0; tile mt stands 64 DV mt bytes behind it
+        uint32_t at = tiles ? (wc * 64 + lane) * 16 : (l16 * DV + 16 * wc + 4 * q) * 4;
+        asm volatile("" : "+v"(at));                 // formed anew, not kept over the loop
+        return at;
+    };
+    auto store_state = [&](float* dst, float sign, bool tiles) {
+        const __amdgpu_buffer_rsrc_t rs = make_rsrc_u(dst, DK * DV * 4);
+        if constexpr (STATE) {
+            const uint32_t at = state_at(tiles);
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+                __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, sign * M[mt]), rs, at + 64 * DV * mt, 0, 0);
+        } else {
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(sign * M[mt][r]), rs, ((row(mt) + r) * DV + col) * 4, 0, 0);
+        }
+    };
+    auto load_state = [&](const float* src, bool tiles) {          // nullptr: an empty range, which reads as zeros
         const __amdgpu_buffer_rsrc_t rs = make_rsrc_u(src, src ? DK * DV * 4 : 0);
+        if constexpr (STATE) {
+            const uint32_t at = state_at(tiles);
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
+            for (int mt = 0; mt < MT; ++mt)
+                M[mt] = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(rs, at + 64 * DV * mt, 0, 0));
+        } else {
 #pragma unroll
-            for (int r = 0; r < 4; ++r)
-                M[mt][r] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rs, ((row(mt) + r) * DV + col) * 4, 0, 0));
+            for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const int k = row(mt) + r;
+                    const uint32_t at = tiles ? k / 16 * (DV * 64) + wc * 1024 + (l16 >> 2) * 256 + k % 16 * 16 + (l16 & 3) * 4
+                                              : (k * DV + col) * 4;
+                    M[mt][r] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rs, at, 0, 0));
+                }
+        }
     };
     // a chunk's place among the states of all chunks: of the one that token w.lo + off belongs to
     auto chunk_unit = [&](int64_t off) {
         const int64_t first = w.lo - static_cast<int64_t>(w.s) * L.seg;
         return ((L.cu ? first / L.ct + w.n : static_cast<int64_t>(w.n) * L.c_per_seq) + (w.lo + off - first) / L.ct) * L.H + h;
     };
-    if constexpr (OWN) load_state(nullptr);
-    else if constexpr (MODE == DX) load_state(L.chunk_states[ST] + chunk_unit(len - 1) * (DK * DV));
-    else load_state(w.n_seg > 1 ? L.seg_states[ST] + seg_unit * (DK * DV) : L.m_in[ST] ? L.m_in[ST] + unit * (DK * DV) : nullptr);
+    if constexpr (OWN) load_state(nullptr, false);
+    else if constexpr (MODE == DX) load_state(L.chunk_states[ST] + chunk_unit(len - 1) * (DK * DV), true);
+    else load_state(w.n_seg > 1 ? L.seg_states[ST] + seg_unit * (DK * DV) : L.m_in[ST] ? L.m_in[ST] + unit * (DK * DV) : nullptr, false);
 
     // ---- operands' byte offsets, as in linear attention's pass.  16 bits, along the channels: channels
     // 32 kk + 8 q .. + 7 of token 16 it + l16; along the tokens: tokens 32 tg + 4 q .. + 3 and 32 tg + 16 + 4 q .. + 3,
-    // of state row tile mt's rows or of the wave's columns.
+    // of state row tile mt's rows or of the wave's columns.  (STATE: tile mt has 16 neighbouring rows; the layout's
+    // swizzle is an exclusive or on the units' number, so tile mt's offset is tile 0's with one of its own.)
     uint32_t chan[2], tok[2];
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
         chan[x] = TA::at(l16, 4 * x + q);
         tok[x] = TA::at(4 * q + (l16 >> 2), 4 * x + (l16 & 3));
     }
-    uint8_t* const lds_c = lds.c + hb * Lds::C_BYTES;
+    const uint32_t tok_b = TA::at(4 * q + (l16 >> 2), (l16 & 3) >> 1) + 8 * (l16 & 1);
     uint8_t* const lds_p = lds.p + (STATE ? 0 : hb * Lds::P_BYTES);
     const uint32_t tok_c = TC::at(4 * q + (l16 >> 2), 2 * wc + ((l16 & 3) >> 1)) + 8 * (l16 & 1);
     auto channels = [&](const uint8_t* sm, int it, int kk) {
@@ -315,25 +359,31 @@ __device__ __forceinline__ void value_pass(const Scan& L, int32_t slot, int32_t 
     };
     const float D = (MODE == Y || MODE == DX) && L.D ? L.D[h] : 0.f;
     const bool exact = STATE ? L.exact[ST] != 0 : MODE == Y && L.m_out[ST] && w.s == w.n_seg - 1;
+    bool stored = false;
     for (int c = 0; c < n_chunks; ++c) {
         const int64_t off = chunk_at(c), tok0 = w.lo + off;
         const int n = chunk_n(off), buf = c & 1;
-        __builtin_amdgcn_s_waitcnt(vmcnt_imm(0));
+        const uint8_t* const lds_b = lds.b + (STATE ? buf : 0) * Lds::B_BYTES;
+        uint8_t* const lds_c = lds.c + ((STATE ? buf : 0) * HB + hb) * Lds::C_BYTES;
+        // The rows are there; a chunk's state, stored behind their transfer, may still be under way.
+        if (CHUNKS && stored) __builtin_amdgcn_s_waitcnt(vmcnt_imm(MT));
+        else __builtin_amdgcn_s_waitcnt(vmcnt_imm(0));
         lds_barrier();                               // the tiles and the decays are there
-        float dt_next = 0.f;
-        if (table >= 0 && c + 1 < n_chunks) dt_next = dt_of(c + 1);
+        if (STATE && c + 1 < n_chunks) {             // (all have left the tiles before them)
+            load_b(c + 1);
+            load_c(c + 1);
+        }
+        const uint32_t dt_next = dt_ahead;
+        if (table >= 0 && c + 2 < n_chunks) dt_ahead = dt_of(c + 2);
         const double* cum = lds.cum[buf][hb];
         const float* del = lds.del[buf][hb];
 
         f32x4 O[IT];
         if constexpr (CHUNKS) {
-            if (MODE == S_CHUNKS ? off % L.ct == 0 : c == 0 || (off + TOK) % L.ct == 0) {
-                float* dst = L.chunk_states[ST] + chunk_unit(off) * (DK * DV);
-                if (live)
-#pragma unroll
-                    for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-                        for (int r = 0; r < 4; ++r) dst[(row(mt) + r) * DV + col] = chunk_sign(c) * M[mt][r];
+            stored = live && (MODE == S_CHUNKS ? off % L.ct == 0 : c == 0 || (off + TOK) % L.ct == 0);
+            if (stored) {
+                __builtin_amdgcn_sched_barrier(0);   // (behind the transfers: see the wait)
+                store_state(L.chunk_states[ST] + chunk_unit(off) * (DK * DV), chunk_sign(c), true);
             }
         }
         if constexpr (!STATE) {
@@ -510,11 +560,13 @@ __device__ __forceinline__ void value_pass(const Scan& L, int32_t slot, int32_t 
                     }
 #pragma unroll
                     for (int mt = 0; mt < MT; ++mt) {
-                        const u32x4 kt = tokens(tok[(mt >> 1) & 1] + 2 * tg * TA::ROWS16 + (mt >> 2) * 128 + 8 * (mt & 1), lds.b,
-                                                TA::ROWS16);
-                        if constexpr (THREE) M[mt] = mfma_bf16(kt, cl, M[mt]);
-                        M[mt] = mfma_bf16(kt, cm, M[mt]);
-                        M[mt] = mfma_bf16(kt, ch, M[mt]);
+                        const uint32_t at = STATE ? (tok_b ^ (32 * (mt & 3))) + (mt >> 2) * 128
+                                                  : tok[(mt >> 1) & 1] + (mt >> 2) * 128 + 8 * (mt & 1);
+                        const u32x4 kt = tokens(at + 2 * tg * TA::ROWS16, lds_b, TA::ROWS16);
+                        auto add = [&](const u32x4& cw) { M[mt] = STATE ? mfma_bf16(cw, kt, M[mt]) : mfma_bf16(kt, cw, M[mt]); };
+                        if constexpr (THREE) add(cl);
+                        add(cm);
+                        add(ch);
                     }
                 }
             };
@@ -528,16 +580,19 @@ __device__ __forceinline__ void value_pass(const Scan& L, int32_t slot, int32_t 
                 for (int r = 0; r < 4; ++r) {
                     const float cw = __uint_as_float(vf[jt][r]) * ww[r];
 #pragma unroll
-                    for (int mt = 0; mt < MT; ++mt)
-                        M[mt] = mfma_f32(lds_get<float>(lds.b, TA::at(16 * jt + 4 * q + r, 4 * mt + (l16 >> 2)) + 4 * (l16 & 3)),
-                                         cw, M[mt]);
+                    for (int mt = 0; mt < MT; ++mt) {
+                        const float b = lds_get<float>(lds_b, TA::at(16 * jt + 4 * q + r, 4 * mt + (l16 >> 2)) + 4 * (l16 & 3));
+                        M[mt] = STATE ? mfma_f32(cw, b, M[mt]) : mfma_f32(b, cw, M[mt]);
+                    }
                 }
             }
         }
+        if constexpr (STATE) continue;
         lds_barrier();                               // the tiles have been read, the output is there
-        if (c + 1 < n_chunks) load_b(c + 1);
-        if constexpr (!STATE)
-            if (c + 1 < n_chunks) load_a(c + 1);
+        if (c + 1 < n_chunks) {
+            load_b(c + 1);
+            load_a(c + 1);
+        }
         if constexpr (STAGED) {
             const uint32_t orow = static_cast<uint32_t>(L.out[0].ld);
             int tt = t;                              // formed anew in each chunk: no registers over the loop
@@ -561,12 +616,7 @@ __device__ __forceinline__ void value_pass(const Scan& L, int32_t slot, int32_t 
     float* dst = nullptr;
     if constexpr (OWN) dst = L.seg_states[ST] + seg_unit * (DK * DV);
     else if (MODE != DX && L.m_out[ST] && w.s == (BACK ? 0 : w.n_seg - 1)) dst = L.m_out[ST] + unit * (DK * DV);
-    if (dst && live) {
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) dst[(row(mt) + r) * DV + col] = chunk_sign(n_chunks) * M[mt][r];
-    }
+    if (dst && live) store_state(dst, chunk_sign(n_chunks), false);
     if constexpr (OWN) {
         if (table >= 0 && h0 + table < h_end && lane == 0) L.seg_log[ST][static_cast<int64_t>(slot) * L.H + h0 + table] = log_sum;
     }
@@ -650,7 +700,7 @@ __global__ void __launch_bounds__(256) scan_kernel(Scan L, int32_t elems) {
 // LDS (160 KB), so that the chunks' states, 8 d_k d_v bytes a head written and read, are few.
 template <int DT, int DK, int DV>
 constexpr int grad_tokens() {
-    return (DT == KDA_BF16 ? (DK == 128 ? 128 : 64) : (DV == 64 ? 64 : 32)) / (DT == KDA_BF16 && DK == 128 && DV == 128 ? 2 : 1);
+    return (DT == KDA_BF16 ? 64 : (DV == 64 ? 64 : 32));
 }
 
 // A chunk's decays, one wave per (chunk, head).
@@ -683,7 +733,7 @@ __global__ void __launch_bounds__(256) table_kernel(Scan L) {
 
 template <int DT, int DK, int DV>
 struct GradLds {
-    static constexpr int ES = DT == KDA_BF16 ? 2 : 4, CT = grad_tokens<DT, DK, DV>(), WAVES = DK / 16;
+    static constexpr int ES = DT == KDA_BF16 ? 2 : 4, CT = grad_tokens<DT, DK, DV>(), WAVES = DK / 16;    // of either kind
     using TA = Tile<DV, ES>;
     using TC = Tile<DK, ES>;
     static constexpr int A_BYTES = CT / TA::R * TA::PIECE, C_BYTES = CT / TC::R * TC::PIECE;
@@ -702,6 +752,11 @@ struct GradLds {
     static constexpr int P = 0, R = WAVES, ROWS = 2 * WAVES, COLS = ROWS + TG, DIAG = COLS + TG;
     float red[DIAG + 1][CT];
     float sums[4][WAVES];
+    // a wave's rows of the next head's states (16 bits; both states of more would not fit, and of fewer would cost the
+    // CU's second workgroup its place)
+    static constexpr bool AHEAD = DT == KDA_BF16 && DK * DV == 8192;
+    static constexpr int S_BYTES = 16 * DV * 4;
+    __align__(16) uint8_t states[AHEAD ? WAVES * 2 * S_BYTES : 16];
     // direction 0: outputs i by groups of j <= i; direction 1: outputs j by groups of i >= j, mirrored.  Group number of
     // (output tile, group of others), and back.
     static __host__ __device__ constexpr int number(int dir, int out, int tg) {
@@ -737,11 +792,22 @@ __device__ __forceinline__ float sum_wave(float x) {
     return sum_q(x);
 }
 
-// One workgroup per (chunk, block of a group's heads); wave w has the output channels 16 w .. 16 w + 15 of dC and dB, and
-// groups of scores of either direction.  B and C are read once, the heads' rows and states come one head after the
-// other, the next one's under this one's products.  The scores' products with B and C are formed once, from their sums
-// over the heads (two bf16 terms: they only feed 16-bit outputs).  The states are read as three (exact), for p, r and
-// what comes of them is handed out in fp32.
+// 2^(A d / ln 2) for a sum d of delta between two tokens, A / ln 2 as hi + lo.
+struct Decay {
+    double A2;
+    float hi, lo;
+    __device__ __forceinline__ explicit Decay(float A)
+        : A2(static_cast<double>(A) * LOG2E), hi(static_cast<float>(A2)), lo(static_cast<float>(A2 - static_cast<double>(hi))) {}
+    __device__ __forceinline__ float operator()(float d) const { return __builtin_amdgcn_exp2f(__builtin_fmaf(d, hi, d * lo)); }
+};
+
+// One workgroup per (chunk, block of a group's heads), of two kinds of waves: wave w of the first kind has the output
+// channels 16 w .. 16 w + 15 of dC and dB and forms the states' parts, those of the second share the groups of scores of
+// both directions and move the rows.  (One kind for both needs 300 registers a lane; what does not fit waits for the rows
+// under way: 743 us for 4 x 4096 x 32.)  B and C are read once, the heads' rows come one head after the other, the next
+// one's under this one's products.  The scores' products with B and C are formed once, from their sums over the heads (two
+// bf16 terms: they only feed 16-bit outputs).  The states are read as three (exact), for p, r and what comes of them is
+// handed out in fp32.
 template <int DT, int DK, int DV>
 __device__ __forceinline__ void grad_pass(const Scan& L, int32_t slot, int32_t block, GradLds<DT, DK, DV>& lds) {
     using Lds = GradLds<DT, DK, DV>;
@@ -754,8 +820,9 @@ __device__ __forceinline__ void grad_pass(const Scan& L, int32_t slot, int32_t b
 
     Where w;
     if (!locate(L, slot, w) || w.hi == w.lo) return;
-    const int t = threadIdx.x, lane = t & 63, q = lane >> 4, l16 = lane & 15;
-    const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
+    const int t = threadIdx.x, lane = t & 63;
+    const int wave_all = __builtin_amdgcn_readfirstlane(t >> 6), wave = wave_all % WAVES;
+    const bool scores = wave_all >= WAVES;           // the second kind
     const int32_t rep = L.H / L.G, g = block / L.blocks, blk = block % L.blocks;
     const int32_t h0 = g * rep + blk * L.heads, left = (g + 1) * rep - h0, heads = left < L.heads ? left : L.heads;
     const int n = static_cast<int>(w.hi - w.lo);
@@ -765,94 +832,106 @@ __device__ __forceinline__ void grad_pass(const Scan& L, int32_t slot, int32_t b
         fetch_rows<TA, CT, WAVES>(lds.xy + buf * 2 * Lds::A_BYTES, L.x.p + w.lo * L.x.ld + (h0 + k) * TA::RB, static_cast<uint32_t>(L.x.ld), n, wave, lane);
         fetch_rows<TA, CT, WAVES>(lds.xy + (buf * 2 + 1) * Lds::A_BYTES, L.dy.p + w.lo * L.dy.ld + (h0 + k) * TA::RB, static_cast<uint32_t>(L.dy.ld), n, wave, lane);
     };
-    f32x4 S[NS], G[NS];                              // row 16 wave + l16 of the states, d_v along the contraction
-    auto load_state = [&](f32x4 (&X)[NS], const float* all, int k) {
-        const float* p = all + (units + k) * (DK * DV) + (16 * wave + l16) * DV;
-#pragma unroll
-        for (int i = 0; i < NS; ++i) X[i] = *reinterpret_cast<const f32x4*>(p + (BF ? 32 * (i >> 1) + 8 * q + 4 * (i & 1) : 16 * i + 4 * q));
+    // row 16 wave + l16 of the states, d_v along the contraction: of tile `wave` of 16 rows, as the state pass leaves it
+    auto state_of = [&](int st, int k) { return L.chunk_states[st] + (units + k) * (DK * DV) + 16 * DV * wave; };
+    auto tile_at = [&](int i) {                      // (16 bits: channels 32 (i >> 1) + 8 q + 4 (i & 1) ..)
+        const int q = lane >> 4, l16 = lane & 15;
+        return BF ? (2 * (i >> 1) + (q >> 1)) * 1024 + (2 * (q & 1) + (i & 1)) * 256 + l16 * 16 : i * 1024 + lane * 16;
     };
+    auto request_states = [&](int st, int k) {
+        const __amdgpu_buffer_rsrc_t r = make_rsrc_u(state_of(st, k), Lds::S_BYTES);
+#pragma unroll
+        for (int i = 0; i < NS; ++i)
+            transfer16(r, i * 1024 + lane * 16, lds.states + (2 * wave + st) * Lds::S_BYTES + i * 1024);
+    };
+    auto load_state = [&](f32x4 (&X)[NS], int st, int k) {
+#pragma unroll
+        for (int i = 0; i < NS; ++i)
+            if constexpr (Lds::AHEAD) X[i] = lds_get<f32x4>(lds.states + (2 * wave + st) * Lds::S_BYTES, tile_at(i));
+            else X[i] = *reinterpret_cast<const f32x4*>(reinterpret_cast<const uint8_t*>(state_of(st, k)) + tile_at(i));
+    };
+    const int ts = t - WAVES * 64;                   // the second kind's lanes
     struct Row {
         double dsum;
         float del, ssum;
     };
     auto load_row = [&](int k) {
-        const int64_t at = (units + k) * CT + t;
+        const int64_t at = (units + k) * CT + ts;
         return Row{L.t_dsum[at], L.t_del[at], L.t_ssum[at]};
     };
     auto put_row = [&](int buf, const Row& r) {
-        lds.dsum[buf][t] = r.dsum;
-        lds.del[buf][t] = r.del;
-        lds.ssum[buf][t] = r.ssum;
+        lds.dsum[buf][ts] = r.dsum;
+        lds.del[buf][ts] = r.del;
+        lds.ssum[buf][ts] = r.ssum;
     };
     static_assert(WAVES * 64 >= CT, "a lane per token");
-    fetch_rows<TC, CT, WAVES>(lds.B, L.B.p + w.lo * L.B.ld + g * TC::RB, static_cast<uint32_t>(L.B.ld), n, wave, lane);
-    fetch_rows<TC, CT, WAVES>(lds.C, L.C.p + w.lo * L.C.ld + g * TC::RB, static_cast<uint32_t>(L.C.ld), n, wave, lane);
-    load_head(0, 0);
-    load_state(S, L.chunk_states[S_STATE], 0);
-    load_state(G, L.chunk_states[G_STATE], 0);
-    if (t < CT) put_row(0, load_row(0));
-
-    uint32_t chan[2], chan_c[2];
-#pragma unroll
-    for (int x = 0; x < 2; ++x) {
-        chan[x] = TA::at(l16, 4 * x + q);
-        chan_c[x] = TC::at(l16, 4 * x + q);
+    if (scores) {
+        fetch_rows<TC, CT, WAVES>(lds.C, L.C.p + w.lo * L.C.ld + g * TC::RB, static_cast<uint32_t>(L.C.ld), n, wave, lane);
+        load_head(0, 0);
+        if (ts < CT) put_row(0, load_row(0));
+    } else {
+        fetch_rows<TC, CT, WAVES>(lds.B, L.B.p + w.lo * L.B.ld + g * TC::RB, static_cast<uint32_t>(L.B.ld), n, wave, lane);
     }
-    const uint32_t tok_c = TC::at(4 * q + (l16 >> 2), 2 * wave + ((l16 & 3) >> 1)) + 8 * (l16 & 1);
-    auto tokens = [&](const uint8_t* sm, int tg) {   // the wave's channels of B or C, 32 tokens along the contraction
-        const u32x2 x = lds_transpose(sm + tok_c + 2 * tg * TC::ROWS16), y = lds_transpose(sm + tok_c + (2 * tg + 1) * TC::ROWS16);
-        return u32x4{x[0], x[1], y[0], y[1]};
+
+    // A lane's place in the tiles, formed anew for every head: what comes of it would else be kept in registers over the
+    // loop, more of them than there are.
+    struct Place {
+        int q, l16;
+        uint32_t chan[2], chan_c[2], own;
+    };
+    auto place = [&]() {
+        int ln = lane;
+        asm volatile("" : "+v"(ln));
+        Place a;
+        a.q = ln >> 4;
+        a.l16 = ln & 15;
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            a.chan[x] = TA::at(a.l16, 4 * x + a.q);
+            a.chan_c[x] = TC::at(a.l16, 4 * x + a.q);
+        }
+        a.own = BF ? TC::at(a.l16, 2 * wave + (a.q >> 1)) + 8 * (a.q & 1) : TC::at(a.l16, 4 * wave + a.q);
+        return a;
     };
     // 16 rows' dot products with 16 others, channels along the contraction
-    auto dots = [&](const uint8_t* rows, const uint8_t* cols, int rt, int ct, auto wide, f32x4 acc) {
+    auto dots = [&](const Place& a, const uint8_t* rows, const uint8_t* cols, int rt, int ct, auto wide, f32x4 acc) {
         constexpr bool WIDE = decltype(wide)::value;               // B and C, or x and dy
         using TT = std::conditional_t<WIDE, TC, TA>;
+        rows += rt * TT::ROWS16;
+        cols += ct * TT::ROWS16;
         if constexpr (BF) {
 #pragma unroll
             for (int kk = 0; kk < (WIDE ? KC : KV); ++kk) {
-                const uint32_t at = (WIDE ? chan_c : chan)[kk & 1] + (kk >> 1) * 128;
-                acc = mfma_bf16(lds_get<u32x4>(rows, at + rt * TT::ROWS16), lds_get<u32x4>(cols, at + ct * TT::ROWS16), acc);
+                const uint32_t at = (WIDE ? a.chan_c : a.chan)[kk & 1] + (kk >> 1) * 128;
+                acc = mfma_bf16(lds_get<u32x4>(rows, at), lds_get<u32x4>(cols, at), acc);
             }
         } else {
 #pragma unroll
             for (int mt = 0; mt < (WIDE ? DK : DV) / 16; ++mt) {
-                const f32x4 a = lds_get<f32x4>(rows, TT::at(16 * rt + l16, 4 * mt + q)), b = lds_get<f32x4>(cols, TT::at(16 * ct + l16, 4 * mt + q));
+                const uint32_t at = TT::at(a.l16, 4 * mt + a.q);
+                const f32x4 x = lds_get<f32x4>(rows, at), y = lds_get<f32x4>(cols, at);
 #pragma unroll
-                for (int r = 0; r < 4; ++r) acc = mfma_f32(a[r], b[r], acc);
+                for (int r = 0; r < 4; ++r) acc = mfma_f32(x[r], y[r], acc);
             }
         }
         return acc;
     };
-    auto own = [&](const uint8_t* sm, int it) {      // token 16 it + l16's channels 16 wave + 4 q .. + 3
+    auto own = [&](const Place& a, const uint8_t* sm, int it) {    // token 16 it + l16's channels 16 wave + 4 q .. + 3
         if constexpr (BF) {
-            const u32x2 x = lds_get<u32x2>(sm, TC::at(16 * it + l16, 2 * wave + (q >> 1)) + 8 * (q & 1));
+            const u32x2 x = lds_get<u32x2>(sm, a.own + it * TC::ROWS16);
             return f32x4{lo_f32(x[0]), hi_f32(x[0]), lo_f32(x[1]), hi_f32(x[1])};
         } else {
-            return lds_get<f32x4>(sm, TC::at(16 * it + l16, 4 * wave + q));
+            return lds_get<f32x4>(sm, a.own + it * TC::ROWS16);
         }
     };
 
-    f32x4 dC[IT], dB[IT], P[ROUNDS][TILES], CB[ROUNDS][TILES];
-#pragma unroll
-    for (int it = 0; it < IT; ++it) dC[it] = dB[it] = zero4();
-    for (int k = 0; k < heads; ++k) {
-        const int buf = k & 1;
+    // Both kinds meet at the same barriers: one in front, two a head, three behind.
+    if (scores) {
+        f32x4 P[ROUNDS][TILES], CB[ROUNDS][TILES];
         __builtin_amdgcn_s_waitcnt(vmcnt_imm(0));
-        lds_barrier();                               // the head's rows and decays are there
-        const uint8_t *x = lds.xy + buf * 2 * Lds::A_BYTES, *dy = x + Lds::A_BYTES;
-        const double* dsum = lds.dsum[buf];
-        const float* del = lds.del[buf];
-        const bool more = k + 1 < heads;
-        // decays by the sum of delta between two tokens
-        const double A2 = static_cast<double>(L.A[h0 + k]) * LOG2E;
-        const float A_hi = static_cast<float>(A2), A_lo = static_cast<float>(A2 - static_cast<double>(A_hi));
-        auto decay = [&](float d) { return __builtin_amdgcn_exp2f(__builtin_fmaf(d, A_hi, d * A_lo)); };
-        Row next{};
-        if (more) {
-            load_head(k + 1, buf ^ 1);
-            if (t < CT) next = load_row(k + 1);
-        }
-        if (k == 0) {                                // what the heads share
+        lds_barrier();                               // B and C and the first head's rows are there
+        {
+            const Place a = place();
 #pragma unroll
             for (int i = 0; i < ROUNDS; ++i) {
                 const int grp = wave + i * WAVES, dir = grp >= Lds::GROUPS;
@@ -863,129 +942,210 @@ __device__ __forceinline__ void grad_pass(const Scan& L, int32_t slot, int32_t b
                 Lds::group(dir, grp - dir * Lds::GROUPS, out, tg);
 #pragma unroll
                 for (int hh = 0; hh < TILES; ++hh)
-                    CB[i][hh] = dots(dir ? lds.C : lds.B, dir ? lds.B : lds.C, TILES * tg + hh, out, std::true_type{}, CB[i][hh]);
+                    CB[i][hh] = dots(a, dir ? lds.C : lds.B, dir ? lds.B : lds.C, TILES * tg + hh, out, std::true_type{}, CB[i][hh]);
             }
         }
-        // ---- scores: rows 16 rt + 4 q + r, column 16 out + l16; direction 0: rows j, column i, direction 1: rows i, column j
-        float zA = 0.f, zb = 0.f, dD = 0.f;
+        for (int k = 0; k < heads; ++k) {
+            const int buf = k & 1;
+            const Place a = place();
+            const int q = a.q, l16 = a.l16;
+            const uint8_t *x = lds.xy + buf * 2 * Lds::A_BYTES, *dy = x + Lds::A_BYTES;
+            const double* dsum = lds.dsum[buf];
+            const float* del = lds.del[buf];
+            const Decay decay(L.A[h0 + k]);
+            const bool more = k + 1 < heads;
+            Row next{};
+            if (more) {
+                load_head(k + 1, buf ^ 1);
+                if (ts < CT) next = load_row(k + 1);
+            }
+            // rows 16 rt + 4 q + r, column 16 out + l16; direction 0: rows j, column i, direction 1: rows i, column j
+            float zA = 0.f, zb = 0.f, dD = 0.f;
 #pragma unroll
-        for (int i = 0; i < ROUNDS; ++i) {
-            const int grp = wave + i * WAVES, dir = grp >= Lds::GROUPS;
-            if (grp >= 2 * Lds::GROUPS) continue;
-            int out, tg;
-            Lds::group(dir, grp - dir * Lds::GROUPS, out, tg);
-            const int col = 16 * out + l16;
-            const double dcol = dsum[col];
-            const float dc = del[col];
-            float sum = 0.f, diag = 0.f;
+            for (int i = 0; i < ROUNDS; ++i) {
+                const int grp = wave + i * WAVES, dir = grp >= Lds::GROUPS;
+                if (grp >= 2 * Lds::GROUPS) continue;
+                int out, tg;
+                Lds::group(dir, grp - dir * Lds::GROUPS, out, tg);
+                const int col = 16 * out + l16;
+                const double dcol = dsum[col];
+                const float dc = del[col];
+                float sum = 0.f, diag = 0.f;
 #pragma unroll
-            for (int hh = 0; hh < TILES; ++hh) {
-                const int rt = TILES * tg + hh, row = 16 * rt + 4 * q;
-                const f32x4 X = dots(dir ? dy : x, dir ? x : dy, rt, out, std::false_type{}, zero4());
-                if (dir == 0) {
-                    const f32x4 dr = lds_get<f32x4>(del, 4 * row), ss = lds_get<f32x4>(lds.ssum[buf], 4 * row);
-                    const float scol = lds.ssum[buf][col];
+                for (int hh = 0; hh < TILES; ++hh) {
+                    const int rt = TILES * tg + hh, row = 16 * rt + 4 * q;
+                    const f32x4 X = dots(a, dir ? dy : x, dir ? x : dy, rt, out, std::false_type{}, zero4());
+                    if (dir == 0) {
+                        const f32x4 dr = lds_get<f32x4>(del, 4 * row), ss = lds_get<f32x4>(lds.ssum[buf], 4 * row);
+                        const float scol = lds.ssum[buf][col];
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        const int j = row + r;
-                        const float d = static_cast<float>(dcol - dsum[j]), e = j <= col ? decay(d) * X[r] : 0.f, y = e * CB[i][hh][r];
-                        const float z = j < col ? y * dr[r] : 0.f;
-                        P[i][hh][r] = __builtin_fmaf(e, dr[r], P[i][hh][r]);
-                        sum += z;
-                        zA = __builtin_fmaf(z, d, zA);
-                        zb = __builtin_fmaf(z, scol - ss[r], zb);
-                        if (j == col) {
-                            diag += y;
-                            dD += X[r];
+                        for (int r = 0; r < 4; ++r) {
+                            const int j = row + r;
+                            const float d = static_cast<float>(dcol - dsum[j]), e = j <= col ? decay(d) * X[r] : 0.f, y = e * CB[i][hh][r];
+                            const float z = j < col ? y * dr[r] : 0.f;
+                            P[i][hh][r] = __builtin_fmaf(e, dr[r], P[i][hh][r]);
+                            sum += z;
+                            zA = __builtin_fmaf(z, d, zA);
+                            zb = __builtin_fmaf(z, scol - ss[r], zb);
+                            if (j == col) {
+                                diag += y;
+                                dD += X[r];
+                            }
+                        }
+                    } else {
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) {
+                            const int j = row + r;
+                            const float e = j >= col ? decay(static_cast<float>(dsum[j] - dcol)) * X[r] : 0.f;
+                            P[i][hh][r] = __builtin_fmaf(e, dc, P[i][hh][r]);
+                            sum += j > col ? e * CB[i][hh][r] : 0.f;
                         }
                     }
-                } else {
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        const int j = row + r;
-                        const float e = j >= col ? decay(static_cast<float>(dsum[j] - dcol)) * X[r] : 0.f;
-                        P[i][hh][r] = __builtin_fmaf(e, dc, P[i][hh][r]);
-                        sum += j > col ? e * CB[i][hh][r] : 0.f;
-                    }
+                }
+                sum = sum_q(sum);
+                if (q == 0) lds.red[(dir ? Lds::COLS : Lds::ROWS) + tg][col] = sum;
+                if (dir == 0 && out / TILES == tg) { // the group that holds the tile's own tokens
+                    diag = sum_q(diag);
+                    if (q == 0) lds.red[Lds::DIAG][col] = diag;
                 }
             }
-            sum = sum_q(sum);
-            if (q == 0) lds.red[(dir ? Lds::COLS : Lds::ROWS) + tg][col] = sum;
-            if (dir == 0 && out / TILES == tg) {     // the group that holds the tile's own tokens
-                diag = sum_q(diag);
-                if (q == 0) lds.red[Lds::DIAG][col] = diag;
+            zA = sum_wave(zA);
+            zb = sum_wave(zb);
+            dD = sum_wave(dD);
+            if (lane == 0) {
+                lds.sums[0][wave] = zA;
+                lds.sums[1][wave] = zb;
+                lds.sums[2][wave] = dD;
+            }
+            if (more && ts < CT) put_row(buf ^ 1, next);           // (all have left the last head's)
+            __builtin_amdgcn_s_waitcnt(vmcnt_imm(0));
+            lds_barrier();                           // the sums and the next head's rows are there
+            if (ts < 4) {
+                float sum = 0.f;
+#pragma unroll
+                for (int v = 0; v < WAVES; ++v) sum += lds.sums[ts][v];
+                if (ts == 3) sum = static_cast<float>(sum * exp2(dsum[CT - 1] * decay.A2));
+                (ts == 0 ? L.zA : ts == 1 ? L.zb : ts == 2 ? L.dDp : L.thr)[units + k] = sum;
+            }
+            lds_barrier();                           // the sums have been read
+        }
+#pragma unroll
+        for (int dir = 0; dir < 2; ++dir) {
+            if (dir == 1) lds_barrier();             // direction 0's scores have been read
+#pragma unroll
+            for (int i = 0; i < ROUNDS; ++i) {
+                const int grp = wave + i * WAVES - dir * Lds::GROUPS;
+                if (grp < 0 || grp >= Lds::GROUPS) continue;
+                if constexpr (BF) {
+                    u32x4 hi, lo;
+#pragma unroll
+                    for (int hh = 0; hh < 2; ++hh) {
+                        uint32_t x0, y0, x1, y1;
+                        split_pair(P[i][hh][0], P[i][hh][1], x0, y0);
+                        split_pair(P[i][hh][2], P[i][hh][3], x1, y1);
+                        hi[2 * hh] = x0; hi[2 * hh + 1] = x1;
+                        lo[2 * hh] = y0; lo[2 * hh + 1] = y1;
+                    }
+                    lds_put(lds.xy, grp * 2048 + lane * 16, hi);
+                    lds_put(lds.xy, grp * 2048 + 1024 + lane * 16, lo);
+                } else {
+                    lds_put(lds.xy, grp * 1024 + lane * 16, P[i][0]);
+                }
+            }
+            lds_barrier();
+        }
+        return;
+    }
+
+    f32x4 dC[IT], dB[IT];
+#pragma unroll
+    for (int it = 0; it < IT; ++it) dC[it] = dB[it] = zero4();
+    if constexpr (Lds::AHEAD) {
+        request_states(S_STATE, 0);
+        request_states(G_STATE, 0);
+    }
+    __builtin_amdgcn_s_waitcnt(vmcnt_imm(0));
+    lds_barrier();
+    for (int k = 0; k < heads; ++k) {
+        const int buf = k & 1;
+        const Place a = place();
+        const int q = a.q, l16 = a.l16;
+        const uint8_t *x = lds.xy + buf * 2 * Lds::A_BYTES, *dy = x + Lds::A_BYTES;
+        const double* dsum = lds.dsum[buf];
+        const float* del = lds.del[buf];
+        const Decay decay(L.A[h0 + k]);
+        f32x4 S[NS], G[NS];
+        if constexpr (Lds::AHEAD) {                  // the states are there; wave 0's four stores behind them may be under way
+            if (wave == 0 && k > 0) __builtin_amdgcn_s_waitcnt(vmcnt_imm(4));
+            else __builtin_amdgcn_s_waitcnt(vmcnt_imm(0));
+            wave_fence();
+        }
+        load_state(S, S_STATE, k);
+        load_state(G, G_STATE, k);
+        if constexpr (Lds::AHEAD) {
+            __builtin_amdgcn_s_waitcnt(0xC07F);      // they are in registers: lgkmcnt(0)
+            wave_fence();
+            if (k + 1 < heads) {
+                request_states(S_STATE, k + 1);
+                request_states(G_STATE, k + 1);
             }
         }
-        // ---- the states' parts
         float thr = 0.f;
 #pragma unroll
         for (int i = 0; i < NS; ++i)
 #pragma unroll
             for (int r = 0; r < 4; ++r) thr = __builtin_fmaf(S[i][r], G[i][r], thr);
+        thr = sum_wave(thr);
+        if (lane == 0) lds.sums[3][wave] = thr;
         const double all = dsum[CT - 1];
-        auto state_part = [&](f32x4 (&X)[NS], const float* states, const uint8_t* rows, auto back) {
+        auto state_part = [&](const f32x4 (&X)[NS], const uint8_t* rows, auto back) {
             constexpr bool BACK = decltype(back)::value;
             u32x4 hi[BF ? KV : 1], mid[BF ? KV : 1], lo[BF ? KV : 1];
-            f32x4 F[BF ? 1 : NS];
             if constexpr (BF) {
 #pragma unroll
                 for (int kk = 0; kk < KV; ++kk)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         const f32x4& m = X[2 * kk + (e >> 1)];
-                        uint32_t a, b, c;
-                        split3(m[2 * (e & 1)], m[2 * (e & 1) + 1], a, b, c);
-                        hi[kk][e] = a;
-                        mid[kk][e] = b;
-                        lo[kk][e] = c;
+                        uint32_t u, v, w3;
+                        split3(m[2 * (e & 1)], m[2 * (e & 1) + 1], u, v, w3);
+                        hi[kk][e] = u;
+                        mid[kk][e] = v;
+                        lo[kk][e] = w3;
                     }
-            } else {
-#pragma unroll
-                for (int i = 0; i < NS; ++i) F[i] = X[i];
             }
-            if (more) load_state(X, states, k + 1);
 #pragma unroll
             for (int it = 0; it < IT; ++it) {
+                if (it % 2 == 0) __builtin_amdgcn_sched_barrier(0);    // (few loads at a time: registers)
                 f32x4 O = zero4();
                 if constexpr (BF) {
 #pragma unroll
                     for (int kk = 0; kk < KV; ++kk) {
-                        const u32x4 a = lds_get<u32x4>(rows, chan[kk & 1] + it * TA::ROWS16 + (kk >> 1) * 128);
-                        O = mfma_bf16(lo[kk], a, O);
-                        O = mfma_bf16(mid[kk], a, O);
-                        O = mfma_bf16(hi[kk], a, O);
+                        const u32x4 v = lds_get<u32x4>(rows, a.chan[kk & 1] + it * TA::ROWS16 + (kk >> 1) * 128);
+                        O = mfma_bf16(lo[kk], v, O);
+                        O = mfma_bf16(mid[kk], v, O);
+                        O = mfma_bf16(hi[kk], v, O);
                     }
                 } else {
 #pragma unroll
                     for (int i = 0; i < NS; ++i) {
-                        const f32x4 a = lds_get<f32x4>(rows, TA::at(16 * it + l16, 4 * i + q));
+                        const f32x4 v = lds_get<f32x4>(rows, TA::at(l16, 4 * i + q) + it * TA::ROWS16);
 #pragma unroll
-                        for (int r = 0; r < 4; ++r) O = mfma_f32(F[i][r], a[r], O);
+                        for (int r = 0; r < 4; ++r) O = mfma_f32(X[i][r], v[r], O);
                     }
                 }
                 const double di = dsum[16 * it + l16];
                 O *= decay(static_cast<float>(BACK ? all - di : di));
-                const f32x4 o = own(BACK ? lds.B : lds.C, it);
+                const f32x4 o = own(a, BACK ? lds.B : lds.C, it);
                 if constexpr (BACK) dB[it] += O * del[16 * it + l16];
                 else dC[it] += O;
                 const float s = sum_q(__builtin_fmaf(o[3], O[3], __builtin_fmaf(o[2], O[2], __builtin_fmaf(o[1], O[1], o[0] * O[0]))));
                 if (q == 0) lds.red[(BACK ? Lds::R : Lds::P) + wave][16 * it + l16] = s;
             }
         };
-        state_part(S, L.chunk_states[S_STATE], dy, std::false_type{});
-        state_part(G, L.chunk_states[G_STATE], x, std::true_type{});
-        zA = sum_wave(zA);
-        zb = sum_wave(zb);
-        dD = sum_wave(dD);
-        thr = sum_wave(thr);
-        if (lane == 0) {
-            lds.sums[0][wave] = zA;
-            lds.sums[1][wave] = zb;
-            lds.sums[2][wave] = dD;
-            lds.sums[3][wave] = thr;
-        }
-        if (more && t < CT) put_row(buf ^ 1, next);  // (all have left the last head's)
-        lds_barrier();                               // the sums are there, the rows have been read
+        state_part(S, dy, std::false_type{});
+        state_part(G, x, std::true_type{});
+        lds_barrier();                               // the sums are there
         if (t < n) {
             float p = 0.f, r = 0.f, rows = 0.f, cols = 0.f;
 #pragma unroll
@@ -1005,40 +1165,17 @@ __device__ __forceinline__ void grad_pass(const Scan& L, int32_t slot, int32_t b
             L.pp[at] = p;
             L.xr[at] = r;
         }
-        if (t >= WAVES * 64 - 4) {
-            const int i = t - (WAVES * 64 - 4);
-            float sum = 0.f;
-#pragma unroll
-            for (int x = 0; x < WAVES; ++x) sum += lds.sums[i][x];
-            if (i == 3) sum = static_cast<float>(sum * exp2(all * A2));
-            (i == 0 ? L.zA : i == 1 ? L.zb : i == 2 ? L.dDp : L.thr)[units + k] = sum;
-        }
+        lds_barrier();                               // the sums have been read
     }
-    // ---- the scores' parts
+    const int q = lane >> 4, l16 = lane & 15;
+    const uint32_t tok_c = TC::at(4 * q + (l16 >> 2), 2 * wave + ((l16 & 3) >> 1)) + 8 * (l16 & 1);
+    auto tokens = [&](const uint8_t* sm, int tg) {   // the wave's channels of B or C, 32 tokens along the contraction
+        const u32x2 x = lds_transpose(sm + tok_c + 2 * tg * TC::ROWS16), y = lds_transpose(sm + tok_c + (2 * tg + 1) * TC::ROWS16);
+        return u32x4{x[0], x[1], y[0], y[1]};
+    };
 #pragma unroll
     for (int dir = 0; dir < 2; ++dir) {
-        if (dir == 1) lds_barrier();                 // direction 0's scores have been read
-#pragma unroll
-        for (int i = 0; i < ROUNDS; ++i) {
-            const int grp = wave + i * WAVES - dir * Lds::GROUPS;
-            if (grp < 0 || grp >= Lds::GROUPS) continue;
-            if constexpr (BF) {
-                u32x4 hi, lo;
-#pragma unroll
-                for (int hh = 0; hh < 2; ++hh) {
-                    uint32_t x0, y0, x1, y1;
-                    split_pair(P[i][hh][0], P[i][hh][1], x0, y0);
-                    split_pair(P[i][hh][2], P[i][hh][3], x1, y1);
-                    hi[2 * hh] = x0; hi[2 * hh + 1] = x1;
-                    lo[2 * hh] = y0; lo[2 * hh + 1] = y1;
-                }
-                lds_put(lds.xy, grp * 2048 + lane * 16, hi);
-                lds_put(lds.xy, grp * 2048 + 1024 + lane * 16, lo);
-            } else {
-                lds_put(lds.xy, grp * 1024 + lane * 16, P[i][0]);
-            }
-        }
-        lds_barrier();
+        lds_barrier();                               // the scores are there
         f32x4(&O)[IT] = dir ? dB : dC;
         const uint8_t* sm = dir ? lds.C : lds.B;
 #pragma unroll
@@ -1062,6 +1199,7 @@ __device__ __forceinline__ void grad_pass(const Scan& L, int32_t slot, int32_t b
                 }
             }
         }
+        if (dir == 0) lds_barrier();                 // direction 0's scores have been read
         // ---- out: lane l16 holds token 16 it + l16, four neighbouring channels
         if (L.part[dir]) {
             const uint32_t orow = static_cast<uint32_t>(L.G) * DK * 4;
@@ -1086,7 +1224,7 @@ __device__ __forceinline__ void grad_pass(const Scan& L, int32_t slot, int32_t b
 }
 
 template <int DT, int DK, int DV>
-__global__ void __launch_bounds__(DK * 4, DK / 64) grad_kernel(Scan L) {
+__global__ void __launch_bounds__(DK * 8, DK / 32) grad_kernel(Scan L) {
     __shared__ GradLds<DT, DK, DV> lds;
     uint32_t unit;
     int32_t pass;
@@ -1342,7 +1480,7 @@ hipError_t launch_states(Scan L, int32_t dk, int32_t dv, int32_t passes, hipStre
                                dim3(HB * DV * 4), 0, stream, L, passes);
             return hipGetLastError();
         };
-        if constexpr (DV == 64)
+        if constexpr (DV == 64 && !CHUNKS)
             if (value_heads(L.H, L.G, dv) == 2) return go(Int<2>{});
         return go(Int<1>{});
     });
@@ -1410,7 +1548,7 @@ hipError_t backward(const ScanArgs& a, hipStream_t stream) {
         hipLaunchKernelGGL((table_kernel<DT, CT>), dim3(waves), dim3(256), 0, stream, L);
         hipError_t r = hipGetLastError();
         if (r != hipSuccess) return r;
-        hipLaunchKernelGGL((grad_kernel<DT, DK, DV>), dim3(xcd_grid(int64_t(L.slots) * L.blocks * L.G, 1)), dim3(DK * 4), 0, stream, L);
+        hipLaunchKernelGGL((grad_kernel<DT, DK, DV>), dim3(xcd_grid(int64_t(L.slots) * L.blocks * L.G, 1)), dim3(DK * 8), 0, stream, L);
         r = hipGetLastError();
         if (r != hipSuccess) return r;
         hipLaunchKernelGGL((decay_grad_kernel<DT, CT>), dim3(waves), dim3(256), 0, stream, L);
