@@ -55,8 +55,7 @@ struct Scan {
     double* seg_log[2];      // [slots, H] log2 of a segment's decay
     float* chunk_states[2];  // [c_slots, H, dk, dv]: S before a chunk, G behind it
     float* part[2];          // [head blocks of a group, tokens, G, dk] dC, dB per block; nullptr: one block
-    double* t_dsum;          // [c_slots, H, ct] a chunk's running sums of delta, delta, running sums of its slope
-    float *t_del, *t_ssum;
+    uint8_t* cards;          // [c_slots, H] Card of a chunk's decays
     // [H, tokens]: sum_j z_tj - sum_i z_it; p_t; x_t . u_t from this chunk's outputs, and from later ones (r_t / delta_t)
     float *zz, *pp, *xz, *xr;
     // [c_slots, H]: sums of z_ij (W_i - W_j) for W of delta and of the slopes, of x . dy, <G, S>
@@ -73,6 +72,21 @@ enum { S_STATE = 0, G_STATE = 1 };
 // Passes along the tokens: y, dx, a segment's own contribution to the states, and the states of every chunk.
 enum Mode { Y, DX, S_ONLY, G_ONLY, S_CHUNKS, G_CHUNKS };
 constexpr int32_t WHOLE = 0x7fffffff;
+
+template <int DT>
+constexpr int CHUNK = DT == KDA_BF16 ? 64 : 32;      // tokens
+
+// What a chunk's decays of one head come to, made once for all kernels of the backward pass.  D_i is the running sum of
+// delta in the chunk, e the last token of a token's tile of 16, s the last one before that tile.
+template <int CT>
+struct Card {
+    double dsum[CT];         // D_i
+    float del[CT], ssum[CT]; // delta, running sums of its slope
+    float d_end[CT], s_end[CT];                      // D_e - D_j, and the slopes' sums
+    float w_end[CT], w_start[CT];                    // delta_j e^(A (D_e - D_j)), e^(A (D_i - D_s))
+    float before[CT], after[CT];                     // e^(A D_i), e^(A (D_n - D_i))
+    f32x2 over, pad;         // -e^(A D_n) as a sum of two
+};
 constexpr double LOG2E = 1.4426950408889634074;
 
 // ---------------------------------------------------------------- decays
@@ -173,7 +187,7 @@ __device__ __forceinline__ void decay_state(f32x4 (&M)[MT], f32x2 over) {
 template <int DT, int DK, int DV, int HB, int MODE>
 struct ValueLds {
     static constexpr bool STATE = MODE >= S_ONLY;
-    static constexpr int ES = DT == KDA_BF16 ? 2 : 4, TOK = DT == KDA_BF16 ? 64 : 32, WAVES = HB * DV / 16;
+    static constexpr int ES = DT == KDA_BF16 ? 2 : 4, TOK = CHUNK<DT>, WAVES = HB * DV / 16;
     using TA = Tile<DK, ES>;
     using TC = Tile<DV, ES>;
     static constexpr int C_BYTES = TOK / TC::R * TC::PIECE, P_BYTES = (ES == 2 ? 12 : 3) * 1024;
@@ -200,6 +214,7 @@ __device__ __forceinline__ void value_pass(const Scan& L, int32_t slot, int32_t 
     using TC = typename Lds::TC;
     constexpr bool BF = DT == KDA_BF16, STATE = Lds::STATE, BACK = MODE == DX || MODE == G_ONLY || MODE == G_CHUNKS;
     constexpr bool OWN = MODE == S_ONLY || MODE == G_ONLY, CHUNKS = MODE == S_CHUNKS || MODE == G_CHUNKS;
+    constexpr bool CARDS = CHUNKS || MODE == DX;
     constexpr int TOK = Lds::TOK, WAVES = Lds::WAVES, WPH = DV / 16;
     constexpr int IT = TOK / 16, MT = DK / 16, KK = DK / 32, JG = TOK / 32;
     constexpr int OS = ODT == KDA_BF16 ? 2 : 4;
@@ -243,14 +258,50 @@ __device__ __forceinline__ void value_pass(const Scan& L, int32_t slot, int32_t 
     const int table = wave - (WAVES - HB);
     const int32_t th = h0 + table < h_end ? h0 + (table < 0 ? 0 : table) : h_end - 1;
     const float A = L.A[th], bias = L.bias ? L.bias[th] : 0.f;
-    auto dt_of = [&](int c) {
+    // a chunk's place among those of all sequences: of the chunk that token w.lo + off belongs to
+    const int64_t first = w.lo - static_cast<int64_t>(w.s) * L.seg;
+    const int64_t chunk0 = (L.cu ? first / TOK + w.n : static_cast<int64_t>(w.n) * L.c_per_seq);
+    auto chunk_unit = [&](int64_t off, int32_t head) { return (chunk0 + (w.lo - first + off) / TOK) * L.H + head; };
+    // what the decays are made of, a lane's token; fetched a chunk ahead of its use
+    struct Ahead {
+        uint32_t dt;
+        double dsum;
+        float del, w;
+        f32x2 over;
+    };
+    auto ahead_of = [&](int c) {
         const int64_t off = chunk_at(c);
-        return load_dt<DT>(L, w.lo + off, chunk_n(off), th, lane);
+        Ahead a{};
+        if constexpr (CARDS) {
+            using Cd = Card<TOK>;
+            const uint32_t l = lane % TOK;
+            const __amdgpu_buffer_rsrc_t r = make_rsrc_u(L.cards + chunk_unit(off, th) * sizeof(Cd), sizeof(Cd));
+            auto word = [&](uint32_t at) { return __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(r, at + 4 * l, 0, 0)); };
+            if constexpr (MODE != G_CHUNKS) a.del = word(offsetof(Cd, del));
+            if constexpr (MODE == DX) a.dsum = __builtin_bit_cast(double, __builtin_amdgcn_raw_buffer_load_b64(r, 8 * l, 0, 0));
+            else a.w = word(BACK ? offsetof(Cd, before) : offsetof(Cd, after));
+            a.over = __builtin_bit_cast(f32x2, __builtin_amdgcn_raw_buffer_load_b64(r, offsetof(Cd, over), 0, 0));
+        } else {
+            a.dt = load_dt<DT>(L, w.lo + off, chunk_n(off), th, lane);
+        }
+        return a;
     };
     double log_sum = 0.0;
-    auto decays = [&](int c, uint32_t dt) {
+    auto decays = [&](int c, const Ahead& a) {
         const int buf = c & 1, n = chunk_n(chunk_at(c));
-        const float delta = lane < n ? strength(open_dt<DT>(dt), bias).delta : 0.f;
+        if constexpr (CARDS) {
+            if (lane < TOK) {
+                if constexpr (MODE == DX) {
+                    lds.cum[buf][table][lane] = a.dsum * (static_cast<double>(A) * LOG2E);
+                    lds.del[buf][table][lane] = a.del;
+                } else {
+                    lds.up[STATE ? buf : 0][table][lane] = chunk_sign(c + 1) * (BACK ? a.w : a.del * a.w);
+                }
+                if (lane == 0) lds.over[buf][table] = a.over;
+            }
+            return;
+        }
+        const float delta = lane < n ? strength(open_dt<DT>(a.dt), bias).delta : 0.f;
         const double cum = prefix_sum(static_cast<double>(delta) * (static_cast<double>(A) * LOG2E));
         const double all = lane_value(cum, TOK - 1), over = -exp2(all);
         const float hi = static_cast<float>(over);
@@ -267,9 +318,10 @@ __device__ __forceinline__ void value_pass(const Scan& L, int32_t slot, int32_t 
         load_b(0);
         if constexpr (!STATE) load_a(0);
         load_c(0);
-        if (table >= 0) decays(0, dt_of(0));
+        if (table >= 0) decays(0, ahead_of(0));
     }
-    uint32_t dt_ahead = table >= 0 && n_chunks > 1 ? dt_of(1) : 0u;    // a chunk ahead of its use: it is there by then
+    Ahead ahead{};
+    if (table >= 0 && n_chunks > 1) ahead = ahead_of(1);
 
     // ---- the state, tile mt of 16 rows.  Y and DX: register r of lane (l16, q) holds row row(mt) + r, column 16 wc + l16;
     // STATE: row 16 mt + l16, column 16 wc + 4 q + r, so that a lane's four lie side by side.  The states of the chunks
@@ -316,13 +368,8 @@ __device__ __forceinline__ void value_pass(const Scan& L, int32_t slot, int32_t 
                 }
         }
     };
-    // a chunk's place among the states of all chunks: of the one that token w.lo + off belongs to
-    auto chunk_unit = [&](int64_t off) {
-        const int64_t first = w.lo - static_cast<int64_t>(w.s) * L.seg;
-        return ((L.cu ? first / L.ct + w.n : static_cast<int64_t>(w.n) * L.c_per_seq) + (w.lo + off - first) / L.ct) * L.H + h;
-    };
     if constexpr (OWN) load_state(nullptr, false);
-    else if constexpr (MODE == DX) load_state(L.chunk_states[ST] + chunk_unit(len - 1) * (DK * DV), true);
+    else if constexpr (MODE == DX) load_state(L.chunk_states[ST] + chunk_unit(len - 1, h) * (DK * DV), true);
     else load_state(w.n_seg > 1 ? L.seg_states[ST] + seg_unit * (DK * DV) : L.m_in[ST] ? L.m_in[ST] + unit * (DK * DV) : nullptr, false);
 
     // ---- operands' byte offsets, as in linear attention's pass.  16 bits, along the channels: channels
@@ -373,17 +420,17 @@ __device__ __forceinline__ void value_pass(const Scan& L, int32_t slot, int32_t 
             load_b(c + 1);
             load_c(c + 1);
         }
-        const uint32_t dt_next = dt_ahead;
-        if (table >= 0 && c + 2 < n_chunks) dt_ahead = dt_of(c + 2);
+        const Ahead next = ahead;
+        if (table >= 0 && c + 2 < n_chunks) ahead = ahead_of(c + 2);
         const double* cum = lds.cum[buf][hb];
         const float* del = lds.del[buf][hb];
 
         f32x4 O[IT];
         if constexpr (CHUNKS) {
-            stored = live && (MODE == S_CHUNKS ? off % L.ct == 0 : c == 0 || (off + TOK) % L.ct == 0);
+            stored = live;
             if (stored) {
                 __builtin_amdgcn_sched_barrier(0);   // (behind the transfers: see the wait)
-                store_state(L.chunk_states[ST] + chunk_unit(off) * (DK * DV), chunk_sign(c), true);
+                store_state(L.chunk_states[ST] + chunk_unit(off, h) * (DK * DV), chunk_sign(c), true);
             }
         }
         if constexpr (!STATE) {
@@ -474,7 +521,7 @@ __device__ __forceinline__ void value_pass(const Scan& L, int32_t slot, int32_t 
                 O[it] *= chunk_sign(c) * pow2(BACK ? all - ci : ci);
             }
         }
-        if (table >= 0 && c + 1 < n_chunks) decays(c + 1, dt_next);
+        if (table >= 0 && c + 1 < n_chunks) decays(c + 1, next);
         decay_state(M, lds.over[buf][hb]);
 
         // ---- c along the tokens
@@ -696,44 +743,43 @@ __global__ void __launch_bounds__(256) scan_kernel(Scan L, int32_t elems) {
 
 // ---------------------------------------------------------------- dC, dB and the ways between tokens
 
-// Tokens of a chunk of the gradients: as many as their rows, of one group and of two heads in turn, leave room for in
-// LDS (160 KB), so that the chunks' states, 8 d_k d_v bytes a head written and read, are few.
-template <int DT, int DK, int DV>
-constexpr int grad_tokens() {
-    return (DT == KDA_BF16 ? 64 : (DV == 64 ? 64 : 32));
-}
-
-// A chunk's decays, one wave per (chunk, head).
-template <int DT, int CT>
-__global__ void __launch_bounds__(256) table_kernel(Scan L) {
+// A chunk's decays, one wave per (chunk, head), a token a lane.
+template <int DT>
+__global__ void __launch_bounds__(256) card_kernel(Scan L) {
+    constexpr int CT = CHUNK<DT>;
     const int64_t u = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6);
     const int lane = threadIdx.x & 63;
     if (u >= static_cast<int64_t>(L.c_slots) * L.H) return;
     const int32_t slot = static_cast<int32_t>(u / L.H), h = static_cast<int32_t>(u % L.H);
     Where w;
     if (!locate(L, slot, w)) return;
-    const float bias = L.bias ? L.bias[h] : 0.f;
-    const int n = static_cast<int>(w.hi - w.lo);
-    double d0 = 0.0, s0 = 0.0;
-#pragma unroll
-    for (int b = 0; b < (CT + 63) / 64; ++b) {
-        const int i = 64 * b + lane;
-        Strength s = {0.f, 0.f};
-        if (i < n) s = strength(load_as_f32<DT>(L.dt.p + (w.lo + i) * L.dt.ld, h), bias);
-        const double d = d0 + prefix_sum(static_cast<double>(s.delta)), o = s0 + prefix_sum(static_cast<double>(s.slope));
-        d0 = lane_value(d, 63);
-        s0 = lane_value(o, 63);
-        if (i < CT) {
-            L.t_dsum[u * CT + i] = d;
-            L.t_del[u * CT + i] = s.delta;
-            L.t_ssum[u * CT + i] = static_cast<float>(o);
-        }
+    const double A2 = static_cast<double>(L.A[h]) * LOG2E;
+    Strength s = {0.f, 0.f};
+    if (lane < w.hi - w.lo) s = strength(load_as_f32<DT>(L.dt.p + (w.lo + lane) * L.dt.ld, h), L.bias ? L.bias[h] : 0.f);
+    const double d = prefix_sum(static_cast<double>(s.delta)), o = prefix_sum(static_cast<double>(s.slope));
+    const int e = lane | 15, start = (lane & ~15) - 1;
+    const double de = shuffle(d, e), oe = shuffle(o, e), ds = shuffle(d, start < 0 ? 0 : start), all = lane_value(d, CT - 1);
+    if (lane >= CT) return;
+    Card<CT>& c = reinterpret_cast<Card<CT>*>(L.cards)[u];
+    c.dsum[lane] = d;
+    c.del[lane] = s.delta;
+    c.ssum[lane] = static_cast<float>(o);
+    c.d_end[lane] = static_cast<float>(de - d);
+    c.s_end[lane] = static_cast<float>(oe - o);
+    c.w_end[lane] = s.delta * pow2(A2 * (de - d));
+    c.w_start[lane] = pow2(A2 * (start < 0 ? d : d - ds));
+    c.before[lane] = pow2(A2 * d);
+    c.after[lane] = pow2(A2 * (all - d));
+    if (lane == 0) {
+        const double over = -exp2(A2 * all);
+        const float hi = static_cast<float>(over);
+        c.over = f32x2{hi, static_cast<float>(over - static_cast<double>(hi))};
     }
 }
 
 template <int DT, int DK, int DV>
 struct GradLds {
-    static constexpr int ES = DT == KDA_BF16 ? 2 : 4, CT = grad_tokens<DT, DK, DV>(), WAVES = DK / 16;    // of either kind
+    static constexpr int ES = DT == KDA_BF16 ? 2 : 4, CT = CHUNK<DT>, WAVES = DK / 16;    // of either kind
     using TA = Tile<DV, ES>;
     using TC = Tile<DK, ES>;
     static constexpr int A_BYTES = CT / TA::R * TA::PIECE, C_BYTES = CT / TC::R * TC::PIECE;
@@ -746,15 +792,16 @@ struct GradLds {
     // x and dy of a head and of the next one; in the end the scores, summed over the heads, one direction at a time
     __align__(16) uint8_t xy[4 * A_BYTES];
     static_assert(GROUPS * G_BYTES <= 4 * A_BYTES, "the scores take the place of the rows");
-    __align__(16) double dsum[2][CT];
-    __align__(16) float del[2][CT], ssum[2][CT];
+    static constexpr int CARD = (sizeof(Card<CT>) + 1023) / 1024;  // KB
+    static_assert(CARD <= WAVES, "a wave per KB");
+    __align__(16) uint8_t card[2][CARD * 1024];
     // p and r / delta by waves, sums of z over j and of z / delta over i by groups, z_jj / delta_j
     static constexpr int P = 0, R = WAVES, ROWS = 2 * WAVES, COLS = ROWS + TG, DIAG = COLS + TG;
     float red[DIAG + 1][CT];
     float sums[4][WAVES];
     // a wave's rows of the next head's states (16 bits; both states of more would not fit, and of fewer would cost the
     // CU's second workgroup its place)
-    static constexpr bool AHEAD = DT == KDA_BF16 && DK * DV == 8192;
+    static constexpr bool AHEAD = DT == KDA_BF16 && DK == 128 && DV == 64;
     static constexpr int S_BYTES = 16 * DV * 4;
     __align__(16) uint8_t states[AHEAD ? WAVES * 2 * S_BYTES : 16];
     // direction 0: outputs i by groups of j <= i; direction 1: outputs j by groups of i >= j, mirrored.  Group number of
@@ -788,7 +835,14 @@ __device__ __forceinline__ float sum_q(float x) {
 }
 __device__ __forceinline__ float sum_wave(float x) {
 #pragma unroll
-    for (int off = 1; off < 16; off <<= 1) x += __shfl_xor(x, off, 64);
+    for (int k = 0; k < 4; ++k) {                    // rows of 16 lanes, turned by 8, 4, 2, 1
+        const int u = static_cast<int>(__float_as_uint(x));
+        const int v = k == 0   ? __builtin_amdgcn_update_dpp(0, u, 0x128, 0xf, 0xf, false)
+                      : k == 1 ? __builtin_amdgcn_update_dpp(0, u, 0x124, 0xf, 0xf, false)
+                      : k == 2 ? __builtin_amdgcn_update_dpp(0, u, 0x122, 0xf, 0xf, false)
+                               : __builtin_amdgcn_update_dpp(0, u, 0x121, 0xf, 0xf, false);
+        x += __uint_as_float(static_cast<uint32_t>(v));
+    }
     return sum_q(x);
 }
 
@@ -831,6 +885,8 @@ __device__ __forceinline__ void grad_pass(const Scan& L, int32_t slot, int32_t b
     auto load_head = [&](int k, int buf) {
         fetch_rows<TA, CT, WAVES>(lds.xy + buf * 2 * Lds::A_BYTES, L.x.p + w.lo * L.x.ld + (h0 + k) * TA::RB, static_cast<uint32_t>(L.x.ld), n, wave, lane);
         fetch_rows<TA, CT, WAVES>(lds.xy + (buf * 2 + 1) * Lds::A_BYTES, L.dy.p + w.lo * L.dy.ld + (h0 + k) * TA::RB, static_cast<uint32_t>(L.dy.ld), n, wave, lane);
+        if (wave < Lds::CARD)
+            transfer16(make_rsrc_u(L.cards + (units + k) * sizeof(Card<CT>), sizeof(Card<CT>)), wave * 1024 + lane * 16, lds.card[buf] + wave * 1024);
     };
     // row 16 wave + l16 of the states, d_v along the contraction: of tile `wave` of 16 rows, as the state pass leaves it
     auto state_of = [&](int st, int k) { return L.chunk_states[st] + (units + k) * (DK * DV) + 16 * DV * wave; };
@@ -851,24 +907,9 @@ __device__ __forceinline__ void grad_pass(const Scan& L, int32_t slot, int32_t b
             else X[i] = *reinterpret_cast<const f32x4*>(reinterpret_cast<const uint8_t*>(state_of(st, k)) + tile_at(i));
     };
     const int ts = t - WAVES * 64;                   // the second kind's lanes
-    struct Row {
-        double dsum;
-        float del, ssum;
-    };
-    auto load_row = [&](int k) {
-        const int64_t at = (units + k) * CT + ts;
-        return Row{L.t_dsum[at], L.t_del[at], L.t_ssum[at]};
-    };
-    auto put_row = [&](int buf, const Row& r) {
-        lds.dsum[buf][ts] = r.dsum;
-        lds.del[buf][ts] = r.del;
-        lds.ssum[buf][ts] = r.ssum;
-    };
-    static_assert(WAVES * 64 >= CT, "a lane per token");
     if (scores) {
         fetch_rows<TC, CT, WAVES>(lds.C, L.C.p + w.lo * L.C.ld + g * TC::RB, static_cast<uint32_t>(L.C.ld), n, wave, lane);
         load_head(0, 0);
-        if (ts < CT) put_row(0, load_row(0));
     } else {
         fetch_rows<TC, CT, WAVES>(lds.B, L.B.p + w.lo * L.B.ld + g * TC::RB, static_cast<uint32_t>(L.B.ld), n, wave, lane);
     }
@@ -950,15 +991,10 @@ __device__ __forceinline__ void grad_pass(const Scan& L, int32_t slot, int32_t b
             const Place a = place();
             const int q = a.q, l16 = a.l16;
             const uint8_t *x = lds.xy + buf * 2 * Lds::A_BYTES, *dy = x + Lds::A_BYTES;
-            const double* dsum = lds.dsum[buf];
-            const float* del = lds.del[buf];
+            const Card<CT>& card = *reinterpret_cast<const Card<CT>*>(lds.card[buf]);
+            const double* dsum = card.dsum;
             const Decay decay(L.A[h0 + k]);
-            const bool more = k + 1 < heads;
-            Row next{};
-            if (more) {
-                load_head(k + 1, buf ^ 1);
-                if (ts < CT) next = load_row(k + 1);
-            }
+            if (k + 1 < heads) load_head(k + 1, buf ^ 1);          // (all have left the last head's)
             // rows 16 rt + 4 q + r, column 16 out + l16; direction 0: rows j, column i, direction 1: rows i, column j
             float zA = 0.f, zb = 0.f, dD = 0.f;
 #pragma unroll
@@ -969,26 +1005,57 @@ __device__ __forceinline__ void grad_pass(const Scan& L, int32_t slot, int32_t b
                 Lds::group(dir, grp - dir * Lds::GROUPS, out, tg);
                 const int col = 16 * out + l16;
                 const double dcol = dsum[col];
-                const float dc = del[col];
+                const float dc = card.del[col], scol = card.ssum[col];
                 float sum = 0.f, diag = 0.f;
 #pragma unroll
                 for (int hh = 0; hh < TILES; ++hh) {
                     const int rt = TILES * tg + hh, row = 16 * rt + 4 * q;
+                    if (dir ? rt < out : rt > out) continue;       // (a group's tile on the diagonal's far side)
                     const f32x4 X = dots(a, dir ? dy : x, dir ? x : dy, rt, out, std::false_type{}, zero4());
-                    if (dir == 0) {
-                        const f32x4 dr = lds_get<f32x4>(del, 4 * row), ss = lds_get<f32x4>(lds.ssum[buf], 4 * row);
-                        const float scol = lds.ssum[buf][col];
+                    const f32x4 cb = CB[i][hh];
+                    if (rt != out) {
+                        // the decay by way of the border of the earlier tile: a factor of the row, one of the column
+                        const double border = dsum[16 * (dir ? rt : rt + 1) - 1];
+                        const float d = static_cast<float>(dir ? border - dcol : dcol - border), f = decay(d);
+                        float part = 0.f;
+                        if (dir == 0) {
+                            const f32x4 we = lds_get<f32x4>(card.w_end, 4 * row), de = lds_get<f32x4>(card.d_end, 4 * row),
+                                        se = lds_get<f32x4>(card.s_end, 4 * row);
+#pragma unroll
+                            for (int r = 0; r < 4; ++r) {
+                                const float v = X[r] * f * we[r], z = v * cb[r];
+                                P[i][hh][r] += v;
+                                part += z;
+                                zA = __builtin_fmaf(z, de[r], zA);
+                                zb = __builtin_fmaf(z, se[r], zb);
+                            }
+                            zA = __builtin_fmaf(part, d, zA);
+                            zb = __builtin_fmaf(part, scol - card.ssum[16 * rt + 15], zb);
+                            sum += part;
+                        } else {
+                            const f32x4 ws = lds_get<f32x4>(card.w_start, 4 * row);
+                            const float fd = f * dc;
+#pragma unroll
+                            for (int r = 0; r < 4; ++r) {
+                                const float v = X[r] * ws[r];
+                                P[i][hh][r] = __builtin_fmaf(v, fd, P[i][hh][r]);
+                                part = __builtin_fmaf(v, cb[r], part);
+                            }
+                            sum = __builtin_fmaf(part, f, sum);
+                        }
+                    } else if (dir == 0) {
+                        const f32x4 dr = lds_get<f32x4>(card.del, 4 * row), ss = lds_get<f32x4>(card.ssum, 4 * row);
 #pragma unroll
                         for (int r = 0; r < 4; ++r) {
                             const int j = row + r;
-                            const float d = static_cast<float>(dcol - dsum[j]), e = j <= col ? decay(d) * X[r] : 0.f, y = e * CB[i][hh][r];
+                            const float d = static_cast<float>(dcol - dsum[j]), e = j <= col ? decay(d) * X[r] : 0.f, y = e * cb[r];
                             const float z = j < col ? y * dr[r] : 0.f;
                             P[i][hh][r] = __builtin_fmaf(e, dr[r], P[i][hh][r]);
                             sum += z;
                             zA = __builtin_fmaf(z, d, zA);
                             zb = __builtin_fmaf(z, scol - ss[r], zb);
                             if (j == col) {
-                                diag += y;
+                                diag = y;
                                 dD += X[r];
                             }
                         }
@@ -998,7 +1065,7 @@ __device__ __forceinline__ void grad_pass(const Scan& L, int32_t slot, int32_t b
                             const int j = row + r;
                             const float e = j >= col ? decay(static_cast<float>(dsum[j] - dcol)) * X[r] : 0.f;
                             P[i][hh][r] = __builtin_fmaf(e, dc, P[i][hh][r]);
-                            sum += j > col ? e * CB[i][hh][r] : 0.f;
+                            sum += j > col ? e * cb[r] : 0.f;
                         }
                     }
                 }
@@ -1017,14 +1084,13 @@ __device__ __forceinline__ void grad_pass(const Scan& L, int32_t slot, int32_t b
                 lds.sums[1][wave] = zb;
                 lds.sums[2][wave] = dD;
             }
-            if (more && ts < CT) put_row(buf ^ 1, next);           // (all have left the last head's)
             __builtin_amdgcn_s_waitcnt(vmcnt_imm(0));
             lds_barrier();                           // the sums and the next head's rows are there
             if (ts < 4) {
                 float sum = 0.f;
 #pragma unroll
                 for (int v = 0; v < WAVES; ++v) sum += lds.sums[ts][v];
-                if (ts == 3) sum = static_cast<float>(sum * exp2(dsum[CT - 1] * decay.A2));
+                if (ts == 3) sum = -(sum * card.over[0] + sum * card.over[1]);
                 (ts == 0 ? L.zA : ts == 1 ? L.zb : ts == 2 ? L.dDp : L.thr)[units + k] = sum;
             }
             lds_barrier();                           // the sums have been read
@@ -1071,9 +1137,7 @@ __device__ __forceinline__ void grad_pass(const Scan& L, int32_t slot, int32_t b
         const Place a = place();
         const int q = a.q, l16 = a.l16;
         const uint8_t *x = lds.xy + buf * 2 * Lds::A_BYTES, *dy = x + Lds::A_BYTES;
-        const double* dsum = lds.dsum[buf];
-        const float* del = lds.del[buf];
-        const Decay decay(L.A[h0 + k]);
+        const Card<CT>& card = *reinterpret_cast<const Card<CT>*>(lds.card[buf]);
         f32x4 S[NS], G[NS];
         if constexpr (Lds::AHEAD) {                  // the states are there; wave 0's four stores behind them may be under way
             if (wave == 0 && k > 0) __builtin_amdgcn_s_waitcnt(vmcnt_imm(4));
@@ -1097,7 +1161,6 @@ __device__ __forceinline__ void grad_pass(const Scan& L, int32_t slot, int32_t b
             for (int r = 0; r < 4; ++r) thr = __builtin_fmaf(S[i][r], G[i][r], thr);
         thr = sum_wave(thr);
         if (lane == 0) lds.sums[3][wave] = thr;
-        const double all = dsum[CT - 1];
         auto state_part = [&](const f32x4 (&X)[NS], const uint8_t* rows, auto back) {
             constexpr bool BACK = decltype(back)::value;
             u32x4 hi[BF ? KV : 1], mid[BF ? KV : 1], lo[BF ? KV : 1];
@@ -1134,10 +1197,9 @@ __device__ __forceinline__ void grad_pass(const Scan& L, int32_t slot, int32_t b
                         for (int r = 0; r < 4; ++r) O = mfma_f32(X[i][r], v[r], O);
                     }
                 }
-                const double di = dsum[16 * it + l16];
-                O *= decay(static_cast<float>(BACK ? all - di : di));
+                O *= (BACK ? card.after : card.before)[16 * it + l16];
                 const f32x4 o = own(a, BACK ? lds.B : lds.C, it);
-                if constexpr (BACK) dB[it] += O * del[16 * it + l16];
+                if constexpr (BACK) dB[it] += O * card.del[16 * it + l16];
                 else dC[it] += O;
                 const float s = sum_q(__builtin_fmaf(o[3], O[3], __builtin_fmaf(o[2], O[2], __builtin_fmaf(o[1], O[1], o[0] * O[0]))));
                 if (q == 0) lds.red[(BACK ? Lds::R : Lds::P) + wave][16 * it + l16] = s;
@@ -1160,7 +1222,7 @@ __device__ __forceinline__ void grad_pass(const Scan& L, int32_t slot, int32_t b
                 if (Lds::near(1, tile, tg)) cols += lds.red[Lds::COLS + tg][t];
             }
             const int64_t at = (h0 + k) * L.total + w.lo + t;
-            L.zz[at] = rows - del[t] * cols;
+            L.zz[at] = rows - card.del[t] * cols;
             L.xz[at] = cols + lds.red[Lds::DIAG][t];
             L.pp[at] = p;
             L.xr[at] = r;
@@ -1235,10 +1297,10 @@ __global__ void __launch_bounds__(DK * 8, DK / 32) grad_kernel(Scan L) {
 
 // ---------------------------------------------------------------- ddt, dA, dbias; sums over blocks and chunks
 
-// One wave per (chunk, head), lane l with the tokens l and 64 + l.
-template <int DT, int CT>
+// One wave per (chunk, head), a token a lane.
+template <int DT>
 __global__ void __launch_bounds__(256) decay_grad_kernel(Scan L) {
-    constexpr int NB = (CT + 63) / 64;
+    constexpr int CT = CHUNK<DT>;
     const int64_t u = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6);
     const int lane = threadIdx.x & 63;
     if (u >= static_cast<int64_t>(L.c_slots) * L.H) return;
@@ -1249,44 +1311,27 @@ __global__ void __launch_bounds__(256) decay_grad_kernel(Scan L) {
         return;
     }
     const double A = static_cast<double>(L.A[h]), thr = static_cast<double>(L.thr[u]);
-    const float bias = L.bias ? L.bias[h] : 0.f;
-    const int n = static_cast<int>(w.hi - w.lo);
-    const int64_t row = h * L.total + w.lo;
-    double x[NB], zp[NB], p[NB], r[NB], slope[NB], zs[NB], rs[NB], ds[NB], ss[NB];
-    double z_all = 0.0, r_all = 0.0;
-#pragma unroll
-    for (int b = 0; b < NB; ++b) {
-        const int i = 64 * b + lane;
-        x[b] = zp[b] = p[b] = r[b] = slope[b] = ds[b] = ss[b] = 0.0;
-        if (i < n) {
-            const Strength s = strength(load_as_f32<DT>(L.dt.p + (w.lo + i) * L.dt.ld, h), bias);
-            const float later = L.xr[row + i];
-            x[b] = static_cast<double>(L.xz[row + i]) + later;
-            p[b] = static_cast<double>(L.pp[row + i]);
-            zp[b] = static_cast<double>(L.zz[row + i]) + p[b];
-            r[b] = static_cast<double>(s.delta) * later;
-            slope[b] = static_cast<double>(s.slope);
-            ds[b] = L.t_dsum[u * CT + i];
-            ss[b] = static_cast<double>(L.t_ssum[u * CT + i]);
-        }
-        zs[b] = z_all + prefix_sum(zp[b]);
-        rs[b] = r_all + prefix_sum(r[b]);
-        z_all = lane_value(zs[b], 63);
-        r_all = lane_value(rs[b], 63);
+    const Card<CT>& card = reinterpret_cast<const Card<CT>*>(L.cards)[u];
+    const int64_t at = h * L.total + w.lo + lane;
+    const bool live = lane < w.hi - w.lo;
+    double x = 0.0, zp = 0.0, p = 0.0, r = 0.0, slope = 0.0, ds = 0.0, ss = 0.0;
+    if (live) {
+        const Strength s = strength(load_as_f32<DT>(L.dt.p + (w.lo + lane) * L.dt.ld, h), L.bias ? L.bias[h] : 0.f);
+        const float later = L.xr[at];
+        x = static_cast<double>(L.xz[at]) + later;
+        p = static_cast<double>(L.pp[at]);
+        zp = static_cast<double>(L.zz[at]) + p;
+        r = static_cast<double>(s.delta) * later;
+        slope = static_cast<double>(s.slope);
+        ds = card.dsum[lane];
+        ss = static_cast<double>(card.ssum[lane]);
     }
-    const double d_all = L.t_dsum[u * CT + CT - 1], s_all = static_cast<double>(L.t_ssum[u * CT + CT - 1]);
-    double dA = 0.0, db = 0.0, own = 0.0;            // a lane's part of sum delta dg, sum slope dg, sum slope x . u
-#pragma unroll
-    for (int b = 0; b < NB; ++b) {
-        const int i = 64 * b + lane;
-        const double dg = thr + (z_all - zs[b] + zp[b]) + (rs[b] - r[b]);
-        if (i < n) {
-            store_from_f32<DT>(L.ddt.p + (w.lo + i) * L.ddt.ld, h, static_cast<float>((x[b] + A * dg) * slope[b]));
-            dA += p[b] * ds[b] + r[b] * (d_all - ds[b]);
-            db += p[b] * ss[b] + r[b] * (s_all - ss[b]);
-            own += slope[b] * x[b];
-        }
-    }
+    const double zs = prefix_sum(zp), rs = prefix_sum(r);
+    const double d_all = card.dsum[CT - 1], s_all = static_cast<double>(card.ssum[CT - 1]);
+    const double dg = thr + (lane_value(zs, 63) - zs + zp) + (rs - r);
+    // a lane's part of sum delta dg, sum slope dg, sum slope x . u
+    double dA = p * ds + r * (d_all - ds), db = p * ss + r * (s_all - ss), own = slope * x;
+    if (live) store_from_f32<DT>(L.ddt.p + (w.lo + lane) * L.ddt.ld, h, static_cast<float>((x + A * dg) * slope));
     if (lane == 0) {
         dA += static_cast<double>(L.zA[u]) + thr * d_all;
         db += static_cast<double>(L.zb[u]) + thr * s_all;
@@ -1357,13 +1402,6 @@ auto by_sizes(int32_t dk, int32_t dv, F go) {
     if (dk == 128) return dv == 128 ? go(Int<128>{}, Int<128>{}) : go(Int<128>{}, Int<64>{});
     return dv == 128 ? go(Int<64>{}, Int<128>{}) : go(Int<64>{}, Int<64>{});
 }
-int32_t chunk_tokens(int32_t in_dtype, int32_t dk, int32_t dv) {
-    return by_sizes(dk, dv, [&](auto k, auto v) {
-        constexpr int DK = decltype(k)::value, DV = decltype(v)::value;
-        return in_dtype == KDA_BF16 ? grad_tokens<KDA_BF16, DK, DV>() : grad_tokens<KDA_F32, DK, DV>();
-    });
-}
-
 // Tokens per segment, a multiple of 128, for `units` (sequence, head block) pairs.
 int32_t forward_segment(int64_t units, int32_t n_seqs, int64_t total, int32_t in_dtype, bool packed) {
     const int64_t longest = packed ? total : total / n_seqs, blocks = units / n_seqs;
@@ -1411,8 +1449,8 @@ void set_segments(Scan& L, int32_t (*rule)(int64_t, int32_t, int64_t, int32_t, b
     L.n_seg = L.slots / L.n_seqs;
 }
 // Chunks of the gradients and blocks of heads: as few as leave every CU a workgroup.
-void set_chunks(Scan& L, int32_t dk, int32_t dv, int32_t in_dtype, bool packed) {
-    L.ct = chunk_tokens(in_dtype, dk, dv);
+void set_chunks(Scan& L, int32_t in_dtype, bool packed) {
+    L.ct = in_dtype == KDA_BF16 ? CHUNK<KDA_BF16> : CHUNK<KDA_F32>;
     L.c_slots = static_cast<int32_t>(segment_slots(L.n_seqs, L.total, L.ct, packed));
     L.c_per_seq = L.c_slots / L.n_seqs;
     L.heads = L.H / L.G;
@@ -1434,8 +1472,7 @@ void carve_backward(Scan& L, Carver& ws, int32_t dk, int32_t dv) {
     for (float*& p : L.chunk_states) p = ws.take<float>(cu * dk * dv);
     if (L.blocks > 1)
         for (float*& p : L.part) p = ws.take<float>(L.total * L.G * dk * L.blocks);
-    L.t_dsum = ws.take<double>(cu * L.ct);
-    for (float** p : {&L.t_del, &L.t_ssum}) *p = ws.take<float>(cu * L.ct);
+    L.cards = ws.take<uint8_t>(cu * (L.ct == CHUNK<KDA_BF16> ? sizeof(Card<CHUNK<KDA_BF16>>) : sizeof(Card<CHUNK<KDA_F32>>)));
     for (float** p : {&L.zz, &L.pp, &L.xz, &L.xr}) *p = ws.take<float>(L.H * L.total);
     for (float** p : {&L.zA, &L.zb, &L.dDp, &L.thr, &L.dAp, &L.dbp}) *p = ws.take<float>(cu);
 }
@@ -1517,7 +1554,7 @@ hipError_t backward(const ScanArgs& a, hipStream_t stream) {
     auto out = [&](const RowsOut& r) { return Out{static_cast<uint8_t*>(r.p), r.ld * es}; };
     const bool packed = a.cu != nullptr;
     Scan L = base(a);
-    set_chunks(L, a.dk, a.dv, a.in_dtype, packed);
+    set_chunks(L, a.in_dtype, packed);
     set_segments(L, state_segment, a.dv, a.in_dtype, packed);
     Carver ws{static_cast<uint8_t*>(a.workspace)};
     carve_backward(L, ws, a.dk, a.dv);
@@ -1525,8 +1562,16 @@ hipError_t backward(const ScanArgs& a, hipStream_t stream) {
     L.exact[S_STATE] = L.exact[G_STATE] = 1;
     L.ddt = out(a.ddt);
     L.dA = a.dA; L.dD = a.dD; L.dbias = a.dbias;
+    // the decays, chunk by chunk
+    Scan K = L;
+    K.seg = L.ct;
+    K.slots = L.c_slots;
+    K.n_seg = L.c_per_seq;
+    const unsigned waves = static_cast<unsigned>((int64_t(L.c_slots) * L.H + 3) / 4);
+    hipLaunchKernelGGL((card_kernel<DT>), dim3(waves), dim3(256), 0, stream, K);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
     // the states of every chunk
-    hipError_t e = hipSuccess;
     if (L.seg < WHOLE) e = launch_segments<DT>(L, a.dk, a.dv, 2, stream);
     if (e == hipSuccess) e = launch_states<DT, true>(L, a.dk, a.dv, 2, stream);
     if (e != hipSuccess) return e;
@@ -1537,32 +1582,25 @@ hipError_t backward(const ScanArgs& a, hipStream_t stream) {
     e = launch_value<DT, DT, DX>(X, a.dk, a.dv, stream);
     if (e != hipSuccess) return e;
     // the other gradients, chunk by chunk
-    L.seg = L.ct;
-    L.slots = L.c_slots;
-    L.n_seg = L.c_per_seq;
-    L.out[S_STATE] = out(a.dC);
-    L.out[G_STATE] = out(a.dB);
-    const unsigned waves = static_cast<unsigned>((int64_t(L.c_slots) * L.H + 3) / 4);
+    K.out[S_STATE] = out(a.dC);
+    K.out[G_STATE] = out(a.dB);
     e = by_sizes(a.dk, a.dv, [&](auto k, auto v) {
-        constexpr int DK = decltype(k)::value, DV = decltype(v)::value, CT = grad_tokens<DT, DK, DV>();
-        hipLaunchKernelGGL((table_kernel<DT, CT>), dim3(waves), dim3(256), 0, stream, L);
-        hipError_t r = hipGetLastError();
-        if (r != hipSuccess) return r;
-        hipLaunchKernelGGL((grad_kernel<DT, DK, DV>), dim3(xcd_grid(int64_t(L.slots) * L.blocks * L.G, 1)), dim3(DK * 8), 0, stream, L);
-        r = hipGetLastError();
-        if (r != hipSuccess) return r;
-        hipLaunchKernelGGL((decay_grad_kernel<DT, CT>), dim3(waves), dim3(256), 0, stream, L);
+        constexpr int DK = decltype(k)::value, DV = decltype(v)::value;
+        hipLaunchKernelGGL((grad_kernel<DT, DK, DV>), dim3(xcd_grid(int64_t(K.slots) * K.blocks * K.G, 1)), dim3(DK * 8), 0, stream, K);
         return hipGetLastError();
     });
     if (e != hipSuccess) return e;
+    hipLaunchKernelGGL((decay_grad_kernel<DT>), dim3(waves), dim3(256), 0, stream, K);
+    e = hipGetLastError();
+    if (e != hipSuccess) return e;
     if (L.blocks > 1 && L.total > 0) {
         const int32_t row = a.G * a.dk;
-        const int64_t quads = L.total * row / 4;
-        hipLaunchKernelGGL(part_sum_kernel<DT>, dim3(static_cast<unsigned>((quads + 255) / 256), 2), dim3(256), 0, stream, L, row, quads);
+        const int64_t quads = K.total * row / 4;
+        hipLaunchKernelGGL(part_sum_kernel<DT>, dim3(static_cast<unsigned>((quads + 255) / 256), 2), dim3(256), 0, stream, K, row, quads);
         e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
-    hipLaunchKernelGGL(head_sum_kernel, dim3(L.H), dim3(256), 0, stream, L);
+    hipLaunchKernelGGL(head_sum_kernel, dim3(K.H), dim3(256), 0, stream, K);
     return hipGetLastError();
 }
 
@@ -1577,7 +1615,7 @@ size_t scan_workspace_bytes(int32_t n_seqs, int64_t total, int32_t H, int32_t G,
         L.n_seqs = n_seqs; L.total = total; L.H = H; L.G = G;
         Carver ws{nullptr};
         if (backward) {
-            set_chunks(L, dk, dv, in_dtype, packed);
+            set_chunks(L, in_dtype, packed);
             set_segments(L, state_segment, dv, in_dtype, packed);
             carve_backward(L, ws, dk, dv);
         } else {
