@@ -235,6 +235,7 @@ __device__ __forceinline__ void value_pass(const Scan& L, int32_t slot, int32_t 
     const int64_t len = w.hi - w.lo;
     const int n_chunks = static_cast<int>((len + TOK - 1) / TOK);
     const int64_t unit = static_cast<int64_t>(w.n) * L.H + h, seg_unit = static_cast<int64_t>(slot) * L.H + h;
+    auto state = [&](auto* all, int64_t u) { return all + u * (DK * DV); };
 
     const In &ra = BACK ? L.B : L.C, &rb = BACK ? L.C : L.B, &rc = BACK ? L.dy : L.x;
     auto chunk_at = [&](int c) { return static_cast<int64_t>(BACK ? n_chunks - 1 - c : c) * TOK; };
@@ -245,14 +246,41 @@ __device__ __forceinline__ void value_pass(const Scan& L, int32_t slot, int32_t 
     };
     auto load_b = [&](int c) {
         const int64_t off = chunk_at(c);
-        fetch_rows<TA, TOK, WAVES>(lds.b + (STATE ? c & 1 : 0) * Lds::B_BYTES, rb.p + (w.lo + off) * rb.ld + g * TA::RB, static_cast<uint32_t>(rb.ld), chunk_n(off), wave, lane);
+        fetch_rows<TA, TOK, WAVES>(lds.b, rb.p + (w.lo + off) * rb.ld + g * TA::RB, static_cast<uint32_t>(rb.ld), chunk_n(off), wave, lane);
     };
     auto load_c = [&](int c) {
         const int64_t off = chunk_at(c);
 #pragma unroll
         for (int i = 0; i < HB; ++i)
-            fetch_rows<TC, TOK, WAVES>(lds.c + ((STATE ? c & 1 : 0) * HB + i) * Lds::C_BYTES, rc.p + (w.lo + off) * rc.ld + (h0 + i) * TC::RB,
+            fetch_rows<TC, TOK, WAVES>(lds.c + i * Lds::C_BYTES, rc.p + (w.lo + off) * rc.ld + (h0 + i) * TC::RB,
                                        static_cast<uint32_t>(rc.ld), h0 + i < h_end ? chunk_n(off) : 0, wave, lane);
+    };
+    // STATE: rows come by way of registers (a transfer to LDS under way would be waited for at the next transposing read)
+    constexpr int NB = TOK / TA::R / WAVES, NC = TOK / TC::R / WAVES;
+    struct Rows {
+        u32x4 b[STATE ? NB : 1], c[STATE ? NC : 1];
+    };
+    auto take = [&](auto tile, u32x4* to, const In& from, int64_t unit_bytes, int c) {
+        using TT = decltype(tile);
+        const int64_t off = chunk_at(c);
+        const uint32_t ld = static_cast<uint32_t>(from.ld);
+        const __amdgpu_buffer_rsrc_t r = make_rsrc_u(from.p + (w.lo + off) * from.ld + unit_bytes, (chunk_n(off) - 1) * ld + TT::RB);
+        int ln = lane;
+        asm volatile("" : "+v"(ln));
+        const int r0 = wave * TT::R + ln / TT::UPR, un = ln % TT::UPR;
+        const uint32_t at = r0 * ld + ((un & ~7) | ((un & 7) ^ TT::mix(r0))) * 16;
+#pragma unroll
+        for (int i = 0; i < TOK / TT::R / WAVES; ++i) to[i] = __builtin_amdgcn_raw_buffer_load_b128(r, at + WAVES * i * TT::R * ld, 0, 0);
+    };
+    auto take_rows = [&](Rows& x, int c) {
+        take(TA{}, x.b, rb, g * TA::RB, c);
+        take(TC{}, x.c, rc, h0 * TC::RB, c);
+    };
+    auto put_rows = [&](const Rows& x, int c) {
+#pragma unroll
+        for (int i = 0; i < NB; ++i) lds_put(lds.b + (STATE ? c & 1 : 0) * Lds::B_BYTES, TA::PIECE * (WAVES * i + wave) + lane * 16, x.b[i]);
+#pragma unroll
+        for (int i = 0; i < NC; ++i) lds_put(lds.c + (STATE ? c & 1 : 0) * Lds::C_BYTES, TC::PIECE * (WAVES * i + wave) + lane * 16, x.c[i]);
     };
     // the wave that makes a head's decays
     const int table = wave - (WAVES - HB);
@@ -314,10 +342,16 @@ __device__ __forceinline__ void value_pass(const Scan& L, int32_t slot, int32_t 
         }
     };
 
+    Rows even{}, odd{};                              // rows under way: of the next chunk and of the one after it
     if (n_chunks > 0) {
-        load_b(0);
-        if constexpr (!STATE) load_a(0);
-        load_c(0);
+        if constexpr (STATE) {
+            take_rows(even, 0);
+            if (n_chunks > 1) take_rows(odd, 1);
+        } else {
+            load_b(0);
+            load_a(0);
+            load_c(0);
+        }
         if (table >= 0) decays(0, ahead_of(0));
     }
     Ahead ahead{};
@@ -369,8 +403,8 @@ __device__ __forceinline__ void value_pass(const Scan& L, int32_t slot, int32_t 
         }
     };
     if constexpr (OWN) load_state(nullptr, false);
-    else if constexpr (MODE == DX) load_state(L.chunk_states[ST] + chunk_unit(len - 1, h) * (DK * DV), true);
-    else load_state(w.n_seg > 1 ? L.seg_states[ST] + seg_unit * (DK * DV) : L.m_in[ST] ? L.m_in[ST] + unit * (DK * DV) : nullptr, false);
+    else if constexpr (MODE == DX) load_state(state(L.chunk_states[ST], chunk_unit(len - 1, h)), true);
+    else load_state(w.n_seg > 1 ? state(L.seg_states[ST], seg_unit) : L.m_in[ST] ? state(L.m_in[ST], unit) : nullptr, false);
 
     // ---- operands' byte offsets, as in linear attention's pass.  16 bits, along the channels: channels
     // 32 kk + 8 q .. + 7 of token 16 it + l16; along the tokens: tokens 32 tg + 4 q .. + 3 and 32 tg + 16 + 4 q .. + 3,
@@ -406,20 +440,17 @@ __device__ __forceinline__ void value_pass(const Scan& L, int32_t slot, int32_t 
     };
     const float D = (MODE == Y || MODE == DX) && L.D ? L.D[h] : 0.f;
     const bool exact = STATE ? L.exact[ST] != 0 : MODE == Y && L.m_out[ST] && w.s == w.n_seg - 1;
-    bool stored = false;
-    for (int c = 0; c < n_chunks; ++c) {
+    if constexpr (STATE)
+        if (n_chunks > 0) put_rows(even, 0);
+    auto chunk = [&](int c, Rows& far, const Rows& near) __attribute__((always_inline)) {
         const int64_t off = chunk_at(c), tok0 = w.lo + off;
         const int n = chunk_n(off), buf = c & 1;
         const uint8_t* const lds_b = lds.b + (STATE ? buf : 0) * Lds::B_BYTES;
         uint8_t* const lds_c = lds.c + ((STATE ? buf : 0) * HB + hb) * Lds::C_BYTES;
-        // The rows are there; a chunk's state, stored behind their transfer, may still be under way.
-        if (CHUNKS && stored) __builtin_amdgcn_s_waitcnt(vmcnt_imm(MT));
-        else __builtin_amdgcn_s_waitcnt(vmcnt_imm(0));
+        if constexpr (!STATE) __builtin_amdgcn_s_waitcnt(vmcnt_imm(0));
         lds_barrier();                               // the tiles and the decays are there
-        if (STATE && c + 1 < n_chunks) {             // (all have left the tiles before them)
-            load_b(c + 1);
-            load_c(c + 1);
-        }
+        if constexpr (STATE)
+            if (c + 2 < n_chunks) take_rows(far, c + 2);
         const Ahead next = ahead;
         if (table >= 0 && c + 2 < n_chunks) ahead = ahead_of(c + 2);
         const double* cum = lds.cum[buf][hb];
@@ -427,11 +458,7 @@ __device__ __forceinline__ void value_pass(const Scan& L, int32_t slot, int32_t 
 
         f32x4 O[IT];
         if constexpr (CHUNKS) {
-            stored = live;
-            if (stored) {
-                __builtin_amdgcn_sched_barrier(0);   // (behind the transfers: see the wait)
-                store_state(L.chunk_states[ST] + chunk_unit(off, h) * (DK * DV), chunk_sign(c), true);
-            }
+            if (live) store_state(state(L.chunk_states[ST], chunk_unit(off, h)), chunk_sign(c), true);
         }
         if constexpr (!STATE) {
             if (table >= 0 && lane < TOK) {          // the update's weights, read behind the next barrier
@@ -605,15 +632,27 @@ __device__ __forceinline__ void value_pass(const Scan& L, int32_t slot, int32_t 
                         cm[e] = y;
                         cl[e] = z;
                     }
+                    auto add = [&](int mt, const u32x4& kt, const u32x4& cw) {
+                        M[mt] = STATE ? mfma_bf16(cw, kt, M[mt]) : mfma_bf16(kt, cw, M[mt]);
+                    };
+                    constexpr int NM = STATE ? MT : 1;             // tiles at a time: products that do not wait for each other
 #pragma unroll
-                    for (int mt = 0; mt < MT; ++mt) {
-                        const uint32_t at = STATE ? (tok_b ^ (32 * (mt & 3))) + (mt >> 2) * 128
-                                                  : tok[(mt >> 1) & 1] + (mt >> 2) * 128 + 8 * (mt & 1);
-                        const u32x4 kt = tokens(at + 2 * tg * TA::ROWS16, lds_b, TA::ROWS16);
-                        auto add = [&](const u32x4& cw) { M[mt] = STATE ? mfma_bf16(cw, kt, M[mt]) : mfma_bf16(kt, cw, M[mt]); };
-                        if constexpr (THREE) add(cl);
-                        add(cm);
-                        add(ch);
+                    for (int m0 = 0; m0 < MT; m0 += NM) {
+                        u32x4 kt[NM];
+#pragma unroll
+                        for (int m = 0; m < NM; ++m) {
+                            const int mt = m0 + m;
+                            const uint32_t at = STATE ? (tok_b ^ (32 * (mt & 3))) + (mt >> 2) * 128
+                                                      : tok[(mt >> 1) & 1] + (mt >> 2) * 128 + 8 * (mt & 1);
+                            kt[m] = tokens(at + 2 * tg * TA::ROWS16, lds_b, TA::ROWS16);
+                        }
+                        if constexpr (THREE)
+#pragma unroll
+                            for (int m = 0; m < NM; ++m) add(m0 + m, kt[m], cl);
+#pragma unroll
+                        for (int m = 0; m < NM; ++m) add(m0 + m, kt[m], cm);
+#pragma unroll
+                        for (int m = 0; m < NM; ++m) add(m0 + m, kt[m], ch);
                     }
                 }
             };
@@ -634,7 +673,10 @@ __device__ __forceinline__ void value_pass(const Scan& L, int32_t slot, int32_t 
                 }
             }
         }
-        if constexpr (STATE) continue;
+        if constexpr (STATE) {
+            if (c + 1 < n_chunks) put_rows(near, c + 1);           // (all have left the tiles before them)
+            return;
+        }
         lds_barrier();                               // the tiles have been read, the output is there
         if (c + 1 < n_chunks) {
             load_b(c + 1);
@@ -658,11 +700,19 @@ __device__ __forceinline__ void value_pass(const Scan& L, int32_t slot, int32_t 
         }
         if constexpr (STAGED) lds_barrier();         // the output has been read
         if (c + 1 < n_chunks) load_c(c + 1);
+    };
+    if constexpr (STATE) {
+        for (int c = 0; c < n_chunks; c += 2) {
+            chunk(c, even, odd);
+            if (c + 1 < n_chunks) chunk(c + 1, odd, even);
+        }
+    } else {
+        for (int c = 0; c < n_chunks; ++c) chunk(c, even, odd);
     }
 
     float* dst = nullptr;
-    if constexpr (OWN) dst = L.seg_states[ST] + seg_unit * (DK * DV);
-    else if (MODE != DX && L.m_out[ST] && w.s == (BACK ? 0 : w.n_seg - 1)) dst = L.m_out[ST] + unit * (DK * DV);
+    if constexpr (OWN) dst = state(L.seg_states[ST], seg_unit);
+    else if (MODE != DX && L.m_out[ST] && w.s == (BACK ? 0 : w.n_seg - 1)) dst = state(L.m_out[ST], unit);
     if (dst && live) store_state(dst, chunk_sign(n_chunks), false);
     if constexpr (OWN) {
         if (table >= 0 && h0 + table < h_end && lane == 0) L.seg_log[ST][static_cast<int64_t>(slot) * L.H + h0 + table] = log_sum;
@@ -686,20 +736,20 @@ __global__ void __launch_bounds__(HB * DV * 4, HB * DV == 128 ? 4 : 2) value_ker
     const uint32_t blocks = static_cast<uint32_t>(L.blocks) * L.G;
     value_pass<DT, ODT, DK, DV, HB, MODE>(L, unit / blocks, unit % blocks, lds);
 }
-// The segments' own contributions to S, or G, or both; or the states of all chunks.
-template <int DT, int DK, int DV, int HB, bool CHUNKS>
-__global__ void __launch_bounds__(HB * DV * 4, HB * DV == 128 ? 4 : 2) state_kernel(Scan L, int32_t passes) {
+// The segments' own contributions to S, or G, or both; or the states of all chunks.  One head a workgroup: with two, for
+// d_v = 64, half the CUs had none, and what they saved in rows of B and C was not missed.
+template <int DT, int DK, int DV, bool CHUNKS>
+__global__ void __launch_bounds__(DV * 4, 2) state_kernel(Scan L, int32_t passes) {
     constexpr int SM = CHUNKS ? S_CHUNKS : S_ONLY, GM = CHUNKS ? G_CHUNKS : G_ONLY;
     __shared__ union {
-        ValueLds<DT, DK, DV, HB, SM> s;
-        ValueLds<DT, DK, DV, HB, GM> g;
+        ValueLds<DT, DK, DV, 1, SM> s;
+        ValueLds<DT, DK, DV, 1, GM> g;
     } lds;
     uint32_t unit;
     int32_t pass;
-    if (!unit_of(static_cast<uint32_t>(L.slots) * L.blocks * L.G, passes, unit, pass)) return;
-    const uint32_t blocks = static_cast<uint32_t>(L.blocks) * L.G;
-    if (pass == S_STATE) value_pass<DT, DT, DK, DV, HB, SM>(L, unit / blocks, unit % blocks, lds.s);
-    else value_pass<DT, DT, DK, DV, HB, GM>(L, unit / blocks, unit % blocks, lds.g);
+    if (!unit_of(static_cast<uint32_t>(L.slots) * L.H, passes, unit, pass)) return;
+    if (pass == S_STATE) value_pass<DT, DT, DK, DV, 1, SM>(L, unit / L.H, unit % L.H, lds.s);
+    else value_pass<DT, DT, DK, DV, 1, GM>(L, unit / L.H, unit % L.H, lds.g);
 }
 
 // Segment states: from each segment's own contribution to the state it starts from (S) or that follows it (G), in
@@ -1508,18 +1558,11 @@ hipError_t launch_value(Scan L, int32_t dk, int32_t dv, hipStream_t stream) {
 }
 template <int DT, bool CHUNKS>
 hipError_t launch_states(Scan L, int32_t dk, int32_t dv, int32_t passes, hipStream_t stream) {
+    L.blocks = L.H / L.G;
     return by_sizes(dk, dv, [&](auto k, auto v) {
-        constexpr int DK = decltype(k)::value, DV = decltype(v)::value;
-        auto go = [&](auto heads) {
-            constexpr int HB = decltype(heads)::value;
-            L.blocks = head_blocks(L.H, L.G, HB);
-            hipLaunchKernelGGL((state_kernel<DT, DK, DV, HB, CHUNKS>), dim3(xcd_grid(int64_t(L.slots) * L.blocks * L.G, passes)),
-                               dim3(HB * DV * 4), 0, stream, L, passes);
-            return hipGetLastError();
-        };
-        if constexpr (DV == 64 && !CHUNKS)
-            if (value_heads(L.H, L.G, dv) == 2) return go(Int<2>{});
-        return go(Int<1>{});
+        hipLaunchKernelGGL((state_kernel<DT, decltype(k)::value, decltype(v)::value, CHUNKS>), dim3(xcd_grid(int64_t(L.slots) * L.H, passes)),
+                           dim3(decltype(v)::value * 4), 0, stream, L, passes);
+        return hipGetLastError();
     });
 }
 // The states that the segments start from (S), or that follow them (G).
