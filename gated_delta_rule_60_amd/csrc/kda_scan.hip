@@ -136,6 +136,27 @@ __device__ __forceinline__ double shuffle(double x, int lane) {
 // 2^x, x <= 0 where A <= 0.
 __device__ __forceinline__ float pow2(double x) { return __builtin_amdgcn_exp2f(static_cast<float>(x)); }
 
+// 2^x to 2^-47, x <= 0: what a state is multiplied by, chunk after chunk, so that errors of 2^-24 would add up.  Taylor's
+// series of e^y for |y| <= ln 2 / 2.  The coefficients are formed where they are used: hoisted out of a loop over the
+// chunks they take 20 registers a lane, which the loops do not have (each then came from scratch memory, behind all loads
+// under way: a third of the forward pass).
+template <typename T>
+__device__ __forceinline__ T here(T c) {
+    asm volatile("" : "+s"(c));
+    return c;
+}
+__device__ __forceinline__ double pow2_wide(double x) {
+    x = x < -1100.0 ? -1100.0 : x;
+    const double n = __builtin_rint(x), y = (x - n) * here(0.69314718055994530942);
+    constexpr double over_factorial[12] = {1.0, 1.0, 1.0 / 2, 1.0 / 6, 1.0 / 24, 1.0 / 120, 1.0 / 720, 1.0 / 5040, 1.0 / 40320,
+                                           1.0 / 362880, 1.0 / 3628800, 1.0 / 39916800};
+    double p = over_factorial[11];
+#pragma unroll
+    for (int k = 10; k >= 0; --k) {
+        p = __builtin_fma(p, y, here(over_factorial[k]));
+    }
+    return __builtin_ldexp(p, static_cast<int>(n));
+}
 // The states in registers change sign from chunk to chunk: chunk k works on (-1)^k S.  The MFMAs' sums lose what they
 // drop towards minus infinity, which over all of a state's elements, against inputs that are positive on average (behind
 // a SiLU), adds up: with the signs, dA of 4096 tokens was off by 6e-6 of itself, the same way in every head.
@@ -330,8 +351,8 @@ __device__ __forceinline__ void value_pass(const Scan& L, int32_t slot, int32_t 
             return;
         }
         const float delta = lane < n ? strength(open_dt<DT>(a.dt), bias).delta : 0.f;
-        const double cum = prefix_sum(static_cast<double>(delta) * (static_cast<double>(A) * LOG2E));
-        const double all = lane_value(cum, TOK - 1), over = -exp2(all);
+        const double cum = prefix_sum(static_cast<double>(delta) * (static_cast<double>(here(__uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(A))))) * here(LOG2E)));
+        const double all = lane_value(cum, TOK - 1), over = -pow2_wide(all);
         const float hi = static_cast<float>(over);
         log_sum += all;
         if (lane < TOK) {
@@ -376,11 +397,14 @@ __device__ __forceinline__ void value_pass(const Scan& L, int32_t slot, int32_t 
             for (int mt = 0; mt < MT; ++mt)
                 __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, sign * M[mt]), rs, at + 64 * DV * mt, 0, 0);
         } else {
+            uint32_t at = (row(0) * DV + col) * 4;
+            asm volatile("" : "+v"(at));             // formed anew, not kept over the loop
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
                 for (int r = 0; r < 4; ++r)
-                    __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(sign * M[mt][r]), rs, ((row(mt) + r) * DV + col) * 4, 0, 0);
+                    __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(sign * M[mt][r]), rs,
+                                                          at + ((BF ? 32 * (mt >> 1) + 4 * (mt & 1) : 16 * mt) + r) * DV * 4, 0, 0);
         }
     };
     auto load_state = [&](const float* src, bool tiles) {          // nullptr: an empty range, which reads as zeros
@@ -821,7 +845,7 @@ __global__ void __launch_bounds__(256) card_kernel(Scan L) {
     c.before[lane] = pow2(A2 * d);
     c.after[lane] = pow2(A2 * (all - d));
     if (lane == 0) {
-        const double over = -exp2(A2 * all);
+        const double over = -pow2_wide(A2 * all);
         const float hi = static_cast<float>(over);
         c.over = f32x2{hi, static_cast<float>(over - static_cast<double>(hi))};
     }
