@@ -52,7 +52,7 @@ struct Scan {
     const float* m_in[2];    // S: initial states; G: gradients of the final states; or nullptr
     float* m_out[2];         // S: final states; G: gradients of the initial states; or nullptr
     float* seg_states[2];    // [slots, H, dk, dv]: a segment's S before its first token, G behind its last one
-    double* seg_log[2];      // [slots, H] log2 of a segment's decay
+    f32x2* seg_decay[2];     // [slots, H] a segment's decay as a sum of two
     float* chunk_states[2];  // [c_slots, H, dk, dv]: S before a chunk, G behind it
     float* part[2];          // [head blocks of a group, tokens, G, dk] dC, dB per block; nullptr: one block
     uint8_t* cards;          // [c_slots, H] Card of a chunk's decays
@@ -739,7 +739,11 @@ __device__ __forceinline__ void value_pass(const Scan& L, int32_t slot, int32_t 
     else if (MODE != DX && L.m_out[ST] && w.s == (BACK ? 0 : w.n_seg - 1)) dst = state(L.m_out[ST], unit);
     if (dst && live) store_state(dst, chunk_sign(n_chunks), false);
     if constexpr (OWN) {
-        if (table >= 0 && h0 + table < h_end && lane == 0) L.seg_log[ST][static_cast<int64_t>(slot) * L.H + h0 + table] = log_sum;
+        if (table >= 0 && h0 + table < h_end && lane == 0) {
+            const double all = pow2_wide(log_sum);
+            const float hi = static_cast<float>(all);
+            L.seg_decay[ST][static_cast<int64_t>(slot) * L.H + h0 + table] = f32x2{hi, static_cast<float>(all - static_cast<double>(hi))};
+        }
     }
 }
 
@@ -777,7 +781,8 @@ __global__ void __launch_bounds__(DV * 4, 2) state_kernel(Scan L, int32_t passes
 }
 
 // Segment states: from each segment's own contribution to the state it starts from (S) or that follows it (G), in
-// place.  Grid (sequence * H + head, element blocks of 1024, pass); eight segments' loads at a time.
+// place.  Grid (sequence * H + head, element blocks of 1024, pass); sixteen segments' loads at a time (eight: 16.4 us for the
+// packed 16455 tokens of 8 heads, five round trips to memory for the longest sequence).
 __global__ void __launch_bounds__(256) scan_kernel(Scan L, int32_t elems) {
     const int ST = blockIdx.z;
     const bool back = ST == G_STATE;
@@ -794,22 +799,21 @@ __global__ void __launch_bounds__(256) scan_kernel(Scan L, int32_t elems) {
     auto slot = [&](int32_t i) { return reinterpret_cast<f32x4*>(L.seg_states[ST] + index(i) * elems + e); };
     f32x4 ahead = *slot(0);                          // read before the batch before it writes its place
     *slot(0) = x;
-    for (int32_t i0 = 0; i0 < n_seg - 1; i0 += 8) {
-        f32x4 own[9];
-        double lg[8];
+    constexpr int AT = 16;
+    for (int32_t i0 = 0; i0 < n_seg - 1; i0 += AT) {
+        f32x4 own[AT + 1];
+        f32x2 decay[AT];
         own[0] = ahead;
 #pragma unroll
-        for (int32_t j = 1; j < 9; ++j) own[j] = i0 + j < n_seg - 1 ? *slot(i0 + j) : zero4();
+        for (int32_t j = 1; j <= AT; ++j) own[j] = i0 + j < n_seg - 1 ? *slot(i0 + j) : zero4();
 #pragma unroll
-        for (int32_t j = 0; j < 8; ++j) lg[j] = i0 + j < n_seg - 1 ? L.seg_log[ST][index(i0 + j)] : 0.0;
-        ahead = own[8];
+        for (int32_t j = 0; j < AT; ++j) decay[j] = L.seg_decay[ST][index(i0 + j < n_seg - 1 ? i0 + j : n_seg - 2)];
+        ahead = own[AT];
 #pragma unroll
-        for (int32_t j = 0; j < 8; ++j) {
+        for (int32_t j = 0; j < AT; ++j) {
             if (i0 + j >= n_seg - 1) break;
-            const double l = exp2(lg[j]);
-            const float l_hi = static_cast<float>(l), l_lo = static_cast<float>(l - static_cast<double>(l_hi));
 #pragma unroll
-            for (int r = 0; r < 4; ++r) x[r] = __builtin_fmaf(x[r], l_hi, __builtin_fmaf(x[r], l_lo, own[j][r]));
+            for (int r = 0; r < 4; ++r) x[r] = __builtin_fmaf(x[r], decay[j][0], __builtin_fmaf(x[r], decay[j][1], own[j][r]));
             *slot(i0 + j + 1) = x;                   // segment i's end is what segment i + 1 starts from
         }
     }
@@ -1491,11 +1495,11 @@ int32_t state_segment(int64_t units, int32_t n_seqs, int64_t total, int32_t in_d
     const int64_t seg = std::max<int64_t>(((longest + shares - 1) / shares + 127) / 128 * 128, 512);
     return seg >= longest || seg >= WHOLE ? WHOLE : static_cast<int32_t>(seg);
 }
-// dx starts from the states of a chunk, so its segments cost a state's read only.
+// dx starts from the states of a chunk, so its segments cost a state's read only: short ones, for four workgroups a CU.
 int32_t dx_segment(int64_t units, int32_t n_seqs, int64_t total, int32_t in_dtype, bool packed) {
     const int64_t longest = packed ? total : total / n_seqs, blocks = units / n_seqs;
     const int64_t shares = packed ? std::max<int64_t>(1, 1024 / blocks) : std::max<int64_t>(1, 1024 / units);
-    const int64_t seg = std::max<int64_t>(((longest + shares - 1) / shares + 127) / 128 * 128, 256);
+    const int64_t seg = std::max<int64_t>(((longest + shares - 1) / shares + 63) / 64 * 64, 64);
     return seg >= longest || seg >= WHOLE ? WHOLE : static_cast<int32_t>(seg);
 }
 
@@ -1536,7 +1540,7 @@ void carve_segments(Scan& L, Carver& ws, int64_t elems, int passes) {
     if (L.seg == WHOLE) return;
     for (int st = 0; st < passes; ++st) {
         L.seg_states[st] = ws.take<float>(int64_t(L.slots) * L.H * elems);
-        L.seg_log[st] = ws.take<double>(int64_t(L.slots) * L.H);
+        L.seg_decay[st] = ws.take<f32x2>(int64_t(L.slots) * L.H);
     }
 }
 void carve_forward(Scan& L, Carver& ws, int64_t elems) { carve_segments(L, ws, elems, 1); }
