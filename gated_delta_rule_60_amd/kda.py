@@ -157,8 +157,16 @@ def _expect(fn: str, name: str, t, shape, dtypes=None):
         return
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{fn}: {name} must be a torch.Tensor")
-    if t.shape == shape and (dtypes is None or t.dtype in dtypes) and t.is_contiguous():
-        return
+    if (dtypes is None or t.dtype in dtypes) and t.is_contiguous():
+        size = t.shape
+        if size == shape:
+            return
+        if len(size) == len(shape):
+            for a, w in zip(size, shape):
+                if w is not None and a != w:
+                    break
+            else:
+                return
     if len(t.shape) != len(shape) or any(w is not None and int(a) != int(w)
                                          for a, w in zip(t.shape, shape)):
         want = tuple("*" if w is None else int(w) for w in shape)
@@ -501,6 +509,11 @@ def _fit(dev, *specs) -> bool:
                                   t.dtype is dtype and t.device == dev and t.is_contiguous()):
             return False
     return dev.type == "cuda"
+
+
+def _size(t, dims: int, d: int):
+    """Size d of a tensor of `dims` dimensions, None for anything else."""
+    return t.shape[d] if isinstance(t, torch.Tensor) and t.dim() == dims else None
 
 
 def _alloc(ts, shape, dtype, dev):
@@ -872,19 +885,23 @@ def kda_conv_step(x, weight, windows, bias=None, slots=None, y=None, silu: bool 
     if x.dim() != 2:
         raise ValueError(f"{fn}: x must be a [N, C] tensor")
     N, C = x.shape
-    ldx = _rows(fn, "x", x, (N, C), dt, 1)
-    _expect(fn, "weight", weight, (C, None), (torch.float32,))
-    W = weight.shape[1]
-    _expect(fn, "windows", windows, (None, W - 1, C), (dt,))
-    _expect(fn, "bias", bias, (C,), (torch.float32,))
-    _expect(fn, "slots", slots, (N,), (torch.int32,))
-    ldy = C if y is None else _rows(fn, "y", y, (N, C), dt, 1)
-    dev = _one_device(fn, x=x, weight=weight, windows=windows, bias=bias, slots=slots, y=y)
+    dev, W, n_slots = x.device, _size(weight, 2, 1), _size(windows, 3, 0)
+    ldx = ldy = C
+    if y is not None or not W or n_slots is None or not _fit(
+            dev, (x, (N, C), dt), (weight, (C, W), torch.float32), (windows, (n_slots, W - 1, C), dt),
+            (bias, (C,), torch.float32), (slots, (N,), torch.int32)):
+        ldx = _rows(fn, "x", x, (N, C), dt, 1)
+        _expect(fn, "weight", weight, (C, None), (torch.float32,))
+        _expect(fn, "windows", windows, (None, W - 1, C), (dt,))
+        _expect(fn, "bias", bias, (C,), (torch.float32,))
+        _expect(fn, "slots", slots, (N,), (torch.int32,))
+        ldy = C if y is None else _rows(fn, "y", y, (N, C), dt, 1)
+        _one_device(fn, x=x, weight=weight, windows=windows, bias=bias, slots=slots, y=y)
     ts, sp = _launch_stream(stream, dev)
     if y is None:
         y = _alloc(ts, (N, C), dt, dev)
     _launch(fn, dev, load_library().kda_conv_step, _addr(x), ldx, _DT[dt], _addr(weight), _addr(bias),
-            _addr(windows), _addr(slots), _addr(y), ldy, N, windows.shape[0], C, W, int(silu), sp)
+            _addr(windows), _addr(slots), _addr(y), ldy, N, n_slots, C, W, int(silu), sp)
     return y
 
 
@@ -995,17 +1012,26 @@ def kda_ssm_decode_step(x, dt, A, B, C, state, D=None, dt_bias=None, slots=None,
     (sequence n in slot n).  Sequences whose slot lies outside the pool, and all but the last with one
     slot, are skipped and get zeros.  Returns y [N, H, dv]."""
     fn = "kda_ssm_decode_step"
-    (N,), H, G, dk, dv, (ldx, lddt, ldb, ldc) = _check_ssm(fn, x, dt, A, B, C, D, dt_bias, 1)
-    _expect(fn, "state", state, (None, H, dk, dv), (torch.float32,))
-    _expect(fn, "slots", slots, (N,), (torch.int32,))
-    ldy = H * dv if y is None else _rows(fn, "y", y, (N, H, dv), _float_dtype(fn, "y", y), 1)
-    dev = _one_device(fn, x=x, dt=dt, A=A, B=B, C=C, state=state, D=D, dt_bias=dt_bias, slots=slots, y=y)
+    n_slots, f32 = _size(state, 4, 0), torch.float32
+    quick = y is None and n_slots is not None and _size(x, 3, 0) is not None and _size(B, 3, 0) is not None
+    if quick:
+        (N, H, dv), (_, G, dk), ty, dev = x.shape, B.shape, x.dtype, x.device
+        quick = ty in _FLOATS and A is not None and dt is not None and C is not None and G > 0 and H % G == 0 and _fit(
+            dev, (x, (N, H, dv), ty), (dt, (N, H), ty), (B, (N, G, dk), ty), (C, (N, G, dk), ty), (A, (H,), f32),
+            (D, (H,), f32), (dt_bias, (H,), f32), (state, (n_slots, H, dk, dv), f32), (slots, (N,), torch.int32))
+        ldx, lddt, ldb, ldc, ldy = H * dv, H, G * dk, G * dk, H * dv
+    if not quick:
+        (N,), H, G, dk, dv, (ldx, lddt, ldb, ldc) = _check_ssm(fn, x, dt, A, B, C, D, dt_bias, 1)
+        _expect(fn, "state", state, (None, H, dk, dv), (f32,))
+        _expect(fn, "slots", slots, (N,), (torch.int32,))
+        ldy = H * dv if y is None else _rows(fn, "y", y, (N, H, dv), _float_dtype(fn, "y", y), 1)
+        dev = _one_device(fn, x=x, dt=dt, A=A, B=B, C=C, state=state, D=D, dt_bias=dt_bias, slots=slots, y=y)
     ts, sp = _launch_stream(stream, dev)
     if y is None:
         y = _alloc(ts, (N, H, dv), y_dtype or x.dtype, dev)
     _launch(fn, dev, load_library().kda_ssm_decode_step, _addr(x), ldx, _addr(dt), lddt, _addr(B), ldb,
             _addr(C), ldc, _dt(x), _addr(A), _addr(dt_bias), _addr(D), _addr(state), _addr(slots),
-            _addr(y), ldy, _dt(y), N, state.shape[0], H, G, dk, dv, sp)
+            _addr(y), ldy, _dt(y), N, n_slots, H, G, dk, dv, sp)
     return y
 
 
