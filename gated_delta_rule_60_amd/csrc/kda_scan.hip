@@ -218,9 +218,10 @@ struct ValueLds {
     __align__(16) uint8_t c[BUFS * HB * C_BYTES];
     __align__(16) uint8_t a[STATE ? 16 : TOK / TA::R * TA::PIECE];
     __align__(16) uint8_t p[STATE ? 16 : HB * P_BYTES];              // scores per head
-    __align__(16) double cum[2][HB][TOK];
-    __align__(16) float del[2][HB][TOK], up[STATE ? 2 : 1][HB][TOK];
-    f32x2 over[2][HB];
+    static constexpr bool OWN = MODE == S_ONLY || MODE == G_ONLY;
+    __align__(16) double cum[STATE ? 1 : 2][HB][STATE ? 4 : TOK];  // STATE: the makers' sums of log2 e^g
+    __align__(16) float del[STATE ? 1 : 2][HB][STATE ? 4 : TOK], up[OWN ? 8 : STATE ? 2 : 1][HB][TOK];
+    f32x2 over[OWN ? 8 : 2][HB];
 };
 
 // One workgroup per (segment, HB heads of a group): a and b rows are shared, wave w has 16 columns of head
@@ -303,8 +304,10 @@ __device__ __forceinline__ void value_pass(const Scan& L, int32_t slot, int32_t 
 #pragma unroll
         for (int i = 0; i < NC; ++i) lds_put(lds.c + (STATE ? c & 1 : 0) * Lds::C_BYTES, TC::PIECE * (WAVES * i + wave) + lane * 16, x.c[i]);
     };
-    // the wave that makes a head's decays
-    const int table = wave - (WAVES - HB);
+    // The wave that makes a head's decays of the next chunk.  OWN: four waves, each those of one of the next four chunks, all
+    // at a time (one wave alone holds up the others for half the chunk's time).
+    const int table = OWN ? (wave < 4 ? 0 : -1) : wave - (WAVES - HB);
+    auto ring = [](int c) { return OWN ? c & 7 : c & 1; };
     const int32_t th = h0 + table < h_end ? h0 + (table < 0 ? 0 : table) : h_end - 1;
     const float A = L.A[th], bias = L.bias ? L.bias[th] : 0.f;
     // a chunk's place among those of all sequences: of the chunk that token w.lo + off belongs to
@@ -337,7 +340,7 @@ __device__ __forceinline__ void value_pass(const Scan& L, int32_t slot, int32_t 
     };
     double log_sum = 0.0;
     auto decays = [&](int c, const Ahead& a) {
-        const int buf = c & 1, n = chunk_n(chunk_at(c));
+        const int buf = ring(c), n = chunk_n(chunk_at(c));
         if constexpr (CARDS) {
             if (lane < TOK) {
                 if constexpr (MODE == DX) {
@@ -356,8 +359,10 @@ __device__ __forceinline__ void value_pass(const Scan& L, int32_t slot, int32_t 
         const float hi = static_cast<float>(over);
         log_sum += all;
         if (lane < TOK) {
-            lds.cum[buf][table][lane] = cum;
-            lds.del[buf][table][lane] = delta;
+            if constexpr (!STATE) {
+                lds.cum[buf][table][lane] = cum;
+                lds.del[buf][table][lane] = delta;
+            }
             if (STATE) lds.up[STATE ? buf : 0][table][lane] = chunk_sign(c + 1) * (BACK ? pow2(cum) : delta * pow2(all - cum));
             if (lane == 0) lds.over[buf][table] = f32x2{hi, static_cast<float>(over - static_cast<double>(hi))};
         }
@@ -373,10 +378,11 @@ __device__ __forceinline__ void value_pass(const Scan& L, int32_t slot, int32_t 
             load_a(0);
             load_c(0);
         }
-        if (table >= 0) decays(0, ahead_of(0));
+        if (table >= 0 && (!OWN || wave < n_chunks)) decays(OWN ? wave : 0, ahead_of(OWN ? wave : 0));
     }
     Ahead ahead{};
-    if (table >= 0 && n_chunks > 1) ahead = ahead_of(1);
+    const int first_ahead = OWN ? 4 + wave : 1;
+    if (table >= 0 && first_ahead < n_chunks) ahead = ahead_of(first_ahead);
 
     // ---- the state, tile mt of 16 rows.  Y and DX: register r of lane (l16, q) holds row row(mt) + r, column 16 wc + l16;
     // STATE: row 16 mt + l16, column 16 wc + 4 q + r, so that a lane's four lie side by side.  The states of the chunks
@@ -468,7 +474,7 @@ __device__ __forceinline__ void value_pass(const Scan& L, int32_t slot, int32_t 
         if (n_chunks > 0) put_rows(even, 0);
     auto chunk = [&](int c, Rows& far, const Rows& near) __attribute__((always_inline)) {
         const int64_t off = chunk_at(c), tok0 = w.lo + off;
-        const int n = chunk_n(off), buf = c & 1;
+        const int n = chunk_n(off), buf = c & 1, at_ring = ring(c);
         const uint8_t* const lds_b = lds.b + (STATE ? buf : 0) * Lds::B_BYTES;
         uint8_t* const lds_c = lds.c + ((STATE ? buf : 0) * HB + hb) * Lds::C_BYTES;
         if constexpr (!STATE) __builtin_amdgcn_s_waitcnt(vmcnt_imm(0));
@@ -476,9 +482,11 @@ __device__ __forceinline__ void value_pass(const Scan& L, int32_t slot, int32_t 
         if constexpr (STATE)
             if (c + 2 < n_chunks) take_rows(far, c + 2);
         const Ahead next = ahead;
-        if (table >= 0 && c + 2 < n_chunks) ahead = ahead_of(c + 2);
-        const double* cum = lds.cum[buf][hb];
-        const float* del = lds.del[buf][hb];
+        const bool makes = table >= 0 && (!OWN || c % 4 == 0);
+        const int made = c + first_ahead, far_made = made + (OWN ? 4 : 1);
+        if (makes && far_made < n_chunks) ahead = ahead_of(far_made);
+        const double* cum = lds.cum[STATE ? 0 : buf][hb];
+        const float* del = lds.del[STATE ? 0 : buf][hb];
 
         f32x4 O[IT];
         if constexpr (CHUNKS) {
@@ -572,8 +580,8 @@ __device__ __forceinline__ void value_pass(const Scan& L, int32_t slot, int32_t 
                 O[it] *= chunk_sign(c) * pow2(BACK ? all - ci : ci);
             }
         }
-        if (table >= 0 && c + 1 < n_chunks) decays(c + 1, next);
-        decay_state(M, lds.over[buf][hb]);
+        if (makes && made < n_chunks) decays(made, next);
+        decay_state(M, lds.over[at_ring][hb]);
 
         // ---- c along the tokens
         constexpr int CJ = BF ? JG : IT;
@@ -636,7 +644,7 @@ __device__ __forceinline__ void value_pass(const Scan& L, int32_t slot, int32_t 
             }
         }
         // ---- update
-        const float* up = lds.up[STATE ? buf : 0][hb];
+        const float* up = lds.up[STATE ? at_ring : 0][hb];
         if constexpr (BF) {
             auto update = [&](auto three) {
                 constexpr bool THREE = decltype(three)::value;
@@ -739,10 +747,12 @@ __device__ __forceinline__ void value_pass(const Scan& L, int32_t slot, int32_t 
     else if (MODE != DX && L.m_out[ST] && w.s == (BACK ? 0 : w.n_seg - 1)) dst = state(L.m_out[ST], unit);
     if (dst && live) store_state(dst, chunk_sign(n_chunks), false);
     if constexpr (OWN) {
-        if (table >= 0 && h0 + table < h_end && lane == 0) {
-            const double all = pow2_wide(log_sum);
+        if (table >= 0 && lane == 0) lds.cum[0][0][wave] = log_sum;
+        lds_barrier();
+        if (t == 0) {
+            const double all = pow2_wide((lds.cum[0][0][0] + lds.cum[0][0][1]) + (lds.cum[0][0][2] + lds.cum[0][0][3]));
             const float hi = static_cast<float>(all);
-            L.seg_decay[ST][static_cast<int64_t>(slot) * L.H + h0 + table] = f32x2{hi, static_cast<float>(all - static_cast<double>(hi))};
+            L.seg_decay[ST][seg_unit] = f32x2{hi, static_cast<float>(all - static_cast<double>(hi))};
         }
     }
 }
