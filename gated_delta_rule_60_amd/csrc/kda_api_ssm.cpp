@@ -85,6 +85,10 @@ int scan_sizes(int in_dtype, const int32_t* cu, const ScanShape& s) {
     if (ntok * s.G > (int64_t(1) << 33) / s.dk) return KDA_ERR_UNSUPPORTED;
     return KDA_OK;
 }
+// Workgroups of 1024 lanes per (chunk of the gradients, head) must stay within 2^32 lanes, rounded up to the XCDs.
+bool chunks_fit(int in_dtype, int64_t ntok, int64_t n_seqs, int32_t H) {
+    return ntok / (in_dtype == KDA_BF16 ? 64 : 32) + n_seqs <= ((int64_t(1) << 22) - 8) / H;
+}
 // Row strides of x, dt, B, C and the like: at least a row, 16-byte steps but for dt.
 struct Ld {
     int64_t ld, row;
@@ -224,6 +228,7 @@ size_t kda_ssm_chunk_workspace_size(int32_t n_seqs, int64_t total_tokens, int32_
         !supported_d(dk) || !supported_d(dv) || !valid_dtype(in_dtype))
         return 0;
     if (H > 32768 || (total_tokens / 128 + n_seqs) > (int64_t(1) << 21) / H) return 0;
+    if (backward && !chunks_fit(in_dtype, total_tokens, n_seqs, H)) return 0;
     return kda::scan_workspace_bytes(n_seqs, total_tokens, H, G, dk, dv, in_dtype, backward != 0);
 }
 
@@ -274,6 +279,7 @@ int kda_ssm_chunk_bwd(const void* x, int64_t ldx, const void* dt, int64_t lddt, 
     int st = scan_sizes(in_dtype, cu_seqlens, {B, T, n_seqs, H, G, dk, dv});
     if (st != KDA_OK) return st;
     const int64_t es = esize(in_dtype), ntok = B * T, rv = int64_t(H) * dv, rk = int64_t(G) * dk;
+    if (!chunks_fit(in_dtype, ntok, n_seqs, H)) return KDA_ERR_UNSUPPORTED;
     if ((st = strides_ok({{ldx, rv, true}, {lddt, H, false}, {ldb, rk, true}, {ldc, rk, true}, {lddy, rv, true},
                           {lddx, rv, true}, {ldddt, H, false}, {lddb, rk, true}, {lddc, rk, true}}, es)) != KDA_OK)
         return st;

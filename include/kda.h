@@ -42,7 +42,8 @@
  *   - Debug check: with the environment variable KDA_DEBUG_VALIDATE set (to anything but "" or
  *     "0"), kda_chunk_fwd, kda_chunk_fwd_checkpointed and the three decode calls first test those
  *     preconditions on the device (kda_chunk_fwd_gated tests cu_seqlens only: its g is in range
- *     by construction; the linear-attention calls test g <= 0 and cu_seqlens), wait for the answer
+ *     by construction; the linear-attention calls test g <= 0 and cu_seqlens, those of the selective
+ *     scan A <= 0 and cu_seqlens, the convolution's cu_seqlens), wait for the answer
  *     on `stream` and return KDA_ERR_INVALID_ARGUMENT, with nothing else enqueued, on a violation.
  *     This synchronises the host, shares one word of library-owned device memory between all calls
  *     on a device (overlapping checked calls race on it) and must not be used under stream capture.
@@ -397,10 +398,11 @@ int kda_state_load(const void *codes, int code, const float *scales, const int32
  *     n_slots, or on slot n with slots NULL (then N <= n_slots is required).  A sequence whose slot lies outside
  *     [0, n_slots) -- a padded row of a batch -- is skipped and gets zeros for its output; of several with one slot
  *     only the last is carried out, and the others get zeros.
- *   - Rows of a packed batch that belong to no sequence are left as they were.
+ *   - Rows of a packed batch that belong to no sequence (cu_seqlens[n_seqs] < T: a padded buffer) are left as they were.
+ *     The debug check asks for cu_seqlens[n_seqs] == T and refuses them.
  *   - Inputs are finite numbers: an infinity or a NaN in one token may reach, besides what the formulas give it,
- *     outputs of its sequence's tokens up to 64 before it, gradients of those up to 64 after it, and every token's ddt
- *     up to 512 before it; never another sequence's (the sums over tokens, dA and the like, aside).
+ *     outputs and gradients of its sequence's tokens up to 63 before and behind it; never another sequence's (the sums
+ *     over tokens, dA and the like, aside).
  *
  * kda_conv_fwd -- short causal convolution of every channel (W = 2, 3 or 4 taps):
  *     u_t = bias + sum_i weight[c, i] x_{t - W + 1 + i},   y_t = u_t / (1 + e^-u_t) with silu, else u_t.
@@ -481,7 +483,10 @@ int kda_ssm_chunk_fwd(const void *x, int64_t ldx, const void *dt, int64_t lddt, 
  *   d_final_state : [N, H, d_k, d_v] fp32 or NULL (= zeros).
  *   dA, dD, d_dt_bias : [H] fp32, written; dD, d_dt_bias NULL where they are not wanted.  Sums have a fixed order.
  *   d_initial_state : [N, H, d_k, d_v] fp32 or NULL where it is not wanted.
- *   workspace     : at least kda_ssm_chunk_workspace_size(..., 1) bytes, aligned to 16.
+ *   Sizes         : those of kda_ssm_chunk_fwd, and (B * T / c + n_seqs) * H < 2^22 - 8 with chunks of c = 64 tokens in
+ *                   KDA_BF16, 32 in KDA_F32 (KDA_ERR_UNSUPPORTED past it).
+ *   workspace     : at least kda_ssm_chunk_workspace_size(..., 1) bytes, aligned to 16: the states before, and their
+ *                   gradients behind, every chunk, 8 d_k d_v bytes a head and chunk, are most of it.
  */
 int kda_ssm_chunk_bwd(const void *x, int64_t ldx, const void *dt, int64_t lddt, const void *Bm, int64_t ldb,
                       const void *Cm, int64_t ldc, int in_dtype, const float *A, const float *dt_bias,

@@ -119,6 +119,17 @@ def test_scan_outputs(lib):
         assert K.kda_ssm_chunk_workspace_size(*bad) == 0
 
 
+def test_chunks_of_the_gradients(lib):
+    """Sizes that the forward call takes but the gradients' grids would not hold."""
+    size = lambda T, H, dtype, backward: K.kda_ssm_chunk_workspace_size(1, T, H, H, 64, 64, dtype, backward)
+    T = 128 * ((1 << 21) - 64)
+    assert size(T, 1, f32, False) > 0 and size(T, 1, f32, True) == 0
+    assert size(T // 2, 1, f32, True) > 0 and size(T, 1, bf, True) > 0
+    far = dict(H=1, G=1, in_dt=0, T=T, **{k: (i + 1) << 44 for i, k in enumerate(("x", "dt", "B", "C", "dy", "dx", "ddt", "dB", "dC"))})
+    assert bwd(lib, **far, ws_bytes=0) == UNS
+    assert bwd(lib, **{**far, "T": T // 2}, ws_bytes=0) == WS
+
+
 def test_side_by_side_rows(lib):
     """Gradients in one wider row are disjoint where their columns are, and only there.  (A call that passes the checks
     would launch: so one more argument is wrong in a way that is found later.)"""
