@@ -1481,6 +1481,8 @@ __global__ void __launch_bounds__(256) head_sum_kernel(Scan L) {
 // ---------------------------------------------------------------- host side
 
 int32_t head_blocks(int32_t H, int32_t G, int HB) { return (H / G + HB - 1) / HB; }
+// Heads of a workgroup of y and dx: two share the rows of B and C and the raw scores (24 sequences of 2048 tokens, 32 heads:
+// 242 us; one head: 300.  Few heads would rather have more workgroups: 1000 tokens whole 77 and 63 us).
 int value_heads(int32_t H, int32_t G, int32_t dv) { return dv == 64 && H / G > 1 ? 2 : 1; }
 
 template <int V>
@@ -1490,14 +1492,24 @@ auto by_sizes(int32_t dk, int32_t dv, F go) {
     if (dk == 128) return dv == 128 ? go(Int<128>{}, Int<128>{}) : go(Int<128>{}, Int<64>{});
     return dv == 128 ? go(Int<64>{}, Int<128>{}) : go(Int<64>{}, Int<64>{});
 }
-// Tokens per segment, a multiple of 128, for `units` (sequence, head block) pairs.
+// Tokens per segment of the forward pass, a multiple of 128, for `units` (sequence, head block) pairs: two workgroups a CU,
+// or one where those would have fewer than six chunks (packed 1 .. 8209, 16455 tokens, 8 heads: 72 us with two, 66 with
+// one; one sequence of 65536 tokens, 32 heads: 438 us with two, 504 with one, 457 with four).  256 pairs fill the CUs
+// by themselves.  Short sequences run whole: 520 tokens of 4 heads in bf16 take 45 us whole and 37 in segments, in fp32
+// 112 and 47, but 16 of 600 tokens of 16 heads 56 and 65.
 int32_t forward_segment(int64_t units, int32_t n_seqs, int64_t total, int32_t in_dtype, bool packed) {
-    const int64_t longest = packed ? total : total / n_seqs, blocks = units / n_seqs;
-    if (units >= 256 || longest < 1024) return WHOLE;
-    const int64_t shares = packed ? std::max<int64_t>(1, 512 / blocks - n_seqs / 2) : 512 / units;
-    const int64_t seg = std::max<int64_t>(((longest + shares - 1) / shares + 127) / 128 * 128, in_dtype == KDA_BF16 ? 256 : 128);
+    const int64_t longest = packed ? total : total / n_seqs, blocks = units / n_seqs, least = in_dtype == KDA_BF16 ? 256 : 128;
+    if (units >= 256 || longest < 2 * least * std::max<int64_t>(1, units / 64)) return WHOLE;
+    auto for_workgroups = [&](int64_t n) {
+        const int64_t shares = packed ? std::max<int64_t>(1, n / blocks - n_seqs / 2) : std::max<int64_t>(1, n / units);
+        return ((longest + shares - 1) / shares + 127) / 128 * 128;
+    };
+    int64_t seg = for_workgroups(512);
+    if (2 * seg < 3 * least) seg = std::max(for_workgroups(256), least);
     return seg >= longest || seg >= WHOLE ? WHOLE : static_cast<int32_t>(seg);
 }
+// Of the pass that writes the states of all chunks: it has a workgroup per head and direction, and what segments add (the
+// segments' own states, their scan) must pay: 4 x 4096 tokens of 32 heads take 232 us whole, 273 in four segments.
 int32_t state_segment(int64_t units, int32_t n_seqs, int64_t total, int32_t in_dtype, bool packed) {
     const int64_t longest = packed ? total : total / n_seqs, blocks = units / n_seqs;
     if (units >= 64 || longest < 1024) return WHOLE;
