@@ -5,9 +5,12 @@
 // with the inputs before a sequence's first token from its initial window.
 //
 // Bound by HBM (2 or 3 rows of channels a token, about 16 or 36 VALU instructions an element).  A lane owns V
-// neighbouring channels (16 bytes) and walks SUB tokens with the last W - 1 inputs in registers; a workgroup is 32
-// lanes of channels by 8 walks one behind the other, so that the W - 1 rows a walk reads of its neighbour's come
-// from the caches.  Sums are fp32, over a workgroup's RUN tokens, then fp64 over the workgroups in order.
+// neighbouring channels (16 bytes, 8 of 16-bit elements) and walks SUB tokens with the last W - 1 inputs in registers; a
+// workgroup is 32 lanes of channels by 8 walks one behind the other, so that the W - 1 rows a walk reads of its
+// neighbour's come from the caches.  4 x 4096 tokens of 4352 channels, bf16, 4 taps, SiLU: 57 us (5.0 TB/s), gradients
+// 112 us (3.8 TB/s: three waves a SIMD, two exponentials and two quotients an element); 1780 packed tokens of 2304
+// channels: gradients 20 us, of which a walk of 16 + 3 tokens, load after load, is most.  Sums are fp32, over a
+// workgroup's RUN tokens, then fp64 over the workgroups in order.
 #include "kda_ssm.hpp"
 #include "kda_tile.hpp"
 
@@ -413,13 +416,15 @@ __global__ void __launch_bounds__(256) conv_step_kernel(Conv c, uint8_t* windows
 
 bool fits(const void* p, int64_t bytes) { return reinterpret_cast<uintptr_t>(p) % bytes == 0; }
 
-// The widest accesses that the channels, the strides and the addresses allow: 16 bytes, 8 (16-bit elements), one
-// element.
-int vector_width(const ConvArgs& a, const void* windows) {
+// The widest accesses that the channels, the strides and the addresses allow, up to `most` channels: 16 bytes, 8 (16-bit
+// elements), one element.  Prompts take four channels at most: with eight 16-bit ones a lane's registers (162, gradients
+// 251) leave too few waves to keep loads under way (4 x 4096 x 4352: 67 us against 57, gradients 152 against 112).
+constexpr int PROMPT = 4, STEP_ONE = 8;
+int vector_width(const ConvArgs& a, const void* windows, int most) {
     const int64_t es = a.dtype == KDA_BF16 ? 2 : 4;
     for (int64_t bytes : {16, 8}) {
         const int64_t v = bytes / es;
-        if (v < 4 || a.C % v || a.x.ld % v || a.dy.ld % v || a.out.ld % v) continue;
+        if (v < 4 || v > most || a.C % v || a.x.ld % v || a.dy.ld % v || a.out.ld % v) continue;
         bool ok = true;
         for (const void* p : {a.x.p, a.dy.p, static_cast<const void*>(a.out.p), a.h0, static_cast<const void*>(a.hT), a.dhT,
                               static_cast<const void*>(a.dh0), windows})
@@ -454,7 +459,7 @@ Conv base(const ConvArgs& a, int V) {
 }
 
 // go(DT, V, W) as compile-time constants.
-template <typename F>
+template <int MOST, typename F>
 hipError_t by_kind(int dtype, int V, int W, F go) {
     auto taps = [&](auto dt, auto v) {
         if (W == 2) return go(dt, v, std::integral_constant<int, 2>{});
@@ -465,7 +470,8 @@ hipError_t by_kind(int dtype, int V, int W, F go) {
     using Four = std::integral_constant<int, 4>;
     if (dtype == KDA_BF16) {
         using Bf = std::integral_constant<int, KDA_BF16>;
-        if (V == 8) return taps(Bf{}, std::integral_constant<int, 8>{});
+        if constexpr (MOST == 8)
+            if (V == 8) return taps(Bf{}, std::integral_constant<int, 8>{});
         return V == 4 ? taps(Bf{}, Four{}) : taps(Bf{}, One{});
     }
     using F32 = std::integral_constant<int, KDA_F32>;
@@ -480,9 +486,9 @@ size_t conv_workspace_bytes(int32_t n_seqs, int64_t total, int32_t C, int32_t W)
 }
 
 hipError_t launch_conv_fwd(const ConvArgs& a, hipStream_t stream) {
-    const int V = vector_width(a, nullptr);
+    const int V = vector_width(a, nullptr, PROMPT);
     const Conv c = base(a, V);
-    return by_kind(a.dtype, V, a.W, [&](auto dt, auto v, auto w) {
+    return by_kind<PROMPT>(a.dtype, V, a.W, [&](auto dt, auto v, auto w) {
         constexpr int W = decltype(w)::value;
         const int64_t blocks = int64_t(c.slots) * c.vblocks;
         const int64_t windows = c.hT ? (int64_t(c.n_seqs) * (W - 1) * c.nvec + 255) / 256 : 0;
@@ -494,9 +500,9 @@ hipError_t launch_conv_fwd(const ConvArgs& a, hipStream_t stream) {
 }
 
 hipError_t launch_conv_bwd(const ConvArgs& a, hipStream_t stream) {
-    const int V = vector_width(a, nullptr);
+    const int V = vector_width(a, nullptr, PROMPT);
     const Conv c = base(a, V);
-    const hipError_t e = by_kind(a.dtype, V, a.W, [&](auto dt, auto v, auto w) {
+    const hipError_t e = by_kind<PROMPT>(a.dtype, V, a.W, [&](auto dt, auto v, auto w) {
         hipLaunchKernelGGL((conv_bwd_kernel<decltype(dt)::value, decltype(v)::value, decltype(w)::value>),
                            dim3(static_cast<unsigned>(int64_t(c.slots) * c.vblocks)), dim3(256), 0, stream, c);
         return hipGetLastError();
@@ -509,10 +515,10 @@ hipError_t launch_conv_bwd(const ConvArgs& a, hipStream_t stream) {
 
 hipError_t launch_conv_step(const ConvArgs& a, void* windows, const int32_t* slots, int32_t N, int32_t n_slots,
                             hipStream_t stream) {
-    const int V = vector_width(a, windows);
+    const int V = vector_width(a, windows, STEP_ONE);
     const Conv c = base(a, V);
     const int32_t blocks = (c.nvec + 255) / 256;
-    return by_kind(a.dtype, V, a.W, [&](auto dt, auto v, auto w) {
+    return by_kind<STEP_ONE>(a.dtype, V, a.W, [&](auto dt, auto v, auto w) {
         hipLaunchKernelGGL((conv_step_kernel<decltype(dt)::value, decltype(v)::value, decltype(w)::value>),
                            dim3(static_cast<unsigned>(int64_t(N) * blocks)), dim3(256), 0, stream, c,
                            static_cast<uint8_t*>(windows), slots, N, n_slots, blocks);

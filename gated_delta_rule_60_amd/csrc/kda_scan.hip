@@ -24,6 +24,10 @@
 //
 // All decays between two tokens are 2^(difference of fp64 sums): a difference of fp32 sums would lose a weak decay
 // behind a strong one.
+//
+// Measured, d_k x d_v = 128 x 64, one group, bf16: prompt of 65536 tokens, 32 heads 413 us (state pass 153, scan 14,
+// y 279 at the card's steady clock); gradients of 4 x 4096 tokens, 32 heads 453 us (chunks' states 200, grad 185, dx 90,
+// decays and sums 28).
 #include "kda_ssm.hpp"
 #include "kda_tile.hpp"
 
@@ -229,6 +233,12 @@ struct ValueLds {
 // product's operand): M and the scores are read as two bf16 terms (2^-16), the decayed c as three (exact) where M ends
 // in a state that is handed out in fp32; fp32 inputs use fp32 MFMAs.  The raw scores b a^T are formed once for
 // all HB heads, the last HB waves make the next chunk's decays meanwhile.
+//
+// y and dx are bound by instruction issue: 850 VALU instructions (splits of the state and of c, weights of the scores)
+// and 130 MFMAs a wave and chunk, four waves a SIMD at 128 registers; the rows' transfers are only hidden by the CU's
+// other workgroup.  (A transfer issued before the update's transposing reads would be waited for in front of them.)
+// 65536 x 32: 1.6 TB/s of rows.  The states of all chunks are bound by writing them: 2.7 TB/s for 4 x 4096 x 32; without
+// the stores the pass takes 123 us of 194, without the rows 140.
 template <int DT, int ODT, int DK, int DV, int HB, int MODE>
 __device__ __forceinline__ void value_pass(const Scan& L, int32_t slot, int32_t block, ValueLds<DT, DK, DV, HB, MODE>& lds) {
     using Lds = ValueLds<DT, DK, DV, HB, MODE>;
@@ -943,6 +953,7 @@ struct Decay {
     __device__ __forceinline__ float operator()(float d) const { return __builtin_amdgcn_exp2f(__builtin_fmaf(d, hi, d * lo)); }
 };
 
+// Bound by instruction issue and by the states' reads (537 MB, 2.9 TB/s for 4 x 4096 x 32, 185 us).
 // One workgroup per (chunk, block of a group's heads), of two kinds of waves: wave w of the first kind has the output
 // channels 16 w .. 16 w + 15 of dC and dB and forms the states' parts, those of the second share the groups of scores of
 // both directions and move the rows.  (One kind for both needs 300 registers a lane; what does not fit waits for the rows
@@ -1734,7 +1745,8 @@ hipError_t launch_scan_bwd(const ScanArgs& a, hipStream_t stream) {
 namespace {
 
 // One workgroup per (sequence, head): the state is read once, updated in registers and written once (non-temporal
-// both ways).  Lane t owns four columns of DK / RG rows.
+// both ways).  Lane t owns four columns of DK / RG rows.  Bound by HBM: 256 sequences, 32 heads of 128 x 64 in 101 us,
+// 5.3 TB/s; one sequence in 4.7 us.
 template <int DT, int ODT, int DK, int DV>
 __global__ void __launch_bounds__(256) step_kernel(Scan L, float* __restrict__ states, const int32_t* __restrict__ slots,
                                                    int32_t N, int32_t n_slots) {

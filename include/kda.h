@@ -406,8 +406,8 @@ int kda_state_load(const void *codes, int code, const float *scales, const int32
  *
  * kda_conv_fwd -- short causal convolution of every channel (W = 2, 3 or 4 taps):
  *     u_t = bias + sum_i weight[c, i] x_{t - W + 1 + i},   y_t = u_t / (1 + e^-u_t) with silu, else u_t.
- *   x, y          : [B, T, C] in dtype (KDA_F32 or KDA_BF16), strides ldx, ldy.  Any C; 16-byte accesses where C, the
- *                   strides and the addresses allow them, else 8-byte (16-bit types) or single elements.
+ *   x, y          : [B, T, C] in dtype (KDA_F32 or KDA_BF16), strides ldx, ldy.  Any C; four channels an access
+ *                   where C, the strides and the addresses allow it, else single elements.
  *   weight, bias  : [C, W] fp32; [C] fp32 or NULL (= zeros).
  *   initial_state : [N, W - 1, C] in dtype, the inputs before a sequence's first token, or NULL (= zeros).
  *   final_state   : [N, W - 1, C] in dtype or NULL: the last W - 1 inputs (initial ones where a sequence is
