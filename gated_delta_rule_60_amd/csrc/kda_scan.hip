@@ -234,8 +234,8 @@ struct ValueLds {
 // in a state that is handed out in fp32; fp32 inputs use fp32 MFMAs.  The raw scores b a^T are formed once for
 // all HB heads, the last HB waves make the next chunk's decays meanwhile.
 //
-// y and dx are bound by instruction issue: 850 VALU instructions (splits of the state and of c, weights of the scores)
-// and 130 MFMAs a wave and chunk, four waves a SIMD at 128 registers; the rows' transfers are only hidden by the CU's
+// y and dx are bound by instruction issue: 630 VALU instructions (splits of the state and of c, weights of the scores)
+// and 82 MFMAs a wave and chunk, four waves a SIMD at 128 registers; the rows' transfers are only hidden by the CU's
 // other workgroup.  (A transfer issued before the update's transposing reads would be waited for in front of them.)
 // 65536 x 32: 1.6 TB/s of rows.  The states of all chunks are bound by writing them: 2.7 TB/s for 4 x 4096 x 32; without
 // the stores the pass takes 123 us of 194, without the rows 140.
