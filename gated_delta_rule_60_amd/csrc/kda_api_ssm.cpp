@@ -243,7 +243,7 @@ int kda_ssm_chunk_fwd(const void* x, int64_t ldx, const void* dt, int64_t lddt, 
     const int64_t es = esize(in_dtype), os = esize(y_dtype), ntok = B * T, rv = int64_t(H) * dv, rk = int64_t(G) * dk;
     if ((st = strides_ok({{ldx, rv, true}, {lddt, H, false}, {ldb, rk, true}, {ldc, rk, true}}, es)) != KDA_OK) return st;
     if ((st = strides_ok({{ldy, rv, true}}, os)) != KDA_OK) return st;
-    if (ntok > 0 && (!x || !dt || !Bm || !Cm || !A || !y)) return KDA_ERR_INVALID_ARGUMENT;
+    if (!A || (ntok > 0 && (!x || !dt || !Bm || !Cm || !y))) return KDA_ERR_INVALID_ARGUMENT;
     if (!aligned16({x, Bm, Cm, y, initial_state, final_state, workspace}) || !aligned({dt}, es) ||
         !aligned4({A, dt_bias, D, cu_seqlens}))
         return KDA_ERR_UNSUPPORTED;
@@ -283,7 +283,7 @@ int kda_ssm_chunk_bwd(const void* x, int64_t ldx, const void* dt, int64_t lddt, 
     if ((st = strides_ok({{ldx, rv, true}, {lddt, H, false}, {ldb, rk, true}, {ldc, rk, true}, {lddy, rv, true},
                           {lddx, rv, true}, {ldddt, H, false}, {lddb, rk, true}, {lddc, rk, true}}, es)) != KDA_OK)
         return st;
-    if (!dA || (ntok > 0 && (!x || !dt || !Bm || !Cm || !A || !dy || !dx || !ddt || !dBm || !dCm)))
+    if (!A || !dA || (ntok > 0 && (!x || !dt || !Bm || !Cm || !dy || !dx || !ddt || !dBm || !dCm)))
         return KDA_ERR_INVALID_ARGUMENT;
     if (!aligned16({x, Bm, Cm, dy, dx, dBm, dCm, initial_state, d_final_state, d_initial_state, workspace}) ||
         !aligned({dt, ddt}, es) || !aligned4({A, dt_bias, D, dA, dD, d_dt_bias, cu_seqlens}))

@@ -1238,9 +1238,8 @@ __device__ __forceinline__ void grad_pass(const Scan& L, int32_t slot, int32_t b
         const uint8_t *x = lds.xy + buf * 2 * Lds::A_BYTES, *dy = x + Lds::A_BYTES;
         const Card<CT>& card = *reinterpret_cast<const Card<CT>*>(lds.card[buf]);
         f32x4 S[NS], G[NS];
-        if constexpr (Lds::AHEAD) {                  // the states are there; wave 0's four stores behind them may be under way
-            if (wave == 0 && k > 0) __builtin_amdgcn_s_waitcnt(vmcnt_imm(4));
-            else __builtin_amdgcn_s_waitcnt(vmcnt_imm(0));
+        if constexpr (Lds::AHEAD) {                  // the states are there (wave 0 has waited before its last stores)
+            if (wave > 0) __builtin_amdgcn_s_waitcnt(vmcnt_imm(0));
             wave_fence();
         }
         load_state(S, S_STATE, k);
@@ -1307,6 +1306,8 @@ __device__ __forceinline__ void grad_pass(const Scan& L, int32_t slot, int32_t b
         state_part(S, dy, std::false_type{});
         state_part(G, x, std::true_type{});
         lds_barrier();                               // the sums are there
+        static_assert(CT <= 64, "wave 0 alone stores");
+        if (Lds::AHEAD && wave == 0) __builtin_amdgcn_s_waitcnt(vmcnt_imm(0));   // (the stores need not be waited for later)
         if (t < n) {
             float p = 0.f, r = 0.f, rows = 0.f, cols = 0.f;
 #pragma unroll

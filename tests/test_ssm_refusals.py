@@ -94,7 +94,7 @@ def test_conv_step(lib):
 def test_scan(lib, call):
     each(call, lib, INV, [dict(in_dt=3), dict(nb=0), dict(T=-1), dict(N=2), dict(nb=2, N=2, cu=CU), dict(H=0), dict(G=0),
                           dict(G=3), dict(x=0), dict(dt=0), dict(B=0), dict(C=0), dict(A_=0), dict(ldx=255), dict(lddt=3),
-                          dict(ldb=127), dict(ldc=100), dict(ws=X), dict(ws=A), dict(h0=H0, ws=H0)])
+                          dict(ldb=127), dict(ldc=100), dict(ws=X), dict(ws=A), dict(h0=H0, ws=H0), dict(A_=0, T=0)])
     each(call, lib, UNS, [dict(dk=96), dict(dv=32), dict(x=X + 8), dict(B=B_ + 2), dict(C=C_ + 4), dict(dt=DT + 1),
                           dict(A_=A + 2), dict(ldx=260), dict(ldb=129), dict(ldc=132), dict(ldx=1 << 24), dict(h0=H0 + 4),
                           dict(ws=WSP + 8), dict(cu=CU + 2), dict(H=65536, G=1, ldx=1 << 22, lddt=65536, T=0),
