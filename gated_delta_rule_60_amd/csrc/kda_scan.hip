@@ -1238,8 +1238,9 @@ __device__ __forceinline__ void grad_pass(const Scan& L, int32_t slot, int32_t b
         const uint8_t *x = lds.xy + buf * 2 * Lds::A_BYTES, *dy = x + Lds::A_BYTES;
         const Card<CT>& card = *reinterpret_cast<const Card<CT>*>(lds.card[buf]);
         f32x4 S[NS], G[NS];
-        if constexpr (Lds::AHEAD) {                  // the states are there (wave 0 has waited before its last stores)
-            if (wave > 0) __builtin_amdgcn_s_waitcnt(vmcnt_imm(0));
+        if constexpr (Lds::AHEAD) {                  // the states are there; wave 0's four stores behind them may be under way
+            if (wave == 0 && k > 0) __builtin_amdgcn_s_waitcnt(vmcnt_imm(4));
+            else __builtin_amdgcn_s_waitcnt(vmcnt_imm(0));
             wave_fence();
         }
         load_state(S, S_STATE, k);
@@ -1307,7 +1308,6 @@ __device__ __forceinline__ void grad_pass(const Scan& L, int32_t slot, int32_t b
         state_part(G, x, std::true_type{});
         lds_barrier();                               // the sums are there
         static_assert(CT <= 64, "wave 0 alone stores");
-        if (Lds::AHEAD && wave == 0) __builtin_amdgcn_s_waitcnt(vmcnt_imm(0));   // (the stores need not be waited for later)
         if (t < n) {
             float p = 0.f, r = 0.f, rows = 0.f, cols = 0.f;
 #pragma unroll
@@ -1321,11 +1321,14 @@ __device__ __forceinline__ void grad_pass(const Scan& L, int32_t slot, int32_t b
                 if (Lds::near(0, tile, tg)) rows += lds.red[Lds::ROWS + tg][t];
                 if (Lds::near(1, tile, tg)) cols += lds.red[Lds::COLS + tg][t];
             }
-            const int64_t at = (h0 + k) * L.total + w.lo + t;
-            L.zz[at] = rows - card.del[t] * cols;
-            L.xz[at] = cols + lds.red[Lds::DIAG][t];
-            L.pp[at] = p;
-            L.xr[at] = r;
+            // (builtins, so that they are four: see the wait)
+            auto put = [&](float* all, float x) {
+                __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(x), make_rsrc_u(all + (h0 + k) * L.total + w.lo, n * 4), t * 4, 0, 0);
+            };
+            put(L.zz, rows - card.del[t] * cols);
+            put(L.xz, cols + lds.red[Lds::DIAG][t]);
+            put(L.pp, p);
+            put(L.xr, r);
         }
         lds_barrier();                               // the sums have been read
     }
