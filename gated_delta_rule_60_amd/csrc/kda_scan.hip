@@ -25,9 +25,9 @@
 // All decays between two tokens are 2^(difference of fp64 sums): a difference of fp32 sums would lose a weak decay
 // behind a strong one.
 //
-// Measured, d_k x d_v = 128 x 64, one group, bf16: prompt of 65536 tokens, 32 heads 413 us (state pass 153, scan 14,
-// y 279 at the card's steady clock); gradients of 4 x 4096 tokens, 32 heads 453 us (chunks' states 200, grad 185, dx 90,
-// decays and sums 28).
+// Measured, d_k x d_v = 128 x 64, one group, bf16: prompt of 65536 tokens, 32 heads 410 us (in a trace: state pass
+// 150, scan 14, y 297); gradients of 4 x 4096 tokens, 32 heads 435 us (in a trace: chunks' states 190, grad 175, dx 85,
+// decays and sums 26).
 #include "kda_ssm.hpp"
 #include "kda_tile.hpp"
 
@@ -84,8 +84,8 @@ constexpr int CHUNK = DT == KDA_BF16 ? 64 : 32;      // tokens
 // delta in the chunk, e the last token of a token's tile of 16, s the last one before that tile.
 template <int CT>
 struct Card {
-    double dsum[CT];         // D_i
-    float del[CT], ssum[CT]; // delta, running sums of its slope
+    double dsum[CT], ssum[CT];                       // D_i, running sums of delta's slope
+    float del[CT];
     float d_end[CT], s_end[CT];                      // D_e - D_j, and the slopes' sums
     float w_end[CT], w_start[CT];                    // delta_j e^(A (D_e - D_j)), e^(A (D_i - D_s))
     float before[CT], after[CT];                     // e^(A D_i), e^(A (D_n - D_i))
@@ -861,7 +861,7 @@ __global__ void __launch_bounds__(256) card_kernel(Scan L) {
     Card<CT>& c = reinterpret_cast<Card<CT>*>(L.cards)[u];
     c.dsum[lane] = d;
     c.del[lane] = s.delta;
-    c.ssum[lane] = static_cast<float>(o);
+    c.ssum[lane] = o;
     c.d_end[lane] = static_cast<float>(de - d);
     c.s_end[lane] = static_cast<float>(oe - o);
     c.w_end[lane] = s.delta * pow2(A2 * (de - d));
@@ -1104,7 +1104,8 @@ __device__ __forceinline__ void grad_pass(const Scan& L, int32_t slot, int32_t b
                 Lds::group(dir, grp - dir * Lds::GROUPS, out, tg);
                 const int col = 16 * out + l16;
                 const double dcol = dsum[col];
-                const float dc = card.del[col], scol = card.ssum[col];
+                const double scol = card.ssum[col];
+                const float dc = card.del[col];
                 float sum = 0.f, diag = 0.f;
 #pragma unroll
                 for (int hh = 0; hh < TILES; ++hh) {
@@ -1129,7 +1130,7 @@ __device__ __forceinline__ void grad_pass(const Scan& L, int32_t slot, int32_t b
                                 zb = __builtin_fmaf(z, se[r], zb);
                             }
                             zA = __builtin_fmaf(part, d, zA);
-                            zb = __builtin_fmaf(part, scol - card.ssum[16 * rt + 15], zb);
+                            zb = __builtin_fmaf(part, static_cast<float>(scol - card.ssum[16 * rt + 15]), zb);
                             sum += part;
                         } else {
                             const f32x4 ws = lds_get<f32x4>(card.w_start, 4 * row);
@@ -1143,7 +1144,7 @@ __device__ __forceinline__ void grad_pass(const Scan& L, int32_t slot, int32_t b
                             sum = __builtin_fmaf(part, f, sum);
                         }
                     } else if (dir == 0) {
-                        const f32x4 dr = lds_get<f32x4>(card.del, 4 * row), ss = lds_get<f32x4>(card.ssum, 4 * row);
+                        const f32x4 dr = lds_get<f32x4>(card.del, 4 * row);
 #pragma unroll
                         for (int r = 0; r < 4; ++r) {
                             const int j = row + r;
@@ -1152,7 +1153,7 @@ __device__ __forceinline__ void grad_pass(const Scan& L, int32_t slot, int32_t b
                             P[i][hh][r] = __builtin_fmaf(e, dr[r], P[i][hh][r]);
                             sum += z;
                             zA = __builtin_fmaf(z, d, zA);
-                            zb = __builtin_fmaf(z, scol - ss[r], zb);
+                            zb = __builtin_fmaf(z, static_cast<float>(scol - card.ssum[j]), zb);
                             if (j == col) {
                                 diag = y;
                                 dD += X[r];
@@ -1427,10 +1428,10 @@ __global__ void __launch_bounds__(256) decay_grad_kernel(Scan L) {
         r = static_cast<double>(s.delta) * later;
         slope = static_cast<double>(s.slope);
         ds = card.dsum[lane];
-        ss = static_cast<double>(card.ssum[lane]);
+        ss = card.ssum[lane];
     }
     const double zs = prefix_sum(zp), rs = prefix_sum(r);
-    const double d_all = card.dsum[CT - 1], s_all = static_cast<double>(card.ssum[CT - 1]);
+    const double d_all = card.dsum[CT - 1], s_all = card.ssum[CT - 1];
     const double dg = thr + (lane_value(zs, 63) - zs + zp) + (rs - r);
     // a lane's part of sum delta dg, sum slope dg, sum slope x . u
     double dA = p * ds + r * (d_all - ds), db = p * ss + r * (s_all - ss), own = slope * x;
