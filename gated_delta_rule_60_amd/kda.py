@@ -768,6 +768,13 @@ def _rows(fn, name, t, shape, dtype, lead):
     return ld
 
 
+def _required(fn, **named):
+    """Tensors that the call cannot do without (_expect takes None for an absent one)."""
+    for name, t in named.items():
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{fn}: {name} must be a torch.Tensor")
+
+
 def _float_dtype(fn, name, t):
     if not isinstance(t, torch.Tensor) or t.dtype not in _FLOATS:
         raise TypeError(f"{fn}: {name} must be a float32 or bfloat16 tensor")
@@ -806,6 +813,7 @@ def _check_conv(fn, x, weight, bias, cu_seqlens, like_x, windows):
         raise ValueError(f"{fn}: x must be a [B, T, C] tensor")
     B, T, C = x.shape
     ldx = _rows(fn, "x", x, (B, T, C), dt, 2)
+    _required(fn, weight=weight)
     _expect(fn, "weight", weight, (C, None), (torch.float32,))
     _expect(fn, "bias", bias, (C,), (torch.float32,))
     W = weight.shape[1]
@@ -891,6 +899,7 @@ def kda_conv_step(x, weight, windows, bias=None, slots=None, y=None, silu: bool 
             dev, (x, (N, C), dt), (weight, (C, W), torch.float32), (windows, (n_slots, W - 1, C), dt),
             (bias, (C,), torch.float32), (slots, (N,), torch.int32)):
         ldx = _rows(fn, "x", x, (N, C), dt, 1)
+        _required(fn, weight=weight, windows=windows)
         _expect(fn, "weight", weight, (C, None), (torch.float32,))
         _expect(fn, "windows", windows, (None, W - 1, C), (dt,))
         _expect(fn, "bias", bias, (C,), (torch.float32,))
@@ -926,6 +935,7 @@ def _check_ssm(fn, x, dt, A, B, C, D, dt_bias, lead):
         raise ValueError(f"{fn}: G = {G} must divide H = {H}")
     lds = (_rows(fn, "x", x, tok + (H, dv), ty, lead), _rows(fn, "dt", dt, tok + (H,), ty, lead),
            _rows(fn, "B", B, tok + (G, dk), ty, lead), _rows(fn, "C", C, tok + (G, dk), ty, lead))
+    _required(fn, A=A)
     _expect(fn, "A", A, (H,), (torch.float32,))
     _expect(fn, "D", D, (H,), (torch.float32,))
     _expect(fn, "dt_bias", dt_bias, (H,), (torch.float32,))
@@ -1022,6 +1032,7 @@ def kda_ssm_decode_step(x, dt, A, B, C, state, D=None, dt_bias=None, slots=None,
         ldx, lddt, ldb, ldc, ldy = H * dv, H, G * dk, G * dk, H * dv
     if not quick:
         (N,), H, G, dk, dv, (ldx, lddt, ldb, ldc) = _check_ssm(fn, x, dt, A, B, C, D, dt_bias, 1)
+        _required(fn, state=state)
         _expect(fn, "state", state, (None, H, dk, dv), (f32,))
         _expect(fn, "slots", slots, (N,), (torch.int32,))
         ldy = H * dv if y is None else _rows(fn, "y", y, (N, H, dv), _float_dtype(fn, "y", y), 1)
@@ -1090,6 +1101,7 @@ def kda_slots_copy(src, dst, src_slots=None, dst_slots=None, stream=None):
 
 
 def _count(fn, refs, slots, stream):
+    _required(fn, refs=refs, slots=slots)
     _expect(fn, "refs", refs, (None,), (torch.int32,))
     _expect(fn, "slots", slots, (None,), (torch.int32,))
     dev = _one_device(fn, refs=refs, slots=slots)
@@ -1123,6 +1135,7 @@ def kda_slots_fork(pool, refs, parents, children=None, workspace=None, stream=No
             raise TypeError(f"{fn}: parents must be an int32 tensor or a number")
         _expect(fn, "parents", parents, (None,), (torch.int32,))
         N = parents.numel()
+    _required(fn, refs=refs)
     _expect(fn, "refs", refs, (n_slots,), (torch.int32,))
     _expect(fn, "children", children, (N,), (torch.int32,))
     dev = _pool_device(fn, pool, refs=refs, parents=None if new else parents, children=children,
@@ -1142,6 +1155,7 @@ def kda_slots_compact(pool, refs, table=None, used=None, workspace=None, stream=
     rewritten in place, -1 where it named no used slot.  Returns U, an int32 tensor of one element."""
     fn = "kda_slots_compact"
     pool, n_slots, pa, pb = _planes(fn, "pool", pool)
+    _required(fn, refs=refs)
     _expect(fn, "refs", refs, (n_slots,), (torch.int32,))
     if table is not None:
         _expect(fn, "table", table, tuple(table.shape) if isinstance(table, torch.Tensor) else (), (torch.int32,))
