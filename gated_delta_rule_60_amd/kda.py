@@ -1130,7 +1130,10 @@ def kda_slots_fork(pool, refs, parents, children=None, workspace=None, stream=No
     pool, n_slots, pa, pb = _planes(fn, "pool", pool)
     new = isinstance(parents, int)
     N = parents if new else None
-    if not new:
+    if new:
+        if not 0 <= N < 1 << 31:
+            raise ValueError(f"{fn}: parents must be an int32 tensor or a number from 0 to 2^31 - 1, got {N}")
+    else:
         if not isinstance(parents, torch.Tensor):
             raise TypeError(f"{fn}: parents must be an int32 tensor or a number")
         _expect(fn, "parents", parents, (None,), (torch.int32,))

@@ -40,3 +40,11 @@ def test_refused_by_name(fn, name, value):
     call, args = CALLS[fn]
     with pytest.raises((TypeError, ValueError), match=rf"^{fn}: {name} must be "):
         call(**{**args, name: value})
+
+
+@pytest.mark.parametrize("count", [-1, 1 << 31, 1.5, None])
+def test_number_of_new_sequences(count):
+    """A number of new sequences that the call cannot carry out is refused as such, not by what it would allocate."""
+    refs = torch.zeros(6, dtype=i32)
+    with pytest.raises((TypeError, ValueError), match="^kda_slots_fork: parents must be "):
+        K.kda_slots_fork(torch.zeros(6, 3), refs, count)
