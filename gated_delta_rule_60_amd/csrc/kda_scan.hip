@@ -1541,6 +1541,24 @@ int32_t dx_segment(int64_t units, int32_t n_seqs, int64_t total, int32_t in_dtyp
     return seg >= longest || seg >= WHOLE ? WHOLE : static_cast<int32_t>(seg);
 }
 
+// The rules' segments jump as the sizes grow, and a workspace that is kept for the largest batch must serve every smaller
+// one.  So the workspace's size is formed from the most segments that n_seqs sequences of `total` tokens or fewer of
+// either have, `blocks` head blocks a sequence (n of the sequences that still run in segments):
+//   a segment has `least` tokens or more: total / least + n;
+//   fixed lengths: at most n (W / (n blocks)) for W workgroups; packed: W / blocks - n / 2 and one more a sequence.
+int64_t most_segments(int64_t blocks, int32_t n_seqs, int64_t total, int64_t whole, int64_t workgroups, int64_t shortest, int64_t least) {
+    if (blocks >= whole || total < shortest) return 0;
+    const int64_t n = std::min<int64_t>(n_seqs, (whole - 1) / blocks);
+    return std::min(total / least + n, workgroups / blocks + (n + 1) / 2);
+}
+int64_t most_forward_segments(int64_t blocks, int32_t n_seqs, int64_t total, int32_t in_dtype) {
+    const int64_t least = in_dtype == KDA_BF16 ? 256 : 128;
+    return most_segments(blocks, n_seqs, total, 256, 512, 2 * least, least);
+}
+int64_t most_state_segments(int64_t blocks, int32_t n_seqs, int64_t total) {
+    return most_segments(blocks, n_seqs, total, 64, 256, 1024, 512);
+}
+
 int64_t segment_slots(int32_t n_seqs, int64_t total, int32_t seg, bool packed) {
     if (packed) return total / seg + n_seqs;
     return n_seqs * std::max<int64_t>(1, (total / n_seqs + seg - 1) / seg);
@@ -1574,20 +1592,27 @@ void set_chunks(Scan& L, int32_t in_dtype, bool packed) {
     L.blocks = head_blocks(L.H, L.G, L.heads);
 }
 
+// Rows of d_k that the head blocks of the gradients leave to be added up (where there is more than one block).
+int64_t block_parts(const Scan& L) { return L.total * L.G * L.blocks; }
+// The most of them, for L.total tokens or fewer.  set_chunks halves the heads of a block, and so doubles the blocks at
+// most, while c chunks of ct tokens have c G blocks < 256: fewer than 512 / (c G) blocks, of c ct tokens or fewer.
+int64_t most_block_parts(const Scan& L) { return std::min(L.total * L.H, int64_t(510) * L.ct); }
+
+// Called with a call's own segments and chunks, and with the most that smaller sizes have.
 void carve_segments(Scan& L, Carver& ws, int64_t elems, int passes) {
-    if (L.seg == WHOLE) return;
+    if (L.seg == WHOLE || L.slots == 0) return;
     for (int st = 0; st < passes; ++st) {
         L.seg_states[st] = ws.take<float>(int64_t(L.slots) * L.H * elems);
         L.seg_decay[st] = ws.take<f32x2>(int64_t(L.slots) * L.H);
     }
 }
 void carve_forward(Scan& L, Carver& ws, int64_t elems) { carve_segments(L, ws, elems, 1); }
-void carve_backward(Scan& L, Carver& ws, int32_t dk, int32_t dv) {
+void carve_backward(Scan& L, Carver& ws, int32_t dk, int32_t dv, int64_t parts) {
     const int64_t cu = int64_t(L.c_slots) * L.H;
     carve_segments(L, ws, int64_t(dk) * dv, 2);
     for (float*& p : L.chunk_states) p = ws.take<float>(cu * dk * dv);
     if (L.blocks > 1)
-        for (float*& p : L.part) p = ws.take<float>(L.total * L.G * dk * L.blocks);
+        for (float*& p : L.part) p = ws.take<float>(parts * dk);
     L.cards = ws.take<uint8_t>(cu * (L.ct == CHUNK<KDA_BF16> ? sizeof(Card<CHUNK<KDA_BF16>>) : sizeof(Card<CHUNK<KDA_F32>>)));
     for (float** p : {&L.zz, &L.pp, &L.xz, &L.xr}) *p = ws.take<float>(L.H * L.total);
     for (float** p : {&L.zA, &L.zb, &L.dDp, &L.thr, &L.dAp, &L.dbp}) *p = ws.take<float>(cu);
@@ -1666,7 +1691,7 @@ hipError_t backward(const ScanArgs& a, hipStream_t stream) {
     set_chunks(L, a.in_dtype, packed);
     set_segments(L, state_segment, a.dv, a.in_dtype, packed);
     Carver ws{static_cast<uint8_t*>(a.workspace)};
-    carve_backward(L, ws, a.dk, a.dv);
+    carve_backward(L, ws, a.dk, a.dv, block_parts(L));
     L.m_out[G_STATE] = a.dh0;
     L.exact[S_STATE] = L.exact[G_STATE] = 1;
     L.ddt = out(a.ddt);
@@ -1717,18 +1742,28 @@ hipError_t backward(const ScanArgs& a, hipStream_t stream) {
 
 size_t scan_workspace_bytes(int32_t n_seqs, int64_t total, int32_t H, int32_t G, int32_t dk, int32_t dv,
                             int32_t in_dtype, bool backward) {
-    // what a packed batch of these sizes needs, or fixed-length sequences: whichever is more
+    // what sizes up to these may need, which is never less than what these do as fixed lengths or packed
     size_t most = 0;
-    for (const bool packed : {false, true}) {
+    const int64_t blocks = int64_t(head_blocks(H, G, value_heads(H, G, dv))) * G;
+    for (const int kind : {0, 1, 2}) {               // fixed lengths, packed, the most of all
         Scan L{};
         L.n_seqs = n_seqs; L.total = total; L.H = H; L.G = G;
         Carver ws{nullptr};
         if (backward) {
-            set_chunks(L, in_dtype, packed);
-            set_segments(L, state_segment, dv, in_dtype, packed);
-            carve_backward(L, ws, dk, dv);
+            set_chunks(L, in_dtype, kind >= 1);      // (a packed batch has the more chunks)
+            set_segments(L, state_segment, dv, in_dtype, kind == 1);
+            if (kind == 2) {
+                L.blocks = H / G;
+                L.seg = 0;
+                L.slots = static_cast<int32_t>(most_state_segments(blocks, n_seqs, total));
+            }
+            carve_backward(L, ws, dk, dv, kind == 2 ? most_block_parts(L) : block_parts(L));
         } else {
-            set_segments(L, forward_segment, dv, in_dtype, packed);
+            set_segments(L, forward_segment, dv, in_dtype, kind == 1);
+            if (kind == 2) {
+                L.seg = 0;
+                L.slots = static_cast<int32_t>(most_forward_segments(blocks, n_seqs, total, in_dtype));
+            }
             carve_forward(L, ws, int64_t(dk) * dv);
         }
         most = std::max(most, ws.used);

@@ -918,6 +918,8 @@ def kda_conv_step(x, weight, windows, bias=None, slots=None, y=None, silu: bool 
 
 def kda_ssm_chunk_workspace_size(n_seqs: int, total_tokens: int, H: int, G: int, dk: int, dv: int,
                                  in_dtype: torch.dtype = torch.bfloat16, backward: bool = False) -> int:
+    """Bytes of a scan call's workspace.  Never falls as n_seqs or total_tokens grow: what serves the
+    largest batch serves every smaller one of the same heads and type."""
     return int(load_library().kda_ssm_chunk_workspace_size(n_seqs, total_tokens, H, G, dk, dv,
                                                            _DT[in_dtype], int(backward)))
 

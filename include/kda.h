@@ -104,7 +104,8 @@ int kda_gate(const float *A, const void *z, int z_dtype, void *g, int g_dtype, i
  * (sequence, head) units also need per-segment state buffers.  Batches of bf16 inputs at
  * d_k = d_v = 128 with n_seqs * H >= 256 run one fused kernel that builds the records on chip:
  * their size is 0 (a NULL workspace is accepted).
- * Never fails; returns 0 for invalid sizes (kda_chunk_fwd then reports the error).
+ * Never fails; returns 0 for invalid sizes (kda_chunk_fwd then reports the error).  The size is that of
+ * these very numbers: fewer sequences may need more.
  */
 size_t kda_chunk_fwd_workspace_size(int32_t n_seqs, int64_t total_tokens, int32_t H, int32_t dk,
                                     int32_t dv, int32_t chunk, int in_dtype);
@@ -293,7 +294,8 @@ int kda_decode_commit(const void *q, const void *k, const void *v, const void *b
  *
  * kda_linear_chunk_workspace_size -- workspace bytes of kda_linear_chunk_fwd (backward = 0) or
  * kda_linear_chunk_bwd (backward != 0) for n_seqs sequences of total_tokens tokens (B*T).  May be
- * 0 (a NULL workspace is then accepted).  Never fails; 0 for invalid sizes.
+ * 0 (a NULL workspace is then accepted).  Never fails; 0 for invalid sizes.  The size is that of these very
+ * numbers: fewer tokens or sequences may need more.
  */
 size_t kda_linear_chunk_workspace_size(int32_t n_seqs, int64_t total_tokens, int32_t H, int32_t dk,
                                        int32_t dv, int in_dtype, int backward);
@@ -394,6 +396,8 @@ int kda_state_load(const void *codes, int code, const float *scales, const int32
  *     may be up to 2^24 bytes (KDA_ERR_UNSUPPORTED past it).  States and windows are contiguous.
  *   - Outputs must not overlap inputs or one another (rows of one stride side by side do not).
  *   - The stream must belong to the current device.
+ *   - The workspace sizes never fall as sequences, tokens or slots grow: with the same heads, channels and types, a
+ *     workspace for the largest call serves every smaller one.
  *   - Pools: where a call takes `slots` (device int32 [N]), sequence n works on slot slots[n] of an array of
  *     n_slots, or on slot n with slots NULL (then N <= n_slots is required).  A sequence whose slot lies outside
  *     [0, n_slots) -- a padded row of a batch -- is skipped and gets zeros for its output; of several with one slot
