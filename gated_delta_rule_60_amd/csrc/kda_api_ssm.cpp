@@ -8,7 +8,9 @@
 
 namespace {
 
-constexpr int64_t kMaxRow = int64_t(1) << 24;        // bytes from token to token: a run of rows stays below 2 GiB
+// Bytes from token to token.  The kernels' offsets into a run of 128 tokens, with up to 3 on either side, are unsigned 32-bit
+// numbers: 134 rows span less than 2^32 bytes (though more than 2^31).
+constexpr int64_t kMaxRow = int64_t(1) << 24;
 constexpr int64_t kMaxTokens = (int64_t(1) << 31) - 1;
 
 // `rows` rows of `bytes` each, `ld` bytes apart.
