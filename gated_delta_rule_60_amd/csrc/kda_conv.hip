@@ -4,13 +4,15 @@
 //     du_t = dy_t y'(u_t),   dx_t = sum_k w_{W-1-k} du_{t+k},   dw_i = sum_t du_t x_{t-W+1+i},   dbias = sum_t du_t
 // with the inputs before a sequence's first token from its initial window.
 //
-// Bound by HBM (2 or 3 rows of channels a token, about 16 or 36 VALU instructions an element).  A lane owns V
-// neighbouring channels (16 bytes, 8 of 16-bit elements) and walks SUB tokens with the last W - 1 inputs in registers; a
-// workgroup is 32 lanes of channels by 8 walks one behind the other, so that the W - 1 rows a walk reads of its
-// neighbour's come from the caches.  4 x 4096 tokens of 4352 channels, bf16, 4 taps, SiLU: 57 us (5.0 TB/s), gradients
-// 112 us (3.8 TB/s: three waves a SIMD, two exponentials and two quotients an element); 1780 packed tokens of 2304
-// channels: gradients 20 us, of which a walk of 16 + 3 tokens, load after load, is most.  Sums are fp32, over a
-// workgroup's RUN tokens, then fp64 over the workgroups in order.
+// A lane owns V neighbouring channels (prompts four: 8 bytes of 16-bit elements, 16 of fp32; the step up to 16 bytes) and
+// walks SUB tokens with the last W - 1 inputs in registers; a workgroup is 32 lanes of channels by 8 walks one behind the
+// other, so that the W - 1 rows a walk reads of its neighbour's come from the caches.
+// 4 x 4096 tokens of 4352 channels, 4 taps, SiLU: bf16 58 us (4.9 TB/s), fp32 114 us (5.0 TB/s), bound by HBM (2 rows of
+// channels a token, about 16 VALU instructions an element).  Gradients (3 rows): fp32 180 us (4.8 TB/s), bf16 115 us
+// (3.7 TB/s), bound by VALU issue: 47 instructions an element of a walk, of which it takes 16 + 3 for 16 tokens (one
+// exponential and one reciprocal each); the SIMDs issue all of the kernel's time.  1780 packed tokens of 2304 channels:
+// gradients 19 us, of which a walk, load after load, is most.
+// Sums are fp32, over a workgroup's RUN tokens, then fp64 over the workgroups in order.
 #include "kda_ssm.hpp"
 #include "kda_tile.hpp"
 
@@ -418,7 +420,7 @@ bool fits(const void* p, int64_t bytes) { return reinterpret_cast<uintptr_t>(p) 
 
 // The widest accesses that the channels, the strides and the addresses allow, up to `most` channels: 16 bytes, 8 (16-bit
 // elements), one element.  Prompts take four channels at most: with eight 16-bit ones a lane's registers (162, gradients
-// 251) leave too few waves to keep loads under way (4 x 4096 x 4352: 67 us against 57, gradients 152 against 112).
+// 251) leave too few waves to keep loads under way (4 x 4096 x 4352: 67 us against 58, gradients 152 against 115).
 constexpr int PROMPT = 4, STEP_ONE = 8;
 int vector_width(const ConvArgs& a, const void* windows, int most) {
     const int64_t es = a.dtype == KDA_BF16 ? 2 : 4;

@@ -25,9 +25,10 @@
 // All decays between two tokens are 2^(difference of fp64 sums): a difference of fp32 sums would lose a weak decay
 // behind a strong one.
 //
-// Measured, d_k x d_v = 128 x 64, one group, bf16: prompt of 65536 tokens, 32 heads 410 us (in a trace: state pass
-// 150, scan 14, y 297); gradients of 4 x 4096 tokens, 32 heads 435 us (in a trace: chunks' states 190, grad 175, dx 85,
-// decays and sums 26).
+// Measured, one group, bf16, d_k x d_v = 128 x 64, 32 heads: prompt of 65536 tokens 420 us (in a trace: state pass
+// 148, scan 14, y 273), 4 x 4096 tokens 118; gradients of 4 x 4096 tokens 450 us (in a trace: chunks' states 183, grad 169,
+// dx 80, decays and sums 25); fp32: 304 and 1009 us.  128 x 128, 16 heads: 125 and 539 us (chunks' states 217, grad 228, dx
+// 76, decays and sums 18).
 #include "kda_ssm.hpp"
 #include "kda_tile.hpp"
 
@@ -61,6 +62,7 @@ struct Scan {
     float* part[2];          // [head blocks of a group, tokens, G, dk] dC, dB per block; nullptr: one block
     uint8_t* cards;          // [c_slots, H] Card of a chunk's decays
     // [H, tokens]: sum_j z_tj - sum_i z_it; p_t; x_t . u_t from this chunk's outputs, and from later ones (r_t / delta_t)
+    // (fp32: each is a sum inside a chunk, rounded once; what is formed from them over a chunk or a sequence is fp64)
     float *zz, *pp, *xz, *xr;
     // [c_slots, H]: sums of z_ij (W_i - W_j) for W of delta and of the slopes, of x . dy, <G, S>
     float *zA, *zb, *dDp, *thr;
@@ -230,15 +232,18 @@ struct ValueLds {
 
 // One workgroup per (segment, HB heads of a group): a and b rows are shared, wave w has 16 columns of head
 // w / (DV / 16).  The products are those of linear attention's pass (transposed, so that an accumulator is the next
-// product's operand): M and the scores are read as two bf16 terms (2^-16), the decayed c as three (exact) where M ends
-// in a state that is handed out in fp32; fp32 inputs use fp32 MFMAs.  The raw scores b a^T are formed once for
-// all HB heads, the last HB waves make the next chunk's decays meanwhile.
+// product's operand): M and the scores are read as two bf16 terms (2^-17 each), the decayed c as three (exact) where M ends
+// in a state that is handed out in fp32, else as two; fp32 inputs use fp32 MFMAs.  (Two, whatever y's type: beside inputs of
+// 8 bits an fp32 y is off by 1.2e-6 of its size, a third term would be half as many MFMAs and splits again.  The states
+// between segments count as handed out where a final state is.)  The raw scores b a^T are formed once for all HB heads,
+// the last HB waves make the next chunk's decays meanwhile.
 //
 // y and dx are bound by instruction issue: 630 VALU instructions (splits of the state and of c, weights of the scores)
 // and 82 MFMAs a wave and chunk, four waves a SIMD at 128 registers; the rows' transfers are only hidden by the CU's
 // other workgroup.  (A transfer issued before the update's transposing reads would be waited for in front of them.)
-// 65536 x 32: 1.6 TB/s of rows.  The states of all chunks are bound by writing them: 2.7 TB/s for 4 x 4096 x 32; without
-// the stores the pass takes 123 us of 194, without the rows 140.
+// 65536 x 32: 2.0 TB/s of rows.  Bf16 inputs at 128 x 128, or with an fp32 y, are 4 to 8 registers over 128 (5 to 9 reloads
+// from scratch memory).  The states of all chunks are bound by writing them: 2.9 TB/s for 4 x 4096 x 32; without the
+// stores the pass takes 110 us of 183, without the rows 127.
 template <int DT, int ODT, int DK, int DV, int HB, int MODE>
 __device__ __forceinline__ void value_pass(const Scan& L, int32_t slot, int32_t block, ValueLds<DT, DK, DV, HB, MODE>& lds) {
     using Lds = ValueLds<DT, DK, DV, HB, MODE>;
@@ -953,14 +958,15 @@ struct Decay {
     __device__ __forceinline__ float operator()(float d) const { return __builtin_amdgcn_exp2f(__builtin_fmaf(d, hi, d * lo)); }
 };
 
-// Bound by instruction issue and by the states' reads (537 MB, 2.9 TB/s for 4 x 4096 x 32, 185 us).
+// Bound by instruction issue and by the states' reads (537 MB, 3.2 TB/s for 4 x 4096 x 32, 169 us).  At 128 x 128 in bf16 a
+// lane's rows of both states are 34 registers more than it has: 28 reloads from scratch memory, 228 us for 16 heads.
 // One workgroup per (chunk, block of a group's heads), of two kinds of waves: wave w of the first kind has the output
 // channels 16 w .. 16 w + 15 of dC and dB and forms the states' parts, those of the second share the groups of scores of
 // both directions and move the rows.  (One kind for both needs 300 registers a lane; what does not fit waits for the rows
 // under way: 743 us for 4 x 4096 x 32.)  B and C are read once, the heads' rows come one head after the other, the next
 // one's under this one's products.  The scores' products with B and C are formed once, from their sums over the heads (two
-// bf16 terms: they only feed 16-bit outputs).  The states are read as three (exact), for p, r and what comes of them is
-// handed out in fp32.
+// bf16 terms, 2^-17 each: they only feed 16-bit outputs).  The states are read as three (exact), for p, r and what comes of
+// them is handed out in fp32.
 template <int DT, int DK, int DV>
 __device__ __forceinline__ void grad_pass(const Scan& L, int32_t slot, int32_t block, GradLds<DT, DK, DV>& lds) {
     using Lds = GradLds<DT, DK, DV>;
@@ -1498,7 +1504,8 @@ __global__ void __launch_bounds__(256) head_sum_kernel(Scan L) {
 
 int32_t head_blocks(int32_t H, int32_t G, int HB) { return (H / G + HB - 1) / HB; }
 // Heads of a workgroup of y and dx: two share the rows of B and C and the raw scores (24 sequences of 2048 tokens, 32 heads:
-// 242 us; one head: 300.  Few heads would rather have more workgroups: 1000 tokens whole 77 and 63 us).
+// 249 us; one head: 307.  Few heads would rather have more workgroups: 1000 tokens of 8 heads whole 76 and 62 us, but they
+// run in segments, 36).
 int value_heads(int32_t H, int32_t G, int32_t dv) { return dv == 64 && H / G > 1 ? 2 : 1; }
 
 template <int V>
@@ -1509,10 +1516,10 @@ auto by_sizes(int32_t dk, int32_t dv, F go) {
     return dv == 128 ? go(Int<64>{}, Int<128>{}) : go(Int<64>{}, Int<64>{});
 }
 // Tokens per segment of the forward pass, a multiple of 128, for `units` (sequence, head block) pairs: two workgroups a CU,
-// or one where those would have fewer than six chunks (packed 1 .. 8209, 16455 tokens, 8 heads: 72 us with two, 66 with
-// one; one sequence of 65536 tokens, 32 heads: 438 us with two, 504 with one, 457 with four).  256 pairs fill the CUs
-// by themselves.  Short sequences run whole: 520 tokens of 4 heads in bf16 take 45 us whole and 37 in segments, in fp32
-// 112 and 47, but 16 of 600 tokens of 16 heads 56 and 65.
+// or one where those would have fewer than six chunks (packed 1 .. 8209, 16455 tokens, 8 heads: 71 us with two, 64 with
+// one; one sequence of 65536 tokens, 32 heads: 409 us with two, 494 with one, 433 with four).  256 pairs fill the CUs
+// by themselves.  Short sequences run whole: 520 tokens of 4 heads in bf16 take 44 us whole and 35 in segments, in fp32
+// 111 and 45, but 16 of 600 tokens of 16 heads 55 and 63.
 int32_t forward_segment(int64_t units, int32_t n_seqs, int64_t total, int32_t in_dtype, bool packed) {
     const int64_t longest = packed ? total : total / n_seqs, blocks = units / n_seqs, least = in_dtype == KDA_BF16 ? 256 : 128;
     if (units >= 256 || longest < 2 * least * std::max<int64_t>(1, units / 64)) return WHOLE;
@@ -1525,7 +1532,8 @@ int32_t forward_segment(int64_t units, int32_t n_seqs, int64_t total, int32_t in
     return seg >= longest || seg >= WHOLE ? WHOLE : static_cast<int32_t>(seg);
 }
 // Of the pass that writes the states of all chunks: it has a workgroup per head and direction, and what segments add (the
-// segments' own states, their scan) must pay: 4 x 4096 tokens of 32 heads take 232 us whole, 273 in four segments.
+// segments' own states, their scan) must pay.  Gradients of 32 heads: 4 x 4096 tokens 451 us whole, 516 in four segments;
+// 2 x 4096 300 and 295, 1 x 4096 199 and 148 (1024 tokens, the shortest that run so, 76 and 85).
 int32_t state_segment(int64_t units, int32_t n_seqs, int64_t total, int32_t in_dtype, bool packed) {
     const int64_t longest = packed ? total : total / n_seqs, blocks = units / n_seqs;
     if (units >= 64 || longest < 1024) return WHOLE;
@@ -1785,8 +1793,8 @@ hipError_t launch_scan_bwd(const ScanArgs& a, hipStream_t stream) {
 namespace {
 
 // One workgroup per (sequence, head): the state is read once, updated in registers and written once (non-temporal
-// both ways).  Lane t owns four columns of DK / RG rows.  Bound by HBM: 256 sequences, 32 heads of 128 x 64 in 101 us,
-// 5.3 TB/s; one sequence in 4.7 us.
+// both ways).  Lane t owns four columns of DK / RG rows.  Bound by HBM: 256 sequences, 32 heads of 128 x 64 in 100 to
+// 104 us, 5.2 TB/s; one sequence in 4.7 us.
 template <int DT, int ODT, int DK, int DV>
 __global__ void __launch_bounds__(256) step_kernel(Scan L, float* __restrict__ states, const int32_t* __restrict__ slots,
                                                    int32_t N, int32_t n_slots) {

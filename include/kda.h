@@ -462,8 +462,10 @@ int kda_conv_step(const void *x, int64_t ldx, int dtype, const float *weight, co
  *   H, G, dk, dv  : G divides H; dk, dv 64 or 128 each.  Sizes (KDA_ERR_UNSUPPORTED past them): H <= 32768,
  *                   (B * T / 128 + n_seqs) * H <= 2^21, B * T * G * dk <= 2^33.
  *   workspace     : at least kda_ssm_chunk_workspace_size(..., 0) bytes, aligned to 16 (may be 0).
- * Sums and states are fp32, decays between tokens come from fp64 sums.  bf16 inputs enter the products exactly, states
- * and weighted scores as two or more bf16 terms; y is rounded once to y_dtype.
+ * Sums and states are fp32.  Decays between tokens come from fp64 sums over up to 64 tokens: steps delta_t |A| of 2^29 and
+ * more would drown small ones beside them.  bf16 inputs enter the products exactly.  With them y reads states and
+ * weighted scores as two bf16 terms each (2^-17 a term, error of an fp32 y: about 1e-6 of its size; fp32 inputs: 2e-7),
+ * and is rounded once to y_dtype; the final state holds fp32 accuracy.
  */
 size_t kda_ssm_chunk_workspace_size(int32_t n_seqs, int64_t total_tokens, int32_t H, int32_t G, int32_t dk,
                                     int32_t dv, int in_dtype, int backward);
