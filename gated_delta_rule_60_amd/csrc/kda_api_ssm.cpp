@@ -145,7 +145,7 @@ bool planes_disjoint(const kda::Planes& p, int64_t n_slots, std::initializer_lis
 extern "C" {
 
 size_t kda_conv_bwd_workspace_size(int32_t n_seqs, int64_t total_tokens, int32_t C, int32_t W) {
-    if (n_seqs < 1 || total_tokens < 0 || C < 1 || W < 2 || W > 4) return 0;
+    if (n_seqs < 1 || total_tokens < 0 || total_tokens > kMaxTokens || C < 1 || C > kMaxRow / 2 || W < 2 || W > 4) return 0;
     return kda::conv_workspace_bytes(n_seqs, total_tokens, C, W);
 }
 

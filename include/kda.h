@@ -396,8 +396,8 @@ int kda_state_load(const void *codes, int code, const float *scales, const int32
  *     may be up to 2^24 bytes (KDA_ERR_UNSUPPORTED past it).  States and windows are contiguous.
  *   - Outputs must not overlap inputs or one another (rows of one stride side by side do not).
  *   - The stream must belong to the current device.
- *   - The workspace sizes never fall as sequences, tokens or slots grow: with the same heads, channels and types, a
- *     workspace for the largest call serves every smaller one.
+ *   - The workspace sizes never fail, are 0 for arguments out of range, and never fall as sequences, tokens or slots
+ *     grow within it: with the same heads, channels and types, a workspace for the largest call serves every smaller one.
  *   - Pools: where a call takes `slots` (device int32 [N]), sequence n works on slot slots[n] of an array of
  *     n_slots, or on slot n with slots NULL (then N <= n_slots is required).  A sequence whose slot lies outside
  *     [0, n_slots) -- a padded row of a batch -- is skipped and gets zeros for its output; of several with one slot

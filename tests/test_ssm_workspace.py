@@ -53,6 +53,13 @@ def test_costs_little():
     assert K.kda_ssm_chunk_workspace_size(4, 4 * 4096, 32, 1, 128, 64, bf, True) < 1.25 * states
 
 
+def test_out_of_range():
+    """Sizes beyond what the convolution's gradients take: 0, not what is left of a product past 64 bits."""
+    for T, C in ((1 << 31, 64), (1 << 62, 64), (1, (1 << 23) + 1), (1 << 30, (1 << 31) - 1)):
+        assert K.kda_conv_bwd_workspace_size(1, T, C, 4) == 0, (T, C)
+    assert K.kda_conv_bwd_workspace_size(1, (1 << 31) - 1, 1 << 23, 4) > 1 << 40
+
+
 def test_other_calls_never_fall():
     """The convolution's gradients and the slot pools: the same holds."""
     r = random.Random(2)
